@@ -1,0 +1,474 @@
+// qt2_train.cu -- the training operators' library: kernel launchers and the C ABI declared in
+// include/qt2_train.h (layer norm, the head's softmax cross entropy, gradient norm and clipping).
+//
+// One translation unit, with a device status word, fault hook and caches of its own.  Built for
+// sm_100a only into libqt2_train.so.
+#include <cmath>
+
+#include "qt2_internal.h"
+#include "qt2_train.h"
+#include "qt2_host.cuh"
+#include "qt2_device.cuh"
+#include "norm_kernels.cuh"
+#include "grad_kernels.cuh"
+#include "xent_kernels.cuh"
+
+using namespace qt2;
+
+namespace {
+
+cudaStream_t as_stream(qt2_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+bool dim_ok(int64_t d) { return d > 0 && d < (int64_t(1) << 30); }
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool dtype_ok(int d) { return d == QT2_DTYPE_BF16 || d == QT2_DTYPE_F32; }
+bool ld_shape_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (int64_t(1) << 40); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+qt2_status check_workspace(const void *ws, size_t have, size_t need) {
+    if (!ws || have < need) return QT2_ERR_WORKSPACE;
+    return aligned(ws, kWsAlign) ? QT2_OK : QT2_ERR_ALIGN;
+}
+
+// ------------------------------------------------------------------------------- layer norm
+int norm_splits(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(64, rows / 16)); }
+
+template <class T, class W>
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    layernorm_fwd_kernel<T, W><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T, class W>
+cudaError_t launch_norm_dx(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    layernorm_dx_kernel<T, W><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T>
+cudaError_t launch_norm_dw_part(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads), (unsigned)a.splits);
+    layernorm_dw_part_kernel<T><<<grid, kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class W>
+cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    layernorm_dw_kernel<W><<<(unsigned)ceil_div(a.cols, kNormThreads), kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------- head loss
+// The plan depends on the sizes alone, so that the workspace queries need no device: 74 pairs.
+constexpr int kPairs = 74;
+constexpr int64_t kPieceBytes = 256 << 20;   // of P
+
+struct XentPlan {
+    int64_t num_m, num_v, num_k;   // 256-wide tiles of T, V and K
+    int64_t piece;                 // vocabulary entries of a piece, a multiple of 256
+    int pieces, splits;
+};
+
+XentPlan xent_plan(int64_t T, int64_t K, int64_t V) {
+    XentPlan p;
+    p.num_m = ceil_div(T, 256);
+    p.num_v = ceil_div(V, 256);
+    p.num_k = ceil_div(K, 256);
+    const int64_t most = std::max<int64_t>(1, kPieceBytes / (512 * T));
+    p.pieces = (int)ceil_div(p.num_v, most);
+    p.piece = ceil_div(p.num_v, p.pieces) * 256;
+    p.pieces = (int)ceil_div(p.num_v * 256, p.piece);
+    // dx's jobs are cut along the vocabulary where whole they would outlast an even share of the
+    // launch's stages by much
+    const int64_t nks = p.piece / 64, dx = p.num_m * p.num_k;
+    const int64_t total = dx * nks + p.piece / 256 * p.num_k * ceil_div(T, 64);
+    const int64_t share = std::max<int64_t>(16, total / (2 * kPairs));
+    p.splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, nks / share));
+    return p;
+}
+
+struct XentFwdWs {
+    float2 *part;
+    float *hit;
+    size_t bytes;
+};
+XentFwdWs xent_fwd_ws(const XentPlan &p, int64_t T, void *ws) {
+    Carve c(ws);
+    XentFwdWs w;
+    w.part = reinterpret_cast<float2 *>(c.take((size_t)(2 * p.num_v * T) * sizeof(float2)));
+    w.hit = reinterpret_cast<float *>(c.take((size_t)T * sizeof(float)));
+    w.bytes = c.used;
+    return w;
+}
+struct XentBwdWs {
+    __nv_bfloat16 *P;
+    float *acc;
+    size_t bytes;
+};
+XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, void *ws) {
+    Carve c(ws);
+    XentBwdWs w;
+    w.P = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * p.piece * 2));
+    w.acc = reinterpret_cast<float *>(c.take((size_t)p.splits * p.num_m * p.num_k * 65536 * sizeof(float)));
+    w.bytes = c.used;
+    return w;
+}
+
+bool encode_bf16(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+    return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, 64,
+                          (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int MODE>
+cudaError_t launch_mm(const MmMaps &maps, const MmArgs &a, int64_t jobs, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(mm_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    MmCfg::kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(jobs, sm_count() / 2));
+    mm_pair_kernel<MODE><<<(unsigned)(2 * clusters), MmCfg::kThreads, MmCfg::kSmemBytes, s>>>(maps, a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_xent_loss(const MmArgs &a, int parts, float *loss, float *lse, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    xent_loss_kernel<<<(unsigned)ceil_div(a.T, 32), 256, 0, s>>>(a, parts, loss, lse);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    const int64_t n = (int64_t)a.T * ceil_div(a.K, 8);
+    const int64_t blocks = std::min<int64_t>(ceil_div(n, 256), (int64_t)sm_count() * 16);
+    xent_dx_kernel<<<(unsigned)blocks, 256, 0, s>>>(a.acc, a.T, a.K, a.splits, (int64_t)a.dx_m * 256,
+                                                    (int64_t)a.dx_n * 256, static_cast<__nv_bfloat16 *>(dx), lddx);
+    return cudaGetLastError();
+}
+
+qt2_status xent_check(const void *x, const void *w, const int64_t *targets, int64_t T, int64_t K, int64_t V,
+                      int64_t ldx, int64_t ldw) {
+    if (!x || !w || !targets) return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V) || !ld_shape_ok(ldx, K) || !ld_shape_ok(ldw, K)) return QT2_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(targets, 8) || ldx % 8 || ldw % 8) return QT2_ERR_ALIGN;
+    return QT2_OK;
+}
+
+// ------------------------------------------------------------------------------- gradients
+qt2_status grad_check(const qt2_grad *g, int64_t count, bool with_out) {
+    if (!g) return QT2_ERR_INVALID_ARG;
+    if (count <= 0 || count > (int64_t(1) << 30)) return QT2_ERR_SHAPE;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!dtype_ok(g[i].dtype)) return QT2_ERR_INVALID_ARG;
+        if (g[i].numel < 0 || g[i].numel >= (int64_t(1) << 44)) return QT2_ERR_SHAPE;
+        if (g[i].numel == 0) continue;
+        if (!g[i].grad || (with_out && !g[i].out)) return QT2_ERR_INVALID_ARG;
+        const uintptr_t e = g[i].dtype == QT2_DTYPE_F32 ? 4 : 2;
+        if (!aligned(g[i].grad, e) || (with_out && !aligned(g[i].out, e))) return QT2_ERR_ALIGN;
+    }
+    return QT2_OK;
+}
+
+// The next launch's tensors: fills t from g[at...], skipping empty ones; returns the next `at`.
+int64_t grad_table(GradTable &t, const qt2_grad *g, int64_t at, int64_t count) {
+    t.count = 0;
+    std::memset(t.f32, 0, sizeof t.f32);
+    t.first[0] = 0;
+    for (; at < count && t.count < kGradTable; ++at) {
+        if (g[at].numel == 0) continue;
+        const int k = t.count++;
+        t.grad[k] = g[at].grad;
+        t.out[k] = g[at].out;
+        t.numel[k] = g[at].numel;
+        t.first[k + 1] = t.first[k] + ceil_div(g[at].numel, kGradChunk);
+        if (g[at].dtype == QT2_DTYPE_F32) t.f32[k >> 5] |= 1u << (k & 31);
+    }
+    return at;
+}
+constexpr int kGradBlocks = 148 * 8;
+
+cudaError_t launch_grad_norm(const GradTable &t, double *part, int blocks, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    grad_norm_kernel<<<blocks, kGradThreads, 0, s>>>(t, part);
+    return cudaGetLastError();
+}
+cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    grad_norm_end_kernel<<<1, kGradThreads, 0, s>>>(part, n, norm);
+    return cudaGetLastError();
+}
+cudaError_t launch_grad_clip(const GradTable &t, const float *norm, float max_norm, int blocks, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    grad_clip_kernel<<<blocks, kGradThreads, 0, s>>>(t, norm, max_norm);
+    return cudaGetLastError();
+}
+int grad_blocks(const GradTable &t) { return (int)std::min<int64_t>(t.first[t.count], kGradBlocks); }
+
+// f(T{}, W{}) with the element types of x_dtype and w_dtype.
+template <class F>
+cudaError_t with_types(int x_dtype, int w_dtype, F &&f) {
+    if (x_dtype == QT2_DTYPE_F32) return w_dtype == QT2_DTYPE_F32 ? f(float{}, float{}) : f(float{}, __nv_bfloat16{});
+    return w_dtype == QT2_DTYPE_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+
+}  // namespace
+
+extern "C" {
+
+qt2_status qt2_train_device_status(qt2_stream_t stream, int *code) {
+    QT2_TRACE();
+    if (!code) return QT2_ERR_INVALID_ARG;
+    if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return QT2_ERR_CUDA;
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess) return QT2_ERR_CUDA;
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return QT2_ERR_CUDA;
+    *code = v;
+    return QT2_OK;
+}
+
+void qt2_train_set_fault_hook(qt2_fault_hook hook, void *user) {
+    g_fault_user.store(user, std::memory_order_release);
+    g_fault_hook.store(hook, std::memory_order_release);
+}
+
+int qt2_train_build_checked(void) {
+#ifdef QT2_CHECKED
+    return 1;
+#else
+    return 0;
+#endif
+}
+
+qt2_status qt2_layernorm_fwd(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
+                             const void *bias, int w_dtype, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                             qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!x || !y || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !(eps >= 0.0f) || std::isinf(eps))
+        return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || !dim_ok(cols) || !ld_shape_ok(ldx, cols) || !ld_shape_ok(ldy, cols)) return QT2_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(y, 16) || ldx % 8 || ldy % 8 || !aligned(weight, 16) || !aligned(bias, 16) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
+        return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    NormArgs a{};
+    a.x = x;
+    a.w = weight;
+    a.b = bias;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.eps = eps;
+    return from_cuda(with_types(x_dtype, w_dtype, [&](auto t, auto w) {
+        return launch_norm_fwd<decltype(t), decltype(w)>(a, as_stream(stream));
+    }));
+}
+
+qt2_status qt2_layernorm_bwd_workspace_size(int64_t rows, int64_t cols, size_t *bytes) {
+    if (!bytes) return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || !dim_ok(cols)) return QT2_ERR_SHAPE;
+    *bytes = align_up((size_t)norm_splits(rows) * 2 * cols * sizeof(float), kWsAlign);
+    return QT2_OK;
+}
+
+qt2_status qt2_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int x_dtype, int64_t rows, int64_t cols,
+                             int64_t ldx, const void *weight, int w_dtype, const float *mean, const float *rstd,
+                             void *dx, int64_t lddx, void *dweight, void *dbias, void *workspace, size_t ws_bytes,
+                             qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!dy || !x || !mean || !rstd || (!dx && !dweight && !dbias) || !dtype_ok(x_dtype) || !dtype_ok(w_dtype))
+        return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || !dim_ok(cols) || !ld_shape_ok(ldx, cols) || !ld_shape_ok(lddy, cols) ||
+        (dx && !ld_shape_ok(lddx, cols)))
+        return QT2_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(dy, 16) || ldx % 8 || lddy % 8 || (dx && (!aligned(dx, 16) || lddx % 8)) ||
+        !aligned(weight, 16) || !aligned(dweight, 16) || !aligned(dbias, 16) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return QT2_ERR_ALIGN;
+    size_t need = 0;
+    if (const qt2_status st = qt2_layernorm_bwd_workspace_size(rows, cols, &need)) return st;
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    if (const qt2_status st = check_device()) return st;
+    NormArgs a{};
+    a.x = x;
+    a.dy = dy;
+    a.w = weight;
+    a.y = dx;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.ldx = ldx;
+    a.lddy = lddy;
+    a.ldy = lddx;
+    a.part = static_cast<float *>(workspace);
+    a.splits = norm_splits(rows);
+    a.dw = dweight;
+    a.db = dbias;
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(with_types(x_dtype, w_dtype, [&](auto t, auto w) {
+        using T = decltype(t);
+        using W = decltype(w);
+        cudaError_t e = cudaSuccess;
+        if (dweight || dbias) {   // before dx, which may be dy
+            e = launch_norm_dw_part<T>(a, s);
+            if (e == cudaSuccess) e = launch_norm_dw<W>(a, s);
+        }
+        if (e == cudaSuccess && dx) e = launch_norm_dx<T, W>(a, s);
+        return e;
+    }));
+}
+
+qt2_status qt2_linear_xent_fwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
+    if (!bytes) return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V)) return QT2_ERR_SHAPE;
+    *bytes = xent_fwd_ws(xent_plan(T, K, V), T, nullptr).bytes;
+    return QT2_OK;
+}
+
+qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targets, int64_t T, int64_t K, int64_t V,
+                               int64_t ldx, int64_t ldw, int64_t ignore_index, float *loss, float *lse,
+                               void *workspace, size_t ws_bytes, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!loss || !lse) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = xent_check(x, w, targets, T, K, V, ldx, ldw)) return st;
+    if (!aligned(loss, 4) || !aligned(lse, 4)) return QT2_ERR_ALIGN;
+    const XentPlan p = xent_plan(T, K, V);
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, xent_fwd_ws(p, T, nullptr).bytes)) return st;
+    if (const qt2_status st = check_device()) return st;
+    const XentFwdWs ws = xent_fwd_ws(p, T, workspace);
+    MmMaps maps{};
+    if (!encode_bf16(&maps.x_k, x, K, T, ldx, 128) || !encode_bf16(&maps.w_k, w, K, V, ldw, 128)) return QT2_ERR_CUDA;
+    MmArgs a{};
+    a.T = (int)T;
+    a.K = (int)K;
+    a.V = (int)V;
+    a.vw = (int)(p.num_v * 256);
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.part = ws.part;
+    a.hit = ws.hit;
+    a.num_m = (int)p.num_m;
+    a.num_n = (int)p.num_v;
+    const cudaStream_t s = as_stream(stream);
+    cudaError_t e = launch_mm<kLoss>(maps, a, p.num_m * p.num_v, s);
+    if (e == cudaSuccess) e = launch_xent_loss(a, 2 * a.num_n, loss, lse, s);
+    return from_cuda(e);
+}
+
+qt2_status qt2_linear_xent_bwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
+    if (!bytes) return QT2_ERR_INVALID_ARG;
+    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V)) return QT2_ERR_SHAPE;
+    *bytes = xent_bwd_ws(xent_plan(T, K, V), T, nullptr).bytes;
+    return QT2_OK;
+}
+
+qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targets, const float *lse,
+                               const float *dloss, int64_t T, int64_t K, int64_t V, int64_t ldx, int64_t ldw,
+                               int64_t ignore_index, void *dx, int64_t lddx, void *dw, int dw_dtype, int64_t lddw,
+                               void *workspace, size_t ws_bytes, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!lse || !dloss || (!dx && !dw) || (dw && !dtype_ok(dw_dtype))) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = xent_check(x, w, targets, T, K, V, ldx, ldw)) return st;
+    if ((dx && !ld_shape_ok(lddx, K)) || (dw && !ld_shape_ok(lddw, K))) return QT2_ERR_SHAPE;
+    if (!aligned(lse, 4) || !aligned(dloss, 4) || (dx && (!aligned(dx, 16) || lddx % 8)) ||
+        (dw && (!aligned(dw, 16) || lddw % 8)))
+        return QT2_ERR_ALIGN;
+    const XentPlan p = xent_plan(T, K, V);
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, xent_bwd_ws(p, T, nullptr).bytes)) return st;
+    if (const qt2_status st = check_device()) return st;
+    const XentBwdWs ws = xent_bwd_ws(p, T, workspace);
+    MmMaps maps{};
+    if (!encode_bf16(&maps.x_k, x, K, T, ldx, 128) || !encode_bf16(&maps.w_k, w, K, V, ldw, 128) ||
+        !encode_bf16(&maps.x_mn, x, K, T, ldx, 64) || !encode_bf16(&maps.w_mn, w, K, V, ldw, 64))
+        return QT2_ERR_CUDA;
+    MmArgs a{};
+    a.T = (int)T;
+    a.K = (int)K;
+    a.V = (int)V;
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.P = ws.P;
+    a.num_m = (int)p.num_m;
+    a.splits = p.splits;
+    a.dx_m = (int)p.num_m;
+    a.dx_n = (int)p.num_k;
+    a.acc = ws.acc;
+    a.dw = dw;
+    a.lddw = lddw;
+    a.dw_f32 = dw_dtype == QT2_DTYPE_F32;
+    const cudaStream_t s = as_stream(stream);
+    for (int i = 0; i < p.pieces; ++i) {
+        a.v0 = (int)(i * p.piece);
+        a.vw = (int)std::min<int64_t>(p.piece, p.num_v * 256 - a.v0);
+        a.num_n = a.vw / 256;
+        a.add = i > 0;
+        a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
+        a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
+        a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;
+        if (!encode_bf16(&maps.p_k, ws.P, a.vw, T, a.vw, 128) || !encode_bf16(&maps.p_mn, ws.P, a.vw, T, a.vw, 64))
+            return QT2_ERR_CUDA;
+        cudaError_t e = launch_mm<kProbs>(maps, a, (int64_t)a.num_m * a.num_n, s);
+        if (e == cudaSuccess) e = launch_mm<kGrads>(maps, a, (int64_t)a.dx_jobs + a.dw_jobs, s);
+        if (e != cudaSuccess) return QT2_ERR_CUDA;
+    }
+    if (!dx) return QT2_OK;
+    a.splits = p.splits;
+    return from_cuda(launch_xent_dx(a, dx, lddx, s));
+}
+
+qt2_status qt2_grad_norm_workspace_size(const qt2_grad *grads, int64_t count, size_t *bytes) {
+    if (!bytes) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = grad_check(grads, count, false)) return st;
+    *bytes = (size_t)ceil_div(count, kGradTable) * kGradBlocks * sizeof(double);
+    return QT2_OK;
+}
+
+qt2_status qt2_grad_norm(const qt2_grad *grads, int64_t count, float *norm, void *workspace, size_t ws_bytes,
+                         qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!norm) return QT2_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (const qt2_status st = qt2_grad_norm_workspace_size(grads, count, &need)) return st;
+    if (!aligned(norm, 4)) return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    if (const qt2_status st = check_device()) return st;
+    double *part = static_cast<double *>(workspace);
+    const cudaStream_t s = as_stream(stream);
+    int n = 0;
+    GradTable t;
+    for (int64_t at = 0; at < count;) {
+        at = grad_table(t, grads, at, count);
+        if (t.count == 0) break;
+        const int blocks = grad_blocks(t);
+        if (launch_grad_norm(t, part + n, blocks, s) != cudaSuccess) return QT2_ERR_CUDA;
+        n += blocks;
+    }
+    return from_cuda(launch_grad_norm_end(part, n, norm, s));
+}
+
+qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm, float max_norm,
+                         qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!norm || !(max_norm >= 0.0f)) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = grad_check(grads, count, true)) return st;
+    if (!aligned(norm, 4)) return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    GradTable t;
+    for (int64_t at = 0; at < count;) {
+        at = grad_table(t, grads, at, count);
+        if (t.count == 0) break;
+        if (launch_grad_clip(t, norm, max_norm, grad_blocks(t), as_stream(stream)) != cudaSuccess) return QT2_ERR_CUDA;
+    }
+    return QT2_OK;
+}
+
+}  // extern "C"

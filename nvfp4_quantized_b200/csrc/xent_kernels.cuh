@@ -1,0 +1,479 @@
+// xent_kernels.cuh -- the head's softmax cross entropy without its logits.
+//
+//   l = x w^T, lse_t = log sum_v exp l_tv, loss_t = lse_t - l_t,y(t)          (forward)
+//   P_tv = dloss_t (exp(l_tv - lse_t) - [v = y(t)]), dx = P w, dw = P^T x     (backward)
+//
+// All three products are bf16 with fp32 sums on the tensor cores, in one persistent kernel shape
+// (mm_pair_kernel): a pair of SMs forms 256x256 tiles with tcgen05.mma.cta_group::2, each SM
+// holding its 128 rows of A and half of B, so that a stage of K = 64 moves 64 KB for 8.4 MFLOP.
+// What differs is where the operands come from and what the epilogue does with a tile:
+//   kLoss   A = x, B = w rows; the tile of logits becomes one (max, sum of exp) pair a row and
+//           128 columns, and the target's logit where the tile holds it.
+//   kProbs  the same tile becomes the bf16 entries of P for one piece of the vocabulary.
+//   kGrads  jobs of both gradient products in one launch: dx (A = P, B = w with the vocabulary
+//           contracted, so w is read transposed: an MN-major operand) added up over the pieces in
+//           fp32, and dw (A = P transposed, B = x transposed), whose rows are complete after their
+//           piece.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "qt2_device.cuh"
+#include "qt2_pair.cuh"
+
+namespace qt2 {
+
+// D[tmem] (+)= A[smem] x B[smem], bf16, one pair of SMs (K = 16 per instruction).
+__device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct MmCfg {
+    static constexpr int kStages = 6;
+    static constexpr int kThreads = 384;
+    static constexpr int kEpiWarp0 = 4;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kA = 128 * 64 * 2;   // own 128 rows of A, K = 64
+    static constexpr int kB = 128 * 64 * 2;   // own half of the 256 rows of B
+    static constexpr int kStageBytes = kA + kB;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 512;
+    static constexpr int kTmemCols = 512;     // two 256-column accumulators
+    // fp32 sums, bf16 A and B, M = 256 (pair), N = 256; bits 15 / 16: A / B is MN-major
+    static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (16u << 24);
+    static constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
+};
+
+enum MmMode { kLoss = 0, kProbs = 1, kGrads = 2 };
+
+// Tensor maps: k = K-major reads (box 64 x 128 rows), mn = MN-major reads (box 64 x 64).
+struct MmMaps {
+    CUtensorMap x_k, w_k, p_k, x_mn, w_mn, p_mn;
+};
+
+struct MmArgs {
+    int T, K, V;
+    int v0, vw;            // the piece: its first vocabulary entry and its width (a multiple of 256)
+    const int64_t *targets;
+    int64_t ignore;
+    const float *lse, *dloss;   // kProbs
+    float2 *part;          // kLoss: [2 * tiles of the vocabulary][T]
+    float *hit;            // kLoss: the target's logit
+    __nv_bfloat16 *P;      // [T][vw]
+    int num_m, num_n;      // kLoss, kProbs: tiles
+    int dx_jobs, splits, dx_m, dx_n;   // kGrads: dx's jobs come first: (split, row tile, column tile)
+    int dw_jobs, add;      // add: dx's sums hold earlier pieces
+    float *acc;            // [splits][256 dx_m][256 dx_n]
+    void *dw;
+    int64_t lddw;
+    int dw_f32;
+};
+
+// One job: its tile, and the stages [ks, ks + nk) of its contraction.
+struct MmJob {
+    int m, n, ks, nk, split;
+    bool dw;
+};
+
+template <int MODE>
+__device__ __forceinline__ MmJob mm_job(const MmArgs &a, int j) {
+    MmJob b;
+    b.split = 0;
+    b.dw = false;
+    b.ks = 0;
+    if (MODE != kGrads) {
+        // along the tokens first: the tiles in flight then share all of x and few rows of w
+        b.n = j / a.num_m;
+        b.m = j - b.n * a.num_m;
+        b.nk = (a.K + 63) >> 6;
+        return b;
+    }
+    if (j < a.dx_jobs) {
+        const int nks = a.vw >> 6, tiles = a.dx_m * a.dx_n;
+        b.split = j / tiles;
+        j -= b.split * tiles;
+        b.m = j / a.dx_n;
+        b.n = j - b.m * a.dx_n;
+        const int lo = (int)((int64_t)nks * b.split / a.splits), hi = (int)((int64_t)nks * (b.split + 1) / a.splits);
+        b.ks = lo;
+        b.nk = hi - lo;
+        return b;
+    }
+    j -= a.dx_jobs;
+    const int nn = (a.K + 255) >> 8;
+    b.dw = true;
+    b.m = j / nn;
+    b.n = j - b.m * nn;
+    b.nk = (a.T + 63) >> 6;
+    return b;
+}
+
+// The row's target within the vocabulary, or -1.
+__device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
+    const int64_t y = a.targets[t];
+    return (y == a.ignore || y < 0 || y >= a.V) ? -1 : (int)y;
+}
+
+// What becomes of a tile: the thread holds columns [col, col + 128) of the tile's row `row`.
+template <int MODE>
+__device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col) {
+    if (MODE == kLoss) {
+        if (row >= a.T) return;
+        const int valid = a.V - col;   // columns of the vocabulary from here on
+        if (valid < 128) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                if (i >= valid) v[i] = 0xFF800000u;   // -inf
+        }
+        float m = __uint_as_float(v[0]);
+#pragma unroll
+        for (int i = 1; i < 128; ++i) m = fmaxf(m, __uint_as_float(v[i]));
+        const float sub = (m == -INFINITY ? 0.0f : m) * kLog2e;
+        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 128; i += 4) {
+            s0 += ex2(fmaf(__uint_as_float(v[i]), kLog2e, -sub));
+            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), kLog2e, -sub));
+            s2 += ex2(fmaf(__uint_as_float(v[i + 2]), kLog2e, -sub));
+            s3 += ex2(fmaf(__uint_as_float(v[i + 3]), kLog2e, -sub));
+        }
+        a.part[(int64_t)(col >> 7) * a.T + row] = make_float2(m, (s0 + s1) + (s2 + s3));
+        const int y = xent_target(a, row) - col;
+        if (y >= 0 && y < 128) {
+            float h = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                if (i == y) h = __uint_as_float(v[i]);
+            a.hit[row] = h;
+        }
+    } else if (MODE == kProbs) {
+        if (row >= a.T) return;
+        const int y = xent_target(a, row);
+        const float g = y < 0 ? 0.0f : a.dloss[row], sub = a.lse[row] * kLog2e;
+        const int at = y - (a.v0 + col), valid = a.V - (a.v0 + col);
+        __nv_bfloat16 *dst = a.P + (int64_t)row * a.vw + col;
+        if (!QT2_STORE_OK(dst, 256, a.P, (int64_t)a.T * a.vw * 2)) return;
+#pragma unroll
+        for (int i = 0; i < 128; i += 16) {
+            uint32_t p[8];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                float e[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int c = i + k + q;
+                    e[q] = ex2(fmaf(__uint_as_float(v[c]), kLog2e, -sub)) - (c == at ? 1.0f : 0.0f);
+                    e[q] = (y < 0 || c >= valid) ? 0.0f : e[q] * g;
+                }
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
+                p[k >> 1] = *reinterpret_cast<uint32_t *>(&b2);
+            }
+            st_global_v8(dst + i, p);
+        }
+    } else if (!b.dw) {
+        const int64_t ld = (int64_t)a.dx_n * 256;
+        float *dst = a.acc + ((int64_t)b.split * a.dx_m * 256 + row) * ld + col;
+        if (!QT2_STORE_OK(dst, 512, a.acc, (int64_t)a.splits * a.dx_m * 256 * ld * 4)) return;
+#pragma unroll
+        for (int i = 0; i < 128; i += 8) {
+            uint32_t p[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[k] = v[i + k];
+            if (a.add) {
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) {
+                    const float4 o = *reinterpret_cast<const float4 *>(dst + i + k);
+                    p[k] = __float_as_uint(__uint_as_float(p[k]) + o.x);
+                    p[k + 1] = __float_as_uint(__uint_as_float(p[k + 1]) + o.y);
+                    p[k + 2] = __float_as_uint(__uint_as_float(p[k + 2]) + o.z);
+                    p[k + 3] = __float_as_uint(__uint_as_float(p[k + 3]) + o.w);
+                }
+            }
+            st_global_v8(dst + i, p);
+        }
+    } else {
+        const int64_t r = (int64_t)a.v0 + row;
+        const int n = min(128, a.K - col);   // columns of dw from here on
+        if (row >= a.vw || r >= a.V || n <= 0) return;
+        const int64_t extent = (int64_t)(a.V - 1) * a.lddw + a.K;
+        if (a.dw_f32) {
+            float *dst = static_cast<float *>(a.dw) + r * a.lddw + col;
+            if (!QT2_STORE_OK(dst, n * 4, a.dw, extent * 4)) return;
+#pragma unroll
+            for (int i = 0; i < 128; i += 4) {
+                if (i + 4 <= n) {
+                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (i + k < n) dst[i + k] = __uint_as_float(v[i + k]);
+                }
+            }
+        } else {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dw) + r * a.lddw + col;
+            if (!QT2_STORE_OK(dst, n * 2, a.dw, extent * 2)) return;
+#pragma unroll
+            for (int i = 0; i < 128; i += 8) {
+                if (i + 8 <= n) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]),
+                                                                  __uint_as_float(v[i + 2 * k + 1]));
+                        p[k] = *reinterpret_cast<uint32_t *>(&b2);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(p[0], p[1], p[2], p[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (i + k < n) dst[i + k] = __float2bfloat16_rn(__uint_as_float(v[i + k]));
+                }
+            }
+        }
+    }
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
+    mm_pair_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
+    using Cfg = MmCfg;
+    constexpr int S = Cfg::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_dyn[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    // barriers: full[S] empty[S] acc_full[2] acc_empty[2]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + S * Cfg::kStageBytes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
+
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
+    const int jobs = MODE == kGrads ? a.dx_jobs + a.dw_jobs : a.num_m * a.num_n;
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
+    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = acc_full0 + 16;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);    // the leader's producer (expects both SMs' bytes)
+            mbar_init(empty0 + 8 * s, 1);   // the MMA issuer's commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full0 + 8 * b, 1);
+            mbar_init(acc_empty0 + 8 * b, 2 * Cfg::kEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();   // both CTAs' barriers initialised and TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    int issued = 0;     // producer: stages whose loads were issued
+    int mma_done = 0;   // MMA warp: stages whose MMAs were issued
+    if (warp == 0) {
+        // -------------------------------------------------------------- producer (both CTAs)
+        const uint32_t full_leader0 = mapa_shared(full0, 0);
+        bool ok = true;
+        for (int j = cluster_id; j < jobs && ok; j += num_clusters) {
+            const MmJob b = mm_job<MODE>(a, j);
+            const int am = b.m * 256 + (int)rank * 128, bn = b.n * 256 + (int)rank * 128;
+            for (int ks = b.ks; ks < b.ks + b.nk; ++ks) {
+                const int it = issued, s = it % S;
+                if (it >= S && !mbar_wait_warp(empty0 + 8 * s, ((it / S) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = smem_u32(base + s * Cfg::kStageBytes);
+                const uint32_t fb = full_leader0 + 8 * s;
+                const int k = ks * 64;
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * Cfg::kStageBytes);
+                    if (MODE != kGrads) {
+                        tma_load_2d_pair(st, &maps.x_k, k, am, fb);
+                        tma_load_2d_pair(st + Cfg::kA, &maps.w_k, k, a.v0 + bn, fb);
+                    } else if (!b.dw) {
+                        tma_load_2d_pair(st, &maps.p_k, k, am, fb);
+                        tma_load_2d_pair(st + Cfg::kA, &maps.w_mn, bn, a.v0 + k, fb);
+                        tma_load_2d_pair(st + Cfg::kA + 8192, &maps.w_mn, bn + 64, a.v0 + k, fb);
+                    } else {
+                        tma_load_2d_pair(st, &maps.p_mn, am, k, fb);
+                        tma_load_2d_pair(st + 8192, &maps.p_mn, am + 64, k, fb);
+                        tma_load_2d_pair(st + Cfg::kA, &maps.x_mn, bn, k, fb);
+                        tma_load_2d_pair(st + Cfg::kA + 8192, &maps.x_mn, bn + 64, k, fb);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+            }
+        }
+    } else if (warp == 1 && leader) {
+        // -------------------------------------------------------------- MMA issuer (leader)
+        // Operand tiles in shared memory, 128-byte swizzle.  K-major: 128-byte rows of 64 k, 8-row
+        // groups 1 KB apart, a K = 16 step 32 bytes on.  MN-major: 64 (m or n) a 128-byte line,
+        // one line a k, 8-k groups 1 KB apart, the next 64 (m or n) 8 KB on, a K = 16 step 2 KB on.
+        bool ok = true;
+        int t_iter = 0;
+        for (int j = cluster_id; j < jobs && ok; j += num_clusters, ++t_iter) {
+            const MmJob b = mm_job<MODE>(a, j);
+            const int buf = t_iter & 1;
+            if (t_iter >= 2 && !mbar_wait_warp(acc_empty0 + 8 * buf, ((t_iter >> 1) & 1) ^ 1)) break;
+            tc_fence_after();
+            const bool mn_a = MODE == kGrads && b.dw, mn_b = MODE == kGrads;
+            const uint32_t idesc = Cfg::kIdesc | (mn_a ? Cfg::kIdescMnA : 0) | (mn_b ? Cfg::kIdescMnB : 0);
+            const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
+            const uint32_t lbo_a = mn_a ? 8192 : 16, lbo_b = mn_b ? 8192 : 16;
+            for (int ks = 0; ks < b.nk; ++ks) {
+                const int it = mma_done, s = it % S;
+                if (!mbar_wait_warp(full0 + 8 * s, (it / S) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(base + s * Cfg::kStageBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_pair_f16(tmem + 256 * buf, make_smem_desc(st + step_a * kk, lbo_a, 1024, 2),
+                                        make_smem_desc(st + Cfg::kA + step_b * kk, lbo_b, 1024, 2), idesc,
+                                        (ks | kk) != 0);
+                    tc_commit_pair_both(empty0 + 8 * s);
+                }
+                __syncwarp();
+                mma_done = it + 1;
+            }
+            if (ok) {
+                if (elect_one()) tc_commit_pair_both(acc_full0 + 8 * buf);
+                __syncwarp();
+            }
+        }
+    } else if (warp >= Cfg::kEpiWarp0) {
+        // -------------------------------------------------------------- epilogue (both CTAs)
+        // Warp w reads TMEM lane quadrant w % 4, columns [0, 128) for warps 4..7 and [128, 256)
+        // for warps 8..11; a thread holds 128 columns of one row.
+        const int quad = warp & 3, ew = warp - Cfg::kEpiWarp0;
+        const int cb = (ew >> 2) * 128;
+        const uint32_t acc_empty_leader0 = mapa_shared(acc_empty0, 0);
+        int t_iter = 0;
+        for (int j = cluster_id; j < jobs; j += num_clusters, ++t_iter) {
+            const MmJob b = mm_job<MODE>(a, j);
+            const int buf = t_iter & 1;
+            if (!mbar_wait_warp(acc_full0 + 8 * buf, (t_iter >> 1) & 1)) break;
+            tc_fence_after();
+            const int row = b.m * 256 + (int)rank * 128 + quad * 32 + lane;
+            const int col = b.n * 256 + cb;
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + 256 * buf + cb;
+            uint32_t v[128];
+#pragma unroll
+            for (int c = 0; c < 128; c += 16)
+                tmem_ld_32x32b_x16(taddr + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
+            mm_epilogue<MODE>(a, b, v, row, col);
+            __syncwarp();
+        }
+    }
+    // Every role ends converged.  Only after a timeout can work still be in flight: the leader
+    // waits (bounded) for the loads it issued past the last consumed stage and for the last
+    // issued MMAs, then both CTAs meet before TMEM is freed.
+    __shared__ int consumed, issued_here;
+    if (warp == 1 && leader && lane == 0) consumed = mma_done;
+    if (warp == 0 && lane == 0) issued_here = issued;
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (leader && warp == 0 && lane == 0) {
+        // both SMs' loads of a stage complete on the leader's barrier
+        const int peer = (int)ld_shared_cluster_u32(mapa_shared(smem_u32(&issued_here), 1));
+        const int last = max(issued, peer);
+        for (int it = consumed; it < last; ++it) mbar_wait(full0 + 8 * (it % S), (it / S) & 1);
+    }
+    if (leader && warp == 1 && lane == 0 && mma_done > 0) {
+        const int it = mma_done - 1;
+        mbar_wait(empty0 + 8 * (it % S), (it / S) & 1);
+    }
+    cluster_sync_all();   // no SM frees TMEM or exits while its pair may still touch it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, Cfg::kTmemCols);
+}
+
+// loss and lse from the tiles' (max, sum) pairs: lse = M + log sum_i s_i exp(m_i - M).  A block
+// takes 32 rows; its 8 warps share the pairs.
+__global__ void __launch_bounds__(256) xent_loss_kernel(const MmArgs a, int parts, float *loss, float *lse) {
+    const int t = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+    __shared__ float2 sh[8][32];
+    float m = -INFINITY, s = 0.0f;
+    if (t < a.T) {
+        for (int i = slice; i < parts; i += 8) {
+            const float2 p = a.part[(int64_t)i * a.T + t];
+            const float n = fmaxf(m, p.x), ref = n == -INFINITY ? 0.0f : n;
+            s = s * __expf(m - ref) + p.y * __expf(p.x - ref);
+            m = n;
+        }
+    }
+    sh[slice][threadIdx.x & 31] = make_float2(m, s);
+    __syncthreads();
+    if (slice != 0 || t >= a.T) return;
+    float top = m;
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, sh[i][threadIdx.x].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int i = 0; i < 8; ++i) sum += sh[i][threadIdx.x].y * __expf(sh[i][threadIdx.x].x - ref);
+    const float l = ref + logf(sum);
+    lse[t] = l;
+    const int64_t y = a.targets[t];
+    const int in = xent_target(a, t);
+    if (in < 0 && y != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
+    loss[t] = in < 0 ? 0.0f : l - a.hit[t];
+}
+
+// dx = the sum of the splits' fp32 sums, rounded to bf16.  One thread takes 8 columns of a row.
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, int T, int K, int splits, int64_t rows,
+                                                      int64_t ld, __nv_bfloat16 *dx, int64_t lddx) {
+    const int vecs = (K + 7) >> 3;
+    const int64_t n = (int64_t)T * vecs;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / vecs;
+        const int c = (int)(i - t * vecs) * 8;
+        float v[8] = {};
+        for (int s = 0; s < splits; ++s) {
+            const float4 *src = reinterpret_cast<const float4 *>(acc + (s * rows + t) * ld + c);
+            const float4 p = src[0], q = src[1];
+            v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+            v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
+        }
+        __nv_bfloat16 *dst = dx + t * lddx + c;
+        const int valid = min(8, K - c);
+        if (!QT2_STORE_OK(dst, valid * 2, dx, ((int64_t)(T - 1) * lddx + K) * 2)) continue;
+        if (valid == 8) {
+            uint32_t p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                p[k] = *reinterpret_cast<uint32_t *>(&b2);
+            }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+        } else {
+            for (int k = 0; k < valid; ++k) dst[k] = __float2bfloat16_rn(v[k]);
+        }
+    }
+}
+
+}  // namespace qt2
