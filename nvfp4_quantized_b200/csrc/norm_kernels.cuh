@@ -20,18 +20,167 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;   // of the kernels for rows too long for registers
 
-// Sum over the block, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float *sh) {
+// 16 bytes of a row: 8 bf16 or 4 fp32 elements.
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void unpack(const uint4 &r, float (&v)[8]) {
+    v[0] = bf16_lo(r.x); v[1] = bf16_hi(r.x); v[2] = bf16_lo(r.y); v[3] = bf16_hi(r.y);
+    v[4] = bf16_lo(r.z); v[5] = bf16_hi(r.z); v[6] = bf16_lo(r.w); v[7] = bf16_hi(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4 &r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+// Elements [c, c + E) of a weight vector of either type (`other` where there is none).  No 16 bytes
+// without an element of the vector are touched.
+template <int E>
+__device__ __forceinline__ void load_weight(const void *w, int f32, int c, int cols, float other, float (&v)[E]) {
+    if (!w) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += sh[i];
-    return v;
+        for (int e = 0; e < E; ++e) v[e] = other;
+    } else if (f32) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 q = c + e < cols ? __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + e))
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+        }
+    } else if constexpr (E == 8) {
+        unpack(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c)), v);
+    } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(w) + c));
+        v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+    }
+    if (c + E > cols) {   // what lies behind the vector may be NaN
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c + e >= cols) v[e] = other;
+    }
+}
+
+// Writes elements [c, c + E) of a row that are below cols.
+template <class T, bool WHOLE = false>
+__device__ __forceinline__ void store_row(T *row, int c, int cols, const float (&v)[kVec<T>], const void *base,
+                                          int64_t extent) {
+    if (c >= cols) return;
+    const int n = WHOLE ? kVec<T> : min(kVec<T>, cols - c);
+    if (!QT2_STORE_OK(row + c, n * sizeof(T), base, extent * sizeof(T))) return;
+    if (n == kVec<T>) {
+        *reinterpret_cast<uint4 *>(row + c) = pack(v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e)
+            if (e < n) row[c + e] = from_f32<T>(v[e]);
+    }
+}
+
+// Pairs of fp32 values in a 64-bit register, and the packed instructions on them: they halve the
+// instructions an element costs, which is what bounds these kernels next to HBM.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    const float2 p = f2_get(v);
+    return p.x + p.y;
+}
+// The pairs of a 16-byte vector, and back (rounded to the row's type).
+__device__ __forceinline__ uint64_t bf16_pair_f2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+template <class T>
+__device__ __forceinline__ void pairs_of(const uint4 &r, uint64_t (&v)[kVec<T> / 2]) {
+    if constexpr (kVec<T> == 8) {
+        v[0] = bf16_pair_f2(r.x); v[1] = bf16_pair_f2(r.y); v[2] = bf16_pair_f2(r.z); v[3] = bf16_pair_f2(r.w);
+    } else {
+        v[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+        v[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+}
+template <int E>
+__device__ __forceinline__ void floats_of(const uint64_t (&p)[E / 2], float (&v)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const float2 q = f2_get(p[e / 2]);
+        v[e] = q.x;
+        v[e + 1] = q.y;
+    }
+}
+
+// Sums of N values (a power of two) over the G threads of a row, the same in each of them.  Within
+// a warp the values are scattered over the lanes while they are added: each of the first log2 N
+// exchanges halves the values a lane still holds.  The warps of a longer row's group of threads (the
+// block, or barrier `bar`'s G threads of it) meet at a barrier; the slot alternates between calls, so
+// one barrier a call is enough.
+template <int G>
+__device__ __forceinline__ void group_sync(int bar) {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(G) : "memory");
+}
+template <int G, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (&sh)[2][32][N], int slot, int bar = 0) {
+    constexpr int W = G < 32 ? G : 32;
+    const int lane = threadIdx.x & 31;
+    static_assert(N <= W && (N & (N - 1)) == 0, "values scatter over the lanes");
+    int o = W / 2;
+#pragma unroll
+    for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float mine = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+            v[i] = mine + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+    }
+    // v[0] is value i's partial sum, i the lane's top log2 N bits within the row's lanes
+    float t = v[0];
+#pragma unroll
+    for (; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if constexpr (G > 32) {
+        constexpr int kWarps = G / 32, kEach = 32 / N;   // lanes that hold a value
+        if (lane % kEach == 0) sh[slot][(threadIdx.x % G) >> 5][lane / kEach] = t;
+        group_sync<G>(bar);
+        // kEach lanes a value add up the warps' sums
+        t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w += kEach)
+            if (w + lane % kEach < kWarps) t += sh[slot][w + lane % kEach][lane / kEach];
+#pragma unroll
+        for (int d = kEach / 2; d > 0; d >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = N == 1 ? t : __shfl_sync(0xFFFFFFFFu, t, (lane & ~(W - 1)) + n * (W / N));
 }
 
 struct NormArgs {
@@ -39,31 +188,665 @@ struct NormArgs {
     void *y;             // forward: y; backward: dx
     float *mean, *rstd;
     int64_t rows, ldx, lddy, ldy;
-    int cols;
+    int cols, w_f32;
     float eps;
     float *part;         // [splits][2][cols]
     int splits;
     void *dw, *db;
 };
 
-template <class T, class W>
-__global__ void __launch_bounds__(kNormThreads) layernorm_fwd_kernel(const NormArgs a) {
-    __shared__ float sh[32];
+// Vector c / E of a row, zeros behind the row's end.
+template <class T>
+__device__ __forceinline__ uint4 load_row(const T *row, int c, int cols, bool live) {
+    constexpr int E = kVec<T>;
+    if (!live || c >= cols) return make_uint4(0, 0, 0, 0);
+    uint4 r = *reinterpret_cast<const uint4 *>(row + c);
+    if (c + E > cols) {   // only a row's last vector
+        float v[E];
+        unpack(r, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c + e >= cols) v[e] = 0.0f;
+        r = pack(v);
+    }
+    return r;
+}
+
+// Vector i of a row in shared memory, zeros behind the row's end.
+template <class T>
+__device__ __forceinline__ uint4 stage_vec(const uint4 *stage, int i, int cols) {
+    return load_row(reinterpret_cast<const T *>(stage), i * kVec<T>, cols, true);
+}
+
+// Keeps the compiler from holding a vector's unpacked values across this point: unpacking again is
+// cheaper than the registers (16 vectors of bf16 a lane would take 128).
+__device__ __forceinline__ void repack(uint4 &r) { asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)); }
+
+// ---------------------------------------------------------------------------------------------
+// Forward, a warp a row (short rows: B of them at a time), V vectors of 16 bytes a lane: one read and one write of HBM, no barrier
+// between rows.  A bulk copy brings a warp's next row into its part of shared memory while this row,
+// in packed registers, goes through its three passes (mean, squared differences, result): without
+// it every warp waits for its row, then computes, and HBM idles meanwhile (16384 x 4096 bf16: 58 us).
+// Weights and biases wait in shared memory as fp32, the vectors' first and second halves apart, so
+// that a warp's 16-byte reads touch every bank once; read from global memory for each row they
+// cost more L1 wavefronts than the row itself.
+// ---------------------------------------------------------------------------------------------
+template <class T>
+__host__ __device__ inline int norm_row_bytes(int cols) { return (cols * (int)sizeof(T) + 15) / 16 * 16; }
+
+template <class T, int V, int B>
+__global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(const NormArgs a) {
+    constexpr int E = kVec<T>, P = E / 2, Q = E / 4;
+    extern __shared__ float4 weights[];   // [2 (weight, bias)][Q][32 V], then B rows a warp
+    __shared__ __align__(8) uint64_t full[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t row = ((int64_t)blockIdx.x * warps + warp) * B;
+    const int64_t stride = (int64_t)gridDim.x * warps * B;
+    const uint4 *stage = reinterpret_cast<const uint4 *>(weights + 2 * Q * 32 * V) + warp * B * 32 * V;
+    const uint32_t bar = smem_u32(full + warp);
+    const int row_bytes = norm_row_bytes<T>(a.cols);
+    auto issue = [&](int64_t r) {
+        if (r >= a.rows) return;
+        const int n = (int)min((int64_t)B, a.rows - r);
+        mbar_arrive_expect_tx(bar, n * row_bytes);
+        for (int k = 0; k < n; ++k)
+            bulk_load(smem_u32(stage + k * 32 * V), static_cast<const T *>(a.x) + (r + k) * a.ldx, row_bytes, bar);
+    };
+    if (lane == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        issue(row);
+    }
+    for (int i = threadIdx.x; i < 32 * V && i * E < a.cols; i += blockDim.x) {
+        float w[E], b[E];
+        load_weight(a.w, a.w_f32, i * E, a.cols, 1.0f, w);
+        load_weight(a.b, a.w_f32, i * E, a.cols, 0.0f, b);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            weights[q * 32 * V + i] = make_float4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            weights[(Q + q) * 32 * V + i] = make_float4(b[4 * q], b[4 * q + 1], b[4 * q + 2], b[4 * q + 3]);
+        }
+    }
+    __syncthreads();
+    float none[2][32][B];
+    uint32_t phase = 0;
+    bool ok = true;   // after a wait that ran out (reported), the rest is not waited for
+    for (; row < a.rows; row += stride) {
+        if (ok) ok = mbar_wait_warp(bar, phase);
+        phase ^= 1;
+        uint4 raw[B][V];
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                raw[k][i] = load_row(reinterpret_cast<const T *>(stage + k * 32 * V), (lane + i * 32) * E, a.cols,
+                                     row + k < a.rows);
+        __syncwarp();
+        if (lane == 0 && ok) issue(row + stride);
+        float s[B], mean[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            uint64_t s2[2] = {};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                uint64_t v[P];
+                pairs_of<T>(raw[k][i], v);
+#pragma unroll
+                for (int e = 0; e < P; ++e) s2[e & 1] = f2_add(s2[e & 1], v[e]);
+            }
+            s[k] = f2_sum(f2_add(s2[0], s2[1]));
+        }
+        row_sum<32>(s, none, 0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            mean[k] = s[k] / a.cols;
+            const uint64_t neg = f2(-mean[k], -mean[k]);
+            uint64_t s2[2] = {};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (lane + i * 32) * E;
+                uint64_t v[P];
+                repack(raw[k][i]);
+                pairs_of<T>(raw[k][i], v);
+                if (c + E <= a.cols) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const uint64_t d = f2_add(v[e], neg);
+                        s2[e & 1] = f2_fma(d, d, s2[e & 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const float2 x = f2_get(v[e]);
+                        const uint64_t d = f2(c + 2 * e < a.cols ? x.x - mean[k] : 0.0f,
+                                              c + 2 * e + 1 < a.cols ? x.y - mean[k] : 0.0f);
+                        s2[e & 1] = f2_fma(d, d, s2[e & 1]);
+                    }
+                }
+            }
+            s[k] = f2_sum(f2_add(s2[0], s2[1]));
+        }
+        row_sum<32>(s, none, 0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) s[k] = 1.0f / sqrtf(s[k] / a.cols + a.eps);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (lane + i * 32) * E;
+            if (c >= a.cols) continue;
+            uint64_t w[P], b[P];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float4 p = weights[q * 32 * V + lane + i * 32], r = weights[(Q + q) * 32 * V + lane + i * 32];
+                w[2 * q] = f2(p.x, p.y);
+                w[2 * q + 1] = f2(p.z, p.w);
+                b[2 * q] = f2(r.x, r.y);
+                b[2 * q + 1] = f2(r.z, r.w);
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (row + k >= a.rows) continue;
+                const uint64_t neg = f2(-mean[k], -mean[k]), r2 = f2(s[k], s[k]);
+                uint64_t v[P];
+                repack(raw[k][i]);
+                pairs_of<T>(raw[k][i], v);
+#pragma unroll
+                for (int e = 0; e < P; ++e) v[e] = f2_fma(f2_mul(f2_add(v[e], neg), r2), w[e], b[e]);
+                float o[E];
+                floats_of<E>(v, o);
+                store_row(static_cast<T *>(a.y) + (row + k) * a.ldy, c, a.cols, o, a.y,
+                          (a.rows - 1) * a.ldy + a.cols);
+            }
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (row + k >= a.rows) continue;
+                if (a.mean) a.mean[row + k] = mean[k];
+                if (a.rstd) a.rstd[row + k] = s[k];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Forward, longer rows: a group of G threads a row, V vectors a thread, whose weights and biases stay
+// in registers; the next row comes by bulk copy while this one, in registers, is worked on.
+// ---------------------------------------------------------------------------------------------
+constexpr int kNormAhead = 3;   // rows on their way to a group, next to the one in registers
+template <class T, int G, int V>
+__global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(const NormArgs a) {
+    constexpr int E = kVec<T>, P = E / 2, kGroups = 1024 / G, S = kNormAhead;
+    extern __shared__ __align__(16) uint8_t rows_all[];   // [groups][S][row]
+    __shared__ float sh_all[kGroups][2][32][1];
+    __shared__ __align__(8) uint64_t full_all[kGroups][S];
+    const int cols = a.cols, row_bytes = norm_row_bytes<T>(cols);
+    const int group = threadIdx.x / G, lane = threadIdx.x % G, bar = group + 1;
+    const uint8_t *const ring = rows_all + (size_t)group * S * row_bytes;
+    const uint32_t full0 = smem_u32(full_all[group]);
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    auto issue = [&](int64_t r, int st) {
+        if (r >= a.rows) return;
+        mbar_arrive_expect_tx(full0 + 8 * st, row_bytes);
+        bulk_load(smem_u32(ring + st * row_bytes), static_cast<const T *>(a.x) + r * a.ldx, row_bytes, full0 + 8 * st);
+    };
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_mbar_init();
+        for (int i = 0; i < S; ++i) issue(row + i * step, i);
+    }
+    uint64_t w[V][P], b[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (lane + i * G) * E;
+        float f[E];
+        load_weight(c < cols ? a.w : nullptr, a.w_f32, c, cols, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[i][e] = f2(f[2 * e], f[2 * e + 1]);
+        load_weight(c < cols ? a.b : nullptr, a.w_f32, c, cols, 0.0f, f);
+#pragma unroll
+        for (int e = 0; e < P; ++e) b[i][e] = f2(f[2 * e], f[2 * e + 1]);
+    }
+    __syncthreads();
+    int st = 0, phase = 0;
+    bool ok = true;   // after a wait that ran out (reported), the rest is not waited for
+    for (; row < a.rows; row += step) {
+        if (ok) ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        const uint4 *const stage = reinterpret_cast<const uint4 *>(ring + st * row_bytes);
+        uint4 raw[V];
+        uint64_t s2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            raw[i] = stage_vec<T>(stage, lane + i * G, cols);
+            uint64_t v[P];
+            pairs_of<T>(raw[i], v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) s2 = f2_add(s2, v[e]);
+        }
+        float s[1] = {f2_sum(s2)};
+        row_sum<G>(s, sh_all[group], 0, bar);
+        // every thread has the row in registers: its slot takes the one S on
+        if (lane == 0 && ok) issue(row + S * step, st);
+        if (++st == S) {
+            st = 0;
+            phase ^= 1;
+        }
+        const float mean = s[0] / cols;
+        const uint64_t neg = f2(-mean, -mean);
+        s2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (lane + i * G) * E;
+            uint64_t v[P];
+            repack(raw[i]);
+            pairs_of<T>(raw[i], v);
+            if (c + E <= cols) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const uint64_t d = f2_add(v[e], neg);
+                    s2 = f2_fma(d, d, s2);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const float2 x = f2_get(v[e]);
+                    const uint64_t d = f2(c + 2 * e < cols ? x.x - mean : 0.0f, c + 2 * e + 1 < cols ? x.y - mean : 0.0f);
+                    s2 = f2_fma(d, d, s2);
+                }
+            }
+        }
+        s[0] = f2_sum(s2);
+        row_sum<G>(s, sh_all[group], 1, bar);
+        const float rstd = 1.0f / sqrtf(s[0] / cols + a.eps);
+        const uint64_t r2 = f2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (lane + i * G) * E;
+            if (c >= cols) continue;
+            uint64_t v[P];
+            repack(raw[i]);
+            pairs_of<T>(raw[i], v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) v[e] = f2_fma(f2_mul(f2_add(v[e], neg), r2), w[i][e], b[i][e]);
+            float o[E];
+            floats_of<E>(v, o);
+            store_row(static_cast<T *>(a.y) + row * a.ldy, c, cols, o, a.y, (a.rows - 1) * a.ldy + cols);
+        }
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Backward, rows of up to 64 columns, one read of x and dy and one write of dx: G threads of a warp
+// a row, V vectors a thread, B rows at a time; the next rows are on their way while these are reduced and written.  A thread keeps its
+// columns (and their weights) for all of the block's rows and sums their dw and db in registers; a
+// block leaves one partial sum a column, which layernorm_dw_kernel adds up.  With d = x - mean
+// the row's sums are sum(a) and sum(a d), and
+//   dx = rstd a - (rstd^3 sum(a d) / C) d - rstd sum(a) / C.
+// ---------------------------------------------------------------------------------------------
+template <class T, int G, int V, int B>
+__global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a) {
+    constexpr int E = kVec<T>, P = E / 2, kThreads = 256, kGroups = kThreads / G;
+    __shared__ float sh[2][32][2 * B];
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    uint64_t w[V][P], dw2[V][P] = {}, db2[V][P] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (lane + i * G) * E;
+        float f[E];
+        load_weight(c < a.cols ? a.w : nullptr, a.w_f32, c, a.cols, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[i][e] = f2(f[2 * e], f[2 * e + 1]);
+    }
+    const float inv = 1.0f / a.cols;
+    int slot = 0;
+    uint4 rx[B][V], rd[B][V];
+    float mean[B], rstd[B];
+    auto fetch = [&](int64_t r0) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const bool live = r0 + k < a.rows;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (lane + i * G) * E;
+                rx[k][i] = load_row(static_cast<const T *>(a.x) + (r0 + k) * a.ldx, c, a.cols, live);
+                rd[k][i] = load_row(static_cast<const T *>(a.dy) + (r0 + k) * a.lddy, c, a.cols, live);
+            }
+            mean[k] = live ? a.mean[r0 + k] : 0.0f;
+            rstd[k] = live ? a.rstd[r0 + k] : 0.0f;
+        }
+    };
+    int64_t at = (int64_t)blockIdx.x * kGroups * B;
+    const int64_t stride = (int64_t)gridDim.x * kGroups * B;
+    fetch(at + group * B);
+    // the trip count is the block's, not the group's: every lane of a warp meets the shuffles of row_sum
+    for (; at < a.rows; at += stride) {
+        const int64_t r0 = at + group * B;
+        float s[2 * B], scale[B];
+        uint64_t d[B][V][P], p[B][V][P];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const uint64_t neg = f2(-mean[k], -mean[k]), r2 = f2(rstd[k], rstd[k]);
+            uint64_t s2 = 0, q2 = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                uint64_t x[P], g[P];
+                pairs_of<T>(rx[k][i], x);
+                pairs_of<T>(rd[k][i], g);   // zero behind the row's end
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    d[k][i][e] = f2_add(x[e], neg);
+                    p[k][i][e] = f2_mul(g[e], w[i][e]);
+                    s2 = f2_add(s2, p[k][i][e]);
+                    q2 = f2_fma(p[k][i][e], d[k][i][e], q2);
+                    db2[i][e] = f2_add(db2[i][e], g[e]);
+                    dw2[i][e] = f2_fma(g[e], f2_mul(d[k][i][e], r2), dw2[i][e]);
+                }
+            }
+            s[2 * k] = f2_sum(s2);
+            s[2 * k + 1] = f2_sum(q2);
+            scale[k] = rstd[k];
+        }
+        fetch(r0 + stride);
+        if (a.y) {
+            row_sum<G>(s, sh, slot);
+            slot ^= 1;
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (r0 + k >= a.rows) continue;
+                const float m1 = -s[2 * k] * inv * scale[k];
+                const float m2 = -s[2 * k + 1] * inv * scale[k] * scale[k] * scale[k];
+                const uint64_t m1p = f2(m1, m1), m2p = f2(m2, m2), r2 = f2(scale[k], scale[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        p[k][i][e] = f2_fma(p[k][i][e], r2, f2_fma(d[k][i][e], m2p, m1p));
+                    float o[E];
+                    floats_of<E>(p[k][i], o);
+                    store_row(static_cast<T *>(a.y) + (r0 + k) * a.ldy, (lane + i * G) * E, a.cols, o, a.y,
+                              (a.rows - 1) * a.ldy + a.cols);
+                }
+            }
+        }
+    }
+    if (!a.part) return;
+    float dw[V][E], db[V][E];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        floats_of<E>(dw2[i], dw[i]);
+        floats_of<E>(db2[i], db[i]);
+    }
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    // the groups' sums meet in shared memory, in the groups' order
+    __shared__ float sum[kGroups][G * V * E];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                sum[group][(lane + i * G) * E + e] = which ? db[i][e] : dw[i][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < min(a.cols, G * V * E); c += kThreads) {
+            float t = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) t += sum[q][c];
+            part[which * a.cols + c] = t;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// The same for rows of more than 64 columns: one block an SM, whose groups of G threads each take B
+// rows at a time, V vectors a thread; bulk copies bring the rows of x and dy into the group's ring of
+// S slots in shared memory.  In flight is then what shared memory holds, not what registers are left
+// for; a row's vectors are read from shared memory twice instead of being held over the row's
+// sums.  The groups' sums of dw and db meet in shared memory, so that an SM leaves one partial
+// sum a column (from a block a group, 888 of them at 2048 columns, they cost 19 us of 87).  WHOLE: the
+// row's length is a multiple of the vector's, so that no vector has to be cut.
+// ---------------------------------------------------------------------------------------------
+// The parameters for rows of up to 16 G columns (8 G: half the vectors, twice the rows).  bf16: two
+// rows share the loop's and the sums' instructions, and a deeper ring is worth more than more threads
+// (32768 x 2048: one row at a time 94 us, two 79 us; 640 threads and 2 slots 76 us, 512 and 3 slots less).
+// fp32 has half the instructions a byte, and twice the bytes to hold.
+template <class T, int G, bool HALF>
+struct NormRing {
+    static constexpr bool k16 = sizeof(T) == 2;
+    static constexpr int V = (HALF ? 8 : 16) / kVec<T>;          // vectors a thread
+    static constexpr int B = (k16 ? 2 : 1) * (HALF ? 2 : 1);     // rows at a time
+    static constexpr int S = k16 || G == 512 ? 3 : 2;            // slots of B rows
+    static constexpr int kGroups = (k16 || G == 512 ? 512 : 768) / G;
+    static constexpr int kColumns = (HALF ? 8 : 16) * G;
+    static constexpr int bytes(int cols) { return kGroups * S * B * 2 * norm_row_bytes<T>(cols); }
+};
+
+template <class T, int G, bool HALF, bool WHOLE>
+__global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm_bwd_ring_kernel(const NormArgs a) {
+    using R = NormRing<T, G, HALF>;
+    constexpr int E = kVec<T>, P = E / 2, V = R::V, S = R::S, B = R::B, kGroups = R::kGroups;
+    extern __shared__ __align__(16) uint8_t ring_all[];   // [groups][S][B][2 (x, dy)][row]
+    __shared__ float sh_all[kGroups][2][32][2 * B];
+    __shared__ __align__(8) uint64_t full_all[kGroups][S];
+    const int cols = a.cols, rows = (int)a.rows, row_bytes = norm_row_bytes<T>(cols);
+    const int group = threadIdx.x / G, lane = threadIdx.x % G, bar = group + 1;
+    uint8_t *const ring = ring_all + (size_t)group * S * B * 2 * row_bytes;
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full_all[group]);
+    const int step = (int)gridDim.x * kGroups * B;
+    // the group's first thread brings rows [r, r + B) into slot st
+    auto issue = [&](int r, int st) {
+        const int n = min(B, rows - r);
+        if (n <= 0) return;
+        mbar_arrive_expect_tx(full0 + 8 * st, n * 2 * row_bytes);
+        for (int k = 0; k < n; ++k) {
+            const uint32_t dst = ring0 + (st * B + k) * 2 * row_bytes;
+            bulk_load(dst, static_cast<const T *>(a.x) + (r + k) * a.ldx, row_bytes, full0 + 8 * st);
+            bulk_load(dst + row_bytes, static_cast<const T *>(a.dy) + (r + k) * a.lddy, row_bytes, full0 + 8 * st);
+        }
+    };
+    const int first = ((int)blockIdx.x * kGroups + group) * B;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_mbar_init();
+        for (int i = 0; i < S - 1; ++i) issue(first + i * step, i);
+    }
+    uint64_t w[V][P], dw2[V][P] = {}, db2[V][P] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (lane + i * G) * E;
+        float f[E];
+        load_weight(c < cols ? a.w : nullptr, a.w_f32, c, cols, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[i][e] = f2(f[2 * e], f[2 * e + 1]);
+    }
+    __syncthreads();
+    const float inv = 1.0f / cols;
+    bool ok = true;   // after a wait that ran out (reported), the rest is not waited for
+    float mean[B], rstd[B], next_mean[B], next_rstd[B];
+    auto stats = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            next_mean[k] = r + k < rows ? a.mean[r + k] : 0.0f;
+            next_rstd[k] = r + k < rows ? a.rstd[r + k] : 0.0f;
+        }
+    };
+    stats(first);
+    int st = 0, phase = 0, slot = 0;
+    for (int row = first; row < rows; row += step) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            mean[k] = next_mean[k];
+            rstd[k] = next_rstd[k];
+        }
+        stats(row + step);
+        if (ok) ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        const uint4 *const px = reinterpret_cast<const uint4 *>(ring + st * B * 2 * row_bytes);
+        // pairs of x - mean and of dy of row k's vector v; zeros behind the row's end
+        auto read = [&](int k, int v, uint64_t (&d)[P], uint64_t (&g)[P]) {
+            const int at = lane + v * G, c = at * E;
+            const uint64_t neg = f2(-mean[k], -mean[k]);
+            const uint4 *x = px + 2 * k * (row_bytes >> 4) + at, *y = x + (row_bytes >> 4);
+            if (WHOLE || c + E <= cols) {
+                pairs_of<T>(*x, d);
+                pairs_of<T>(*y, g);
+#pragma unroll
+                for (int e = 0; e < P; ++e) d[e] = f2_add(d[e], neg);
+                return;
+            }
+            float xf[E], yf[E];
+            unpack(*x, xf);
+            unpack(*y, yf);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const bool one = c + e < cols, both = c + e + 1 < cols;
+                d[e / 2] = f2(one ? xf[e] - mean[k] : 0.0f, both ? xf[e + 1] - mean[k] : 0.0f);
+                g[e / 2] = f2(one ? yf[e] : 0.0f, both ? yf[e + 1] : 0.0f);
+            }
+        };
+        float s[2 * B] = {};
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (row + k >= rows) continue;
+            const uint64_t r2 = f2(rstd[k], rstd[k]);
+            uint64_t s2 = 0, q2 = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if ((lane + v * G) * E >= cols) continue;
+                uint64_t d[P], g[P];
+                read(k, v, d, g);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const uint64_t p = f2_mul(g[e], w[v][e]);
+                    s2 = f2_add(s2, p);
+                    q2 = f2_fma(p, d[e], q2);
+                    db2[v][e] = f2_add(db2[v][e], g[e]);
+                    dw2[v][e] = f2_fma(g[e], f2_mul(d[e], r2), dw2[v][e]);
+                }
+            }
+            s[2 * k] = f2_sum(s2);
+            s[2 * k + 1] = f2_sum(q2);
+        }
+        row_sum<G>(s, sh_all[group], slot, bar);
+        slot ^= 1;
+        if (G == 32) __syncwarp();
+        // every thread is past the rows before these: their slot takes the rows S - 1 steps ahead
+        if (lane == 0 && ok) issue(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
+        if (a.y) {
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (row + k >= rows) continue;
+                const float m1 = -s[2 * k] * inv * rstd[k];
+                const float m2 = -s[2 * k + 1] * inv * rstd[k] * rstd[k] * rstd[k];
+                const uint64_t m1p = f2(m1, m1), m2p = f2(m2, m2), r2 = f2(rstd[k], rstd[k]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int c = (lane + v * G) * E;
+                    if (c >= cols) continue;
+                    uint64_t d[P], g[P];
+                    read(k, v, d, g);
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        g[e] = f2_fma(f2_mul(g[e], w[v][e]), r2, f2_fma(d[e], m2p, m1p));
+                    float o[E];
+                    floats_of<E>(g, o);
+                    store_row<T, WHOLE>(static_cast<T *>(a.y) + (row + k) * a.ldy, c, cols, o, a.y,
+                                        (a.rows - 1) * a.ldy + cols);
+                }
+            }
+        }
+        if (++st == S) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    if (!a.part) return;
+    // the rings' rows are all read: every group leaves its sums at the start of its ring
+    __syncthreads();
+    float *const mine = reinterpret_cast<float *>(ring);   // [2][cols]
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float dw[E], db[E];
+        floats_of<E>(dw2[v], dw);
+        floats_of<E>(db2[v], db);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = (lane + v * G) * E + e;
+            if (c >= cols) continue;
+            mine[c] = dw[e];
+            mine[cols + c] = db[e];
+        }
+    }
+    __syncthreads();
+    float *part = a.part + (int64_t)blockIdx.x * 2 * cols;
+    for (int c = threadIdx.x; c < 2 * cols; c += kGroups * G) {
+        float t = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q)
+            t += reinterpret_cast<const float *>(ring_all + (size_t)q * S * B * 2 * row_bytes)[c];
+        part[c] = t;
+    }
+}
+
+// dw (blockIdx.y = 0) or db: the sum of the partial sums, 32 columns a block, 32 slices of the
+// partial sums side by side.
+__global__ void __launch_bounds__(1024) layernorm_dw_kernel(const NormArgs a) {
+    __shared__ float sh[32][33];
+    void *out = blockIdx.y ? a.db : a.dw;
+    if (!out) return;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+    float t = 0.0f;
+    if (c < a.cols) {
+        const float *part = a.part + (int64_t)blockIdx.y * a.cols + c;
+#pragma unroll 16
+        for (int i = slice; i < a.splits; i += 32) t += part[(int64_t)i * 2 * a.cols];
+    }
+    sh[slice][threadIdx.x & 31] = t;
+    __syncthreads();
+    t = sh[threadIdx.x & 31][slice];   // column `slice` of the block's 32, one slice a lane
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    const int d = blockIdx.x * 32 + slice;
+    if ((threadIdx.x & 31) != 0 || d >= a.cols) return;
+    if (!QT2_STORE_OK(static_cast<uint8_t *>(out) + (int64_t)d * (a.w_f32 ? 4 : 2), a.w_f32 ? 4 : 2, out,
+                      (int64_t)a.cols * (a.w_f32 ? 4 : 2)))
+        return;
+    if (a.w_f32)
+        static_cast<float *>(out)[d] = t;
+    else
+        static_cast<__nv_bfloat16 *>(out)[d] = __float2bfloat16_rn(t);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Rows too long for registers: a block a row, which it reads three times (from L2 after the first).
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ float weight_at(const void *w, int f32, int c, float other) {
+    if (!w) return other;
+    return f32 ? static_cast<const float *>(w)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const NormArgs a) {
+    __shared__ float sh[2][32][1];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
     T *y = static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy;
-    const W *w = static_cast<const W *>(a.w), *b = static_cast<const W *>(a.b);
-    float s = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) s += to_f32(x[c]);
-    const float mean = block_sum(s, sh) / a.cols;
-    s = 0.0f;
+    float s[1] = {0.0f};
+    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) s[0] += to_f32(x[c]);
+    row_sum<kNormThreads>(s, sh, 0);
+    const float mean = s[0] / a.cols;
+    s[0] = 0.0f;
     for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
         const float d = to_f32(x[c]) - mean;
-        s = fmaf(d, d, s);
+        s[0] = fmaf(d, d, s[0]);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(s, sh) / a.cols + a.eps);
+    row_sum<kNormThreads>(s, sh, 1);
+    const float rstd = 1.0f / sqrtf(s[0] / a.cols + a.eps);
     for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
         const float h = (to_f32(x[c]) - mean) * rstd;
-        const float o = fmaf(h, w ? to_f32(w[c]) : 1.0f, b ? to_f32(b[c]) : 0.0f);
+        const float o = fmaf(h, weight_at(a.w, a.w_f32, c, 1.0f), weight_at(a.b, a.w_f32, c, 0.0f));
         if (QT2_STORE_OK(y + c, sizeof(T), a.y, ((a.rows - 1) * a.ldy + a.cols) * sizeof(T))) y[c] = from_f32<T>(o);
     }
     if (threadIdx.x == 0) {
@@ -72,32 +855,31 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_kernel(const NormA
     }
 }
 
-template <class T, class W>
-__global__ void __launch_bounds__(kNormThreads) layernorm_dx_kernel(const NormArgs a) {
-    __shared__ float sh[32];
+template <class T>
+__global__ void __launch_bounds__(kNormThreads) layernorm_dx_long_kernel(const NormArgs a) {
+    __shared__ float sh[2][32][2];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
     const T *dy = static_cast<const T *>(a.dy) + (int64_t)blockIdx.x * a.lddy;
     T *dx = static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy;
-    const W *w = static_cast<const W *>(a.w);
     const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-    float s = 0.0f, q = 0.0f;
+    float s[2] = {};
     for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.0f);
-        s += g;
-        q = fmaf(g, h, q);
+        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * weight_at(a.w, a.w_f32, c, 1.0f);
+        s[0] += g;
+        s[1] = fmaf(g, h, s[1]);
     }
-    s = block_sum(s, sh) / a.cols;
-    q = block_sum(q, sh) / a.cols;
+    row_sum<kNormThreads>(s, sh, 0);
+    const float m1 = s[0] / a.cols, m2 = s[1] / a.cols;
     for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.0f);
+        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * weight_at(a.w, a.w_f32, c, 1.0f);
         if (QT2_STORE_OK(dx + c, sizeof(T), a.y, ((a.rows - 1) * a.ldy + a.cols) * sizeof(T)))
-            dx[c] = from_f32<T>(rstd * (g - s - h * q));
+            dx[c] = from_f32<T>(rstd * (g - m1 - h * m2));
     }
 }
 
 // Partial sums of dw and db over rows split, split + splits, ...: one thread a column.
 template <class T>
-__global__ void __launch_bounds__(kNormThreads) layernorm_dw_part_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) layernorm_dw_long_kernel(const NormArgs a) {
     const int c = blockIdx.x * kNormThreads + threadIdx.x;
     if (c >= a.cols) return;
     float dw = 0.0f, db = 0.0f;
@@ -108,21 +890,6 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_dw_part_kernel(const N
     }
     a.part[((int64_t)blockIdx.y * 2) * a.cols + c] = dw;
     a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = db;
-}
-
-template <class W>
-__global__ void __launch_bounds__(kNormThreads) layernorm_dw_kernel(const NormArgs a) {
-    const int c = blockIdx.x * kNormThreads + threadIdx.x;
-    if (c >= a.cols) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int i = 0; i < a.splits; ++i) {
-        dw += a.part[((int64_t)i * 2) * a.cols + c];
-        db += a.part[((int64_t)i * 2 + 1) * a.cols + c];
-    }
-    if (a.dw && QT2_STORE_OK(static_cast<W *>(a.dw) + c, sizeof(W), a.dw, a.cols * sizeof(W)))
-        static_cast<W *>(a.dw)[c] = from_f32<W>(dw);
-    if (a.db && QT2_STORE_OK(static_cast<W *>(a.db) + c, sizeof(W), a.db, a.cols * sizeof(W)))
-        static_cast<W *>(a.db)[c] = from_f32<W>(db);
 }
 
 }  // namespace qt2

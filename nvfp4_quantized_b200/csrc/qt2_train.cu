@@ -31,32 +31,158 @@ qt2_status check_workspace(const void *ws, size_t have, size_t need) {
 }
 
 // ------------------------------------------------------------------------------- layer norm
-int norm_splits(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(64, rows / 16)); }
-
-template <class T, class W>
+// Resident blocks of a kernel on this device, asked once a device.
+template <class F>
+cudaError_t resident_blocks(PerDeviceOnce &once, std::atomic<int> *blocks, F kernel, int threads, int smem, int64_t *n) {
+    const cudaError_t e = once.run([&] {
+        int v = 0;
+        const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, smem);
+        if (f == cudaSuccess) blocks[current_device()].store(std::max(1, v) * sm_count());
+        return f;
+    });
+    if (e == cudaSuccess) *n = blocks[current_device()].load();
+    return e;
+}
+template <class T, int V, int B>
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_fwd_kernel<T, W><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
+    static PerDeviceOnce attr, once;
+    static std::atomic<int> blocks[kMaxDevices];
+    // weights and biases as fp32, and B rows a warp
+    auto smem = [](int warps) { return 32 * V * 16 * (8 / (int)sizeof(T) + B * warps); };
+    int64_t n = 0;
+    cudaError_t e = attr.run([&] {
+        return cudaFuncSetAttribute(layernorm_fwd_kernel<T, V, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(8));
+    });
+    if (e == cudaSuccess) e = resident_blocks(once, blocks, layernorm_fwd_kernel<T, V, B>, 256, smem(8), &n);
+    if (e != cudaSuccess) return e;
+    // fewer rows than the SMs have warps: smaller blocks spread them over more SMs
+    const int64_t steps = ceil_div(a.rows, B);
+    const int warps = (int)std::min<int64_t>(8, ceil_div(steps, sm_count()));
+    layernorm_fwd_kernel<T, V, B><<<(unsigned)std::min(n, ceil_div(steps, warps)), warps * 32, smem(warps), s>>>(a);
     return cudaGetLastError();
 }
-template <class T, class W>
-cudaError_t launch_norm_dx(const NormArgs &a, cudaStream_t s) {
+template <class T, int G>
+cudaError_t launch_norm_fwd_group(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_dx_kernel<T, W><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
+    constexpr int V = 16 / kVec<T>, kGroups = 1024 / G;
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(layernorm_fwd_group_kernel<T, G, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kGroups * kNormAhead * norm_row_bytes<T>(16 * G));
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = std::min<int64_t>(sm_count(), ceil_div(a.rows, kGroups));
+    layernorm_fwd_group_kernel<T, G, V>
+        <<<(unsigned)blocks, kGroups * G, kGroups * kNormAhead * norm_row_bytes<T>(a.cols), s>>>(a);
     return cudaGetLastError();
 }
 template <class T>
-cudaError_t launch_norm_dw_part(const NormArgs &a, cudaStream_t s) {
+cudaError_t launch_norm_fwd_long(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads), (unsigned)a.splits);
-    layernorm_dw_part_kernel<T><<<grid, kNormThreads, 0, s>>>(a);
+    layernorm_fwd_long_kernel<T><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <class W>
+template <class T>
+cudaError_t norm_fwd(const NormArgs &a, cudaStream_t s) {
+    const int64_t n = ceil_div(a.cols, kVec<T>);   // 16-byte vectors a row
+    if (n <= 32) return launch_norm_fwd<T, 1, 4>(a, s);
+    if (n <= 64) return launch_norm_fwd<T, 2, 4>(a, s);
+    if (n <= 128) return launch_norm_fwd<T, 4, 2>(a, s);
+    if (n <= 256) return launch_norm_fwd<T, 8, 1>(a, s);
+    if (n <= 512) return launch_norm_fwd<T, 16, 1>(a, s);
+    if (a.cols <= 4096) return launch_norm_fwd_group<T, 256>(a, s);
+    if (a.cols <= 8192) return launch_norm_fwd_group<T, 512>(a, s);
+    if (a.cols <= 16384) return launch_norm_fwd_group<T, 1024>(a, s);
+    return launch_norm_fwd_long<T>(a, s);
+}
+
+// The backward pass's threads a row (0: the row is too long for registers), rows a block and step,
+// and its blocks: resident ones, since every block leaves a partial
+// sum of dw and db, and no more of them than it takes for every one to run as many steps (rows too
+// long: the slices of the rows that dw and db are summed in).
+struct NormBwdPlan {
+    int threads, step, blocks;
+};
+template <class T>
+NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
+    auto ring = [](auto r) {
+        using R = decltype(r);
+        return NormBwdPlan{32, R::kGroups * R::B, 148};
+    };
+    NormBwdPlan p = cols <= 64     ? NormBwdPlan{8, 64, 148 * 2}
+                    : cols <= 256  ? ring(NormRing<T, 32, true>{})
+                    : cols <= 512  ? ring(NormRing<T, 32, false>{})
+                    : cols <= 1024 ? ring(NormRing<T, 64, false>{})
+                    : cols <= 2048 ? ring(NormRing<T, 128, false>{})
+                    : cols <= 4096 ? ring(NormRing<T, 256, false>{})
+                    : cols <= 8192 ? ring(NormRing<T, 512, false>{})
+                                   : NormBwdPlan{0, 16, 64};
+    const int64_t steps = ceil_div(rows, p.step);
+    p.blocks = (int)ceil_div(steps, ceil_div(steps, p.blocks));
+    return p;
+}
+
+template <class T, int G, int V, int B>
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    layernorm_bwd_kernel<T, G, V, B><<<(unsigned)a.splits, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T, int G, bool HALF, bool WHOLE>
+cudaError_t launch_norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    using R = NormRing<T, G, HALF>;
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, R::bytes(R::kColumns));
+    });
+    if (e != cudaSuccess) return e;
+    layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>
+        <<<(unsigned)a.splits, R::kGroups * G, R::bytes(a.cols), s>>>(a);
+    return cudaGetLastError();
+}
+template <class T, int G, bool HALF>
+cudaError_t norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
+    return a.cols % kVec<T> ? launch_norm_bwd_ring<T, G, HALF, false>(a, s)
+                            : launch_norm_bwd_ring<T, G, HALF, true>(a, s);
+}
 cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_dw_kernel<W><<<(unsigned)ceil_div(a.cols, kNormThreads), kNormThreads, 0, s>>>(a);
+    layernorm_dw_kernel<<<dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0, s>>>(a);
     return cudaGetLastError();
+}
+template <class T>
+cudaError_t launch_norm_dx_long(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    layernorm_dx_long_kernel<T><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T>
+cudaError_t launch_norm_dw_long(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads), (unsigned)a.splits);
+    layernorm_dw_long_kernel<T><<<grid, kNormThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T>
+cudaError_t norm_bwd(const NormArgs &a, int threads, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (threads == 0) {   // the sums before dx, which may be dy
+        if (a.part) e = launch_norm_dw_long<T>(a, s);
+        if (e == cudaSuccess && a.y) e = launch_norm_dx_long<T>(a, s);
+    } else {
+        e = a.cols <= 64     ? launch_norm_bwd<T, 8, 8 / kVec<T>, 2>(a, s)
+            : a.cols <= 256  ? norm_bwd_ring<T, 32, true>(a, s)
+            : a.cols <= 512  ? norm_bwd_ring<T, 32, false>(a, s)
+            : a.cols <= 1024 ? norm_bwd_ring<T, 64, false>(a, s)
+            : a.cols <= 2048 ? norm_bwd_ring<T, 128, false>(a, s)
+            : a.cols <= 4096 ? norm_bwd_ring<T, 256, false>(a, s)
+                             : norm_bwd_ring<T, 512, false>(a, s);
+    }
+    if (e == cudaSuccess && a.part) e = launch_norm_dw(a, s);
+    return e;
 }
 
 // ------------------------------------------------------------------------------- head loss
@@ -207,13 +333,6 @@ cudaError_t launch_grad_clip(const GradTable &t, const float *norm, float max_no
 }
 int grad_blocks(const GradTable &t) { return (int)std::min<int64_t>(t.first[t.count], kGradBlocks); }
 
-// f(T{}, W{}) with the element types of x_dtype and w_dtype.
-template <class F>
-cudaError_t with_types(int x_dtype, int w_dtype, F &&f) {
-    if (x_dtype == QT2_DTYPE_F32) return w_dtype == QT2_DTYPE_F32 ? f(float{}, float{}) : f(float{}, __nv_bfloat16{});
-    return w_dtype == QT2_DTYPE_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
-}
-
 }  // namespace
 
 extern "C" {
@@ -265,16 +384,18 @@ qt2_status qt2_layernorm_fwd(const void *x, int x_dtype, int64_t rows, int64_t c
     a.cols = (int)cols;
     a.ldx = ldx;
     a.ldy = ldy;
+    a.w_f32 = w_dtype == QT2_DTYPE_F32;
     a.eps = eps;
-    return from_cuda(with_types(x_dtype, w_dtype, [&](auto t, auto w) {
-        return launch_norm_fwd<decltype(t), decltype(w)>(a, as_stream(stream));
-    }));
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(x_dtype == QT2_DTYPE_F32 ? norm_fwd<float>(a, s) : norm_fwd<__nv_bfloat16>(a, s));
 }
 
 qt2_status qt2_layernorm_bwd_workspace_size(int64_t rows, int64_t cols, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
     if (!dim_ok(rows) || !dim_ok(cols)) return QT2_ERR_SHAPE;
-    *bytes = align_up((size_t)norm_splits(rows) * 2 * cols * sizeof(float), kWsAlign);
+    const int blocks = std::max(norm_bwd_plan<float>(rows, cols).blocks,
+                                norm_bwd_plan<__nv_bfloat16>(rows, cols).blocks);
+    *bytes = align_up((size_t)blocks * 2 * cols * sizeof(float), kWsAlign);
     return QT2_OK;
 }
 
@@ -307,22 +428,16 @@ qt2_status qt2_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int x_
     a.ldx = ldx;
     a.lddy = lddy;
     a.ldy = lddx;
-    a.part = static_cast<float *>(workspace);
-    a.splits = norm_splits(rows);
+    a.w_f32 = w_dtype == QT2_DTYPE_F32;
+    a.part = dweight || dbias ? static_cast<float *>(workspace) : nullptr;
+    const NormBwdPlan p = x_dtype == QT2_DTYPE_F32 ? norm_bwd_plan<float>(rows, cols)
+                                                   : norm_bwd_plan<__nv_bfloat16>(rows, cols);
+    a.splits = p.blocks;
     a.dw = dweight;
     a.db = dbias;
     const cudaStream_t s = as_stream(stream);
-    return from_cuda(with_types(x_dtype, w_dtype, [&](auto t, auto w) {
-        using T = decltype(t);
-        using W = decltype(w);
-        cudaError_t e = cudaSuccess;
-        if (dweight || dbias) {   // before dx, which may be dy
-            e = launch_norm_dw_part<T>(a, s);
-            if (e == cudaSuccess) e = launch_norm_dw<W>(a, s);
-        }
-        if (e == cudaSuccess && dx) e = launch_norm_dx<T, W>(a, s);
-        return e;
-    }));
+    return from_cuda(x_dtype == QT2_DTYPE_F32 ? norm_bwd<float>(a, p.threads, s)
+                                              : norm_bwd<__nv_bfloat16>(a, p.threads, s));
 }
 
 qt2_status qt2_linear_xent_fwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
