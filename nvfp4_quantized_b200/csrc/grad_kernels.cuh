@@ -2,8 +2,10 @@
 //
 //   norm = sqrt(sum_i sum_j g_ij^2),  out = g min(1, max_norm / (norm + 1e-6))
 //
-// The list travels in the kernel's parameters (no copy to the device, nothing that a captured
-// graph could find changed); tensors are cut into chunks that the blocks take in turn.
+// Both are streams over HBM: one read for the norm, one read and one write for the clipping.  The
+// list travels in the kernel's parameters (no copy to the device, nothing that a captured graph
+// could find changed).  Tensors are cut into chunks of 16-byte vectors, counted from the aligned
+// address at or below the tensor's first element; a thread has kGradVecs of them in flight.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -13,89 +15,193 @@
 namespace qt2 {
 
 constexpr int kGradThreads = 256;
-constexpr int kGradChunk = 8192;        // elements a block takes at a time
-constexpr int kGradTable = 128;         // tensors a launch takes
+constexpr int kGradVecs = 8;
+constexpr int kGradChunk = kGradThreads * kGradVecs;   // vectors a block takes at a time: 32 KB
+constexpr int kGradSmall = 32, kGradLarge = 512;       // tensors a launch's parameters hold
 
+template <int N>
 struct GradTable {
-    const void *grad[kGradTable];
-    void *out[kGradTable];
-    int64_t numel[kGradTable];
-    int64_t first[kGradTable + 1];      // chunks before tensor i; first[count] is their sum
-    uint32_t f32[kGradTable / 32];      // bit i: tensor i is fp32
+    const void *grad[N];
+    void *out[N];
+    int64_t numel[N];
+    int32_t first[N + 1];      // chunks before tensor i; first[count] is their sum
+    uint32_t f32[N / 32];      // bit i: tensor i is fp32
     int count;
 };
 
-__device__ __forceinline__ int grad_find(const GradTable &t, int64_t chunk) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
+// One chunk of a tensor: its vectors [lo, hi) from the aligned address `base` on, of which elements
+// [head, end) are the tensor's (counted from base).
+struct GradChunk {
+    const uint8_t *base;
+    int64_t lo, hi, head, end;
+    int tensor;
+    bool f32;
+};
+
+template <int N>
+__device__ __forceinline__ GradChunk grad_chunk(const GradTable<N> &t, int chunk) {
+    int k = 0, top = t.count - 1;
+    while (k < top) {
+        const int mid = (k + top + 1) >> 1;
         if (t.first[mid] <= chunk)
-            lo = mid;
+            k = mid;
         else
-            hi = mid - 1;
+            top = mid - 1;
     }
-    return lo;
+    GradChunk c;
+    c.tensor = k;
+    c.f32 = (t.f32[k >> 5] >> (k & 31)) & 1;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(t.grad[k]);
+    c.base = reinterpret_cast<const uint8_t *>(p & ~uintptr_t(15));
+    const int shift = c.f32 ? 2 : 1;
+    c.head = (int64_t)(p & 15) >> shift;
+    c.end = c.head + t.numel[k];
+    c.lo = (int64_t)(chunk - t.first[k]) * kGradChunk;
+    c.hi = min(c.lo + kGradChunk, (c.end + (16 >> shift) - 1) >> (4 - shift));
+    return c;
 }
 
-__device__ __forceinline__ float grad_load(const void *p, int64_t i, bool f32) {
-    return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+// The fp32 values of a vector; elements that are not the tensor's are zero.
+__device__ __forceinline__ void grad_values(const uint4 &r, const GradChunk &c, int64_t vec, float (&v)[8]) {
+    if (c.f32) {
+        v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+        v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+        v[4] = v[5] = v[6] = v[7] = 0.0f;
+    } else {
+        v[0] = bf16_lo(r.x); v[1] = bf16_hi(r.x); v[2] = bf16_lo(r.y); v[3] = bf16_hi(r.y);
+        v[4] = bf16_lo(r.z); v[5] = bf16_hi(r.z); v[6] = bf16_lo(r.w); v[7] = bf16_hi(r.w);
+    }
+    const int n = c.f32 ? 4 : 8;
+    const int64_t at = vec * n;
+    if (at < c.head || at + n > c.end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (at + e < c.head || at + e >= c.end) v[e] = 0.0f;
+    }
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable t, double *part) {
+// The vector's sum of squares.  In fp32 where that loses nothing: from 2^-80 up squares that underflow
+// are 2^-43 of it at most, and up to 2^120 none overflowed; else (also zeros, inf and NaN) in fp64.
+__device__ __forceinline__ double grad_squares(const float (&v)[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
+    if (s >= 0x1p-80f && s <= 0x1p120f) return (double)s;
+    float any = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) any = fmaxf(any, fabsf(v[e]));   // 0 for a vector of NaNs, whose s is NaN
+    if (any == 0.0f) return (double)s;
+    double d = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d += (double)v[e] * (double)v[e];
+    return d;
+}
+
+__device__ __forceinline__ double grad_block_sum(double sum) {
     __shared__ double sh[kGradThreads / 32];
-    double sum = 0.0;
-    const int64_t chunks = t.first[t.count];
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int k = grad_find(t, c);
-        const int64_t lo = (c - t.first[k]) * kGradChunk, hi = min(t.numel[k], lo + kGradChunk);
-        const bool f32 = (t.f32[k >> 5] >> (k & 31)) & 1;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kGradThreads) {
-            const double g = grad_load(t.grad[k], i, f32);
-            sum += g * g;
-        }
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
     __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kGradThreads / 32; ++i) sum += sh[i];
+    return sum;
+}
+
+// part[blockIdx.x] = the sum of squares of the block's chunks, or (norm given: the only block of
+// the only launch) the norm itself.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double *part,
+                                                                 float *norm) {
+    double sum = 0.0;
+    for (int k = blockIdx.x; k < t.first[t.count]; k += gridDim.x) {
+        const GradChunk c = grad_chunk(t, k);
+        uint4 r[kGradVecs];
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t v = c.lo + threadIdx.x + i * kGradThreads;
+            r[i] = v < c.hi ? __ldg(reinterpret_cast<const uint4 *>(c.base) + v) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            float f[8];
+            grad_values(r[i], c, c.lo + threadIdx.x + i * kGradThreads, f);
+            sum += grad_squares(f);
+        }
+    }
+    sum = grad_block_sum(sum);
     if (threadIdx.x == 0) {
-        for (int i = 1; i < kGradThreads / 32; ++i) sum += sh[i];
-        part[blockIdx.x] = sum;
+        if (norm)
+            *norm = (float)sqrt(sum);
+        else
+            part[blockIdx.x] = sum;
     }
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const double *part, int n, float *norm) {
-    __shared__ double sh[kGradThreads / 32];
     double sum = 0.0;
     for (int i = threadIdx.x; i < n; i += kGradThreads) sum += part[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kGradThreads / 32; ++i) sum += sh[i];
-        *norm = (float)sqrt(sum);
-    }
+    sum = grad_block_sum(sum);
+    if (threadIdx.x == 0) *norm = (float)sqrt(sum);
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradTable t,
+// The chunks from the last to the first: what the norm's pass read last is still in L2.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradTable<N> t,
                                                                  const float *norm, float max_norm) {
-    const float r = max_norm / (*norm + 1e-6f), f = r > 1.0f ? 1.0f : r;   // a NaN stays
-    const int64_t chunks = t.first[t.count];
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int k = grad_find(t, c);
-        if (f == 1.0f && t.out[k] == t.grad[k]) continue;
-        const int64_t lo = (c - t.first[k]) * kGradChunk, hi = min(t.numel[k], lo + kGradChunk);
-        const bool f32 = (t.f32[k >> 5] >> (k & 31)) & 1;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kGradThreads) {
-            const float g = grad_load(t.grad[k], i, f32) * f;
-            if (!QT2_STORE_OK(static_cast<uint8_t *>(t.out[k]) + i * (f32 ? 4 : 2), f32 ? 4 : 2, t.out[k],
-                              t.numel[k] * (f32 ? 4 : 2)))
+    const float q = max_norm / (*norm + 1e-6f), f = q > 1.0f ? 1.0f : q;   // a NaN stays
+    for (int k = t.first[t.count] - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
+        const GradChunk c = grad_chunk(t, k);
+        if (f == 1.0f && t.out[c.tensor] == t.grad[c.tensor]) continue;
+        // the output's address that belongs to `base`
+        uint8_t *const out = static_cast<uint8_t *>(t.out[c.tensor]) - (c.head << (c.f32 ? 2 : 1));
+        const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+        uint4 r[kGradVecs];
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t v = c.lo + threadIdx.x + i * kGradThreads;
+            r[i] = v < c.hi ? *(reinterpret_cast<const uint4 *>(c.base) + v) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int64_t v = c.lo + threadIdx.x + i * kGradThreads;
+            if (v >= c.hi) continue;
+            const int n = c.f32 ? 4 : 8;
+            const int64_t at = v * n;
+            float x[8];
+            grad_values(r[i], c, v, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= f;
+            const int64_t size = (c.end - c.head) * (c.f32 ? 4 : 2);
+            if (same && at >= c.head && at + n <= c.end) {
+                uint4 w;
+                if (c.f32) {
+                    w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                   __float_as_uint(x[3]));
+                } else {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    w = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+                if (QT2_STORE_OK(out + v * 16, 16, t.out[c.tensor], size)) *reinterpret_cast<uint4 *>(out + v * 16) = w;
                 continue;
-            if (f32)
-                static_cast<float *>(t.out[k])[i] = g;
-            else
-                static_cast<__nv_bfloat16 *>(t.out[k])[i] = __float2bfloat16_rn(g);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e >= n || at + e < c.head || at + e >= c.end) continue;
+                if (c.f32) {
+                    float *p = reinterpret_cast<float *>(out) + at + e;
+                    if (QT2_STORE_OK(p, 4, t.out[c.tensor], size)) *p = x[e];
+                } else {
+                    __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(out) + at + e;
+                    if (QT2_STORE_OK(p, 2, t.out[c.tensor], size)) *p = __float2bfloat16_rn(x[e]);
+                }
+            }
         }
     }
 }

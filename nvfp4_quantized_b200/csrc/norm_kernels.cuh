@@ -189,6 +189,7 @@ struct NormArgs {
     float *mean, *rstd;
     int64_t rows, ldx, lddy, ldy;
     int cols, w_f32;
+    int warps;           // forward: warps of a block that have rows
     float eps;
     float *part;         // [splits][2][cols]
     int splits;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
     constexpr int E = kVec<T>, P = E / 2, Q = E / 4;
     extern __shared__ float4 weights[];   // [2 (weight, bias)][Q][32 V], then B rows a warp
     __shared__ __align__(8) uint64_t full[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = a.warps;
     int64_t row = ((int64_t)blockIdx.x * warps + warp) * B;
     const int64_t stride = (int64_t)gridDim.x * warps * B;
     const uint4 *stage = reinterpret_cast<const uint4 *>(weights + 2 * Q * 32 * V) + warp * B * 32 * V;
@@ -252,12 +253,15 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
         for (int k = 0; k < n; ++k)
             bulk_load(smem_u32(stage + k * 32 * V), static_cast<const T *>(a.x) + (r + k) * a.ldx, row_bytes, bar);
     };
-    if (lane == 0) {
+    if (lane == 0 && warp < warps) {
         mbar_init(bar, 1);
         fence_mbar_init();
         issue(row);
     }
-    for (int i = threadIdx.x; i < 32 * V && i * E < a.cols; i += blockDim.x) {
+#pragma unroll
+    for (int j = 0; j < (V + 7) / 8; ++j) {   // by all of the block's threads: 256
+        const int i = (int)threadIdx.x + j * 256;
+        if (i >= 32 * V || i * E >= a.cols) continue;
         float w[E], b[E];
         load_weight(a.w, a.w_f32, i * E, a.cols, 1.0f, w);
         load_weight(a.b, a.w_f32, i * E, a.cols, 0.0f, b);
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
         }
     }
     __syncthreads();
+    if (warp >= warps) return;
     float none[2][32][B];
     uint32_t phase = 0;
     bool ok = true;   // after a wait that ran out (reported), the rest is not waited for

@@ -56,10 +56,11 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     });
     if (e == cudaSuccess) e = resident_blocks(once, blocks, layernorm_fwd_kernel<T, V, B>, 256, smem(8), &n);
     if (e != cudaSuccess) return e;
-    // fewer rows than the SMs have warps: smaller blocks spread them over more SMs
+    // fewer rows than the SMs have warps: spread over more SMs, fewer warps of a block have some
     const int64_t steps = ceil_div(a.rows, B);
-    const int warps = (int)std::min<int64_t>(8, ceil_div(steps, sm_count()));
-    layernorm_fwd_kernel<T, V, B><<<(unsigned)std::min(n, ceil_div(steps, warps)), warps * 32, smem(warps), s>>>(a);
+    NormArgs b = a;
+    b.warps = (int)std::min<int64_t>(8, ceil_div(steps, sm_count()));
+    layernorm_fwd_kernel<T, V, B><<<(unsigned)std::min(n, ceil_div(steps, b.warps)), 256, smem(b.warps), s>>>(b);
     return cudaGetLastError();
 }
 template <class T, int G>
@@ -289,7 +290,7 @@ qt2_status grad_check(const qt2_grad *g, int64_t count, bool with_out) {
     if (count <= 0 || count > (int64_t(1) << 30)) return QT2_ERR_SHAPE;
     for (int64_t i = 0; i < count; ++i) {
         if (!dtype_ok(g[i].dtype)) return QT2_ERR_INVALID_ARG;
-        if (g[i].numel < 0 || g[i].numel >= (int64_t(1) << 44)) return QT2_ERR_SHAPE;
+        if (g[i].numel < 0 || g[i].numel >= (int64_t(1) << 42)) return QT2_ERR_SHAPE;
         if (g[i].numel == 0) continue;
         if (!g[i].grad || (with_out && !g[i].out)) return QT2_ERR_INVALID_ARG;
         const uintptr_t e = g[i].dtype == QT2_DTYPE_F32 ? 4 : 2;
@@ -298,27 +299,40 @@ qt2_status grad_check(const qt2_grad *g, int64_t count, bool with_out) {
     return QT2_OK;
 }
 
+// Launches beyond one a full table that tensors of many TB add.
+int64_t grad_over(const qt2_grad *g, int64_t count) {
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) chunks += ceil_div(g[i].numel, 4 * kGradChunk) + 1;
+    return chunks / (INT32_MAX / 2);
+}
 // The next launch's tensors: fills t from g[at...], skipping empty ones; returns the next `at`.
-int64_t grad_table(GradTable &t, const qt2_grad *g, int64_t at, int64_t count) {
+template <int N>
+int64_t grad_table(GradTable<N> &t, const qt2_grad *g, int64_t at, int64_t count) {
     t.count = 0;
     std::memset(t.f32, 0, sizeof t.f32);
     t.first[0] = 0;
-    for (; at < count && t.count < kGradTable; ++at) {
+    for (; at < count && t.count < N; ++at) {
         if (g[at].numel == 0) continue;
-        const int k = t.count++;
+        const int k = t.count, esz = g[at].dtype == QT2_DTYPE_F32 ? 4 : 2;
+        const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(g[at].grad) & 15) + g[at].numel * esz;
+        const int64_t next = t.first[k] + ceil_div(bytes, 16 * kGradChunk);
+        if (next > INT32_MAX) break;   // 64 TB a launch
+        ++t.count;
         t.grad[k] = g[at].grad;
         t.out[k] = g[at].out;
         t.numel[k] = g[at].numel;
-        t.first[k + 1] = t.first[k] + ceil_div(g[at].numel, kGradChunk);
-        if (g[at].dtype == QT2_DTYPE_F32) t.f32[k >> 5] |= 1u << (k & 31);
+        t.first[k + 1] = (int32_t)next;
+        if (esz == 4) t.f32[k >> 5] |= 1u << (k & 31);
     }
     return at;
 }
-constexpr int kGradBlocks = 148 * 8;
+constexpr int kGradBlocks = 148 * 8;   // resident ones: more would not raise the bandwidth
+constexpr int kGradAlone = 8;          // chunks that one block reads faster than two launches take
 
-cudaError_t launch_grad_norm(const GradTable &t, double *part, int blocks, cudaStream_t s) {
+template <int N>
+cudaError_t launch_grad_norm(const GradTable<N> &t, double *part, float *norm, int blocks, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    grad_norm_kernel<<<blocks, kGradThreads, 0, s>>>(t, part);
+    grad_norm_kernel<N><<<blocks, kGradThreads, 0, s>>>(t, part, norm);
     return cudaGetLastError();
 }
 cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStream_t s) {
@@ -326,12 +340,41 @@ cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStr
     grad_norm_end_kernel<<<1, kGradThreads, 0, s>>>(part, n, norm);
     return cudaGetLastError();
 }
-cudaError_t launch_grad_clip(const GradTable &t, const float *norm, float max_norm, int blocks, cudaStream_t s) {
+template <int N>
+cudaError_t launch_grad_clip(const GradTable<N> &t, const float *norm, float max_norm, int blocks, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    grad_clip_kernel<<<blocks, kGradThreads, 0, s>>>(t, norm, max_norm);
+    grad_clip_kernel<N><<<blocks, kGradThreads, 0, s>>>(t, norm, max_norm);
     return cudaGetLastError();
 }
-int grad_blocks(const GradTable &t) { return (int)std::min<int64_t>(t.first[t.count], kGradBlocks); }
+template <int N>
+int grad_blocks(const GradTable<N> &t) { return std::min<int>(t.first[t.count], kGradBlocks); }
+
+template <int N>
+cudaError_t grad_norm(const qt2_grad *grads, int64_t count, float *norm, double *part, cudaStream_t s) {
+    GradTable<N> t;
+    int n = 0;
+    for (int64_t at = 0; at < count;) {
+        at = grad_table(t, grads, at, count);
+        if (t.count == 0) break;
+        const bool alone = n == 0 && at == count && t.first[t.count] <= kGradAlone;
+        const int blocks = alone ? 1 : grad_blocks(t);
+        const cudaError_t e = launch_grad_norm(t, part + n, alone ? norm : nullptr, blocks, s);
+        if (e != cudaSuccess || alone) return e;
+        n += blocks;
+    }
+    return launch_grad_norm_end(part, n, norm, s);
+}
+template <int N>
+cudaError_t grad_clip(const qt2_grad *grads, int64_t count, const float *norm, float max_norm, cudaStream_t s) {
+    GradTable<N> t;
+    for (int64_t at = 0; at < count;) {
+        at = grad_table(t, grads, at, count);
+        if (t.count == 0) break;
+        const cudaError_t e = launch_grad_clip(t, norm, max_norm, grad_blocks(t), s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 }  // namespace
 
@@ -543,7 +586,9 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
 qt2_status qt2_grad_norm_workspace_size(const qt2_grad *grads, int64_t count, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
     if (const qt2_status st = grad_check(grads, count, false)) return st;
-    *bytes = (size_t)ceil_div(count, kGradTable) * kGradBlocks * sizeof(double);
+    // a launch takes at least kGradSmall tensors, unless their chunks are more than it can count
+    *bytes = (size_t)(ceil_div(count, count <= kGradSmall ? kGradSmall : kGradLarge) + grad_over(grads, count)) *
+             kGradBlocks * sizeof(double);
     return QT2_OK;
 }
 
@@ -557,17 +602,8 @@ qt2_status qt2_grad_norm(const qt2_grad *grads, int64_t count, float *norm, void
     if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
     if (const qt2_status st = check_device()) return st;
     double *part = static_cast<double *>(workspace);
-    const cudaStream_t s = as_stream(stream);
-    int n = 0;
-    GradTable t;
-    for (int64_t at = 0; at < count;) {
-        at = grad_table(t, grads, at, count);
-        if (t.count == 0) break;
-        const int blocks = grad_blocks(t);
-        if (launch_grad_norm(t, part + n, blocks, s) != cudaSuccess) return QT2_ERR_CUDA;
-        n += blocks;
-    }
-    return from_cuda(launch_grad_norm_end(part, n, norm, s));
+    return from_cuda(count <= kGradSmall ? grad_norm<kGradSmall>(grads, count, norm, part, as_stream(stream))
+                                         : grad_norm<kGradLarge>(grads, count, norm, part, as_stream(stream)));
 }
 
 qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm, float max_norm,
@@ -577,13 +613,8 @@ qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm
     if (const qt2_status st = grad_check(grads, count, true)) return st;
     if (!aligned(norm, 4)) return QT2_ERR_ALIGN;
     if (const qt2_status st = check_device()) return st;
-    GradTable t;
-    for (int64_t at = 0; at < count;) {
-        at = grad_table(t, grads, at, count);
-        if (t.count == 0) break;
-        if (launch_grad_clip(t, norm, max_norm, grad_blocks(t), as_stream(stream)) != cudaSuccess) return QT2_ERR_CUDA;
-    }
-    return QT2_OK;
+    return from_cuda(count <= kGradSmall ? grad_clip<kGradSmall>(grads, count, norm, max_norm, as_stream(stream))
+                                         : grad_clip<kGradLarge>(grads, count, norm, max_norm, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -119,7 +119,15 @@ def _only(fn: str, dtype: torch.dtype, *tensors):
             raise QT2Error(fn, QT2_ERR_INVALID_ARG)
 
 
-_stream = qt2._stream
+# The current stream's handle; torch.cuda.current_stream() makes a Stream object for it, which takes
+# longer than a small kernel (3.4 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return qt2._stream(stream)
 
 
 # --------------------------------------------------------------------------------------------- entry points
