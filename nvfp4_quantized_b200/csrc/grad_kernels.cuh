@@ -114,6 +114,7 @@ __device__ __forceinline__ double grad_block_sum(double sum) {
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double *part,
                                                                  float *norm) {
+    grid_dependency();
     double sum = 0.0;
     for (int k = blockIdx.x; k < t.first[t.count]; k += gridDim.x) {
         const GradChunk c = grad_chunk(t, k);
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const double *part, int n, float *norm) {
+    grid_dependency();
     double sum = 0.0;
     for (int i = threadIdx.x; i < n; i += kGradThreads) sum += part[i];
     sum = grad_block_sum(sum);
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const doubl
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradTable<N> t,
                                                                  const float *norm, float max_norm) {
+    grid_dependency();
     const float q = max_norm / (*norm + 1e-6f), f = q > 1.0f ? 1.0f : q;   // a NaN stays
     for (int k = t.first[t.count] - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
         const GradChunk c = grad_chunk(t, k);

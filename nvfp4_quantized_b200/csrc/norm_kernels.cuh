@@ -256,8 +256,9 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
     if (lane == 0 && warp < warps) {
         mbar_init(bar, 1);
         fence_mbar_init();
-        issue(row);
     }
+    grid_dependency();
+    if (lane == 0 && warp < warps) issue(row);
 #pragma unroll
     for (int j = 0; j < (V + 7) / 8; ++j) {   // by all of the block's threads: 256
         const int i = (int)threadIdx.x + j * 256;
@@ -398,8 +399,10 @@ __global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(con
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
         fence_mbar_init();
-        for (int i = 0; i < S; ++i) issue(row + i * step, i);
     }
+    grid_dependency();
+    if (lane == 0)
+        for (int i = 0; i < S; ++i) issue(row + i * step, i);
     uint64_t w[V][P], b[V][P];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(con
 // ---------------------------------------------------------------------------------------------
 template <class T, int G, int V, int B>
 __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a) {
+    grid_dependency();
     constexpr int E = kVec<T>, P = E / 2, kThreads = 256, kGroups = kThreads / G;
     __shared__ float sh[2][32][2 * B];
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
@@ -657,8 +661,10 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
         fence_mbar_init();
-        for (int i = 0; i < S - 1; ++i) issue(first + i * step, i);
     }
+    grid_dependency();
+    if (lane == 0)
+        for (int i = 0; i < S - 1; ++i) issue(first + i * step, i);
     uint64_t w[V][P], dw2[V][P] = {}, db2[V][P] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -799,6 +805,7 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
 // dw (blockIdx.y = 0) or db: the sum of the partial sums, 32 columns a block, 32 slices of the
 // partial sums side by side.
 __global__ void __launch_bounds__(1024) layernorm_dw_kernel(const NormArgs a) {
+    grid_dependency();
     __shared__ float sh[32][33];
     void *out = blockIdx.y ? a.db : a.dw;
     if (!out) return;
@@ -835,6 +842,7 @@ __device__ __forceinline__ float weight_at(const void *w, int f32, int c, float 
 
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const NormArgs a) {
+    grid_dependency();
     __shared__ float sh[2][32][1];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
     T *y = static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy;
@@ -862,6 +870,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const 
 
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_dx_long_kernel(const NormArgs a) {
+    grid_dependency();
     __shared__ float sh[2][32][2];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
     const T *dy = static_cast<const T *>(a.dy) + (int64_t)blockIdx.x * a.lddy;
@@ -885,6 +894,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_dx_long_kernel(const N
 // Partial sums of dw and db over rows split, split + splits, ...: one thread a column.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_dw_long_kernel(const NormArgs a) {
+    grid_dependency();
     const int c = blockIdx.x * kNormThreads + threadIdx.x;
     if (c >= a.cols) return;
     float dw = 0.0f, db = 0.0f;

@@ -224,6 +224,16 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ------------------------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched with it may start while the one before it in the
+// stream still runs, and waits here, before its first access to global memory, until that one has
+// completed and its writes are visible; the kernel itself lets its successor start at once.
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void grid_dependency() {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------------------
 // Thread-block cluster helpers
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {

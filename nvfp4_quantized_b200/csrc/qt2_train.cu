@@ -30,6 +30,29 @@ qt2_status check_workspace(const void *ws, size_t have, size_t need) {
     return aligned(ws, kWsAlign) ? QT2_OK : QT2_ERR_ALIGN;
 }
 
+// Every kernel is launched so that its start overlaps the end of the one before it in the stream
+// (grid_dependency).
+template <class T>
+struct Same {
+    using type = T;
+};
+template <class... P>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   const typename Same<P>::type &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    void *list[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+    return cudaLaunchKernelExC(&c, reinterpret_cast<const void *>(kernel), list);
+}
+
 // ------------------------------------------------------------------------------- layer norm
 // Resident blocks of a kernel on this device, asked once a device.
 template <class F>
@@ -60,8 +83,8 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     const int64_t steps = ceil_div(a.rows, B);
     NormArgs b = a;
     b.warps = (int)std::min<int64_t>(8, ceil_div(steps, sm_count()));
-    layernorm_fwd_kernel<T, V, B><<<(unsigned)std::min(n, ceil_div(steps, b.warps)), 256, smem(b.warps), s>>>(b);
-    return cudaGetLastError();
+    return launch(layernorm_fwd_kernel<T, V, B>, (unsigned)std::min(n, ceil_div(steps, b.warps)), 256, smem(b.warps),
+                  s, b);
 }
 template <class T, int G>
 cudaError_t launch_norm_fwd_group(const NormArgs &a, cudaStream_t s) {
@@ -74,15 +97,13 @@ cudaError_t launch_norm_fwd_group(const NormArgs &a, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     const int64_t blocks = std::min<int64_t>(sm_count(), ceil_div(a.rows, kGroups));
-    layernorm_fwd_group_kernel<T, G, V>
-        <<<(unsigned)blocks, kGroups * G, kGroups * kNormAhead * norm_row_bytes<T>(a.cols), s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_fwd_group_kernel<T, G, V>, (unsigned)blocks, kGroups * G,
+                  kGroups * kNormAhead * norm_row_bytes<T>(a.cols), s, a);
 }
 template <class T>
 cudaError_t launch_norm_fwd_long(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_fwd_long_kernel<T><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_fwd_long_kernel<T>, (unsigned)a.rows, kNormThreads, 0, s, a);
 }
 template <class T>
 cudaError_t norm_fwd(const NormArgs &a, cudaStream_t s) {
@@ -127,8 +148,7 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
 template <class T, int G, int V, int B>
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_bwd_kernel<T, G, V, B><<<(unsigned)a.splits, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_bwd_kernel<T, G, V, B>, (unsigned)a.splits, 256, 0, s, a);
 }
 template <class T, int G, bool HALF, bool WHOLE>
 cudaError_t launch_norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
@@ -140,9 +160,8 @@ cudaError_t launch_norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, R::bytes(R::kColumns));
     });
     if (e != cudaSuccess) return e;
-    layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>
-        <<<(unsigned)a.splits, R::kGroups * G, R::bytes(a.cols), s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>, (unsigned)a.splits, R::kGroups * G, R::bytes(a.cols),
+                  s, a);
 }
 template <class T, int G, bool HALF>
 cudaError_t norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
@@ -151,21 +170,18 @@ cudaError_t norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
 }
 cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_dw_kernel<<<dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_dw_kernel, dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0, s, a);
 }
 template <class T>
 cudaError_t launch_norm_dx_long(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    layernorm_dx_long_kernel<T><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_dx_long_kernel<T>, (unsigned)a.rows, kNormThreads, 0, s, a);
 }
 template <class T>
 cudaError_t launch_norm_dw_long(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads), (unsigned)a.splits);
-    layernorm_dw_long_kernel<T><<<grid, kNormThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(layernorm_dw_long_kernel<T>, grid, kNormThreads, 0, s, a);
 }
 template <class T>
 cudaError_t norm_bwd(const NormArgs &a, int threads, cudaStream_t s) {
@@ -190,6 +206,7 @@ cudaError_t norm_bwd(const NormArgs &a, int threads, cudaStream_t s) {
 // The plan depends on the sizes alone, so that the workspace queries need no device: 74 pairs.
 constexpr int kPairs = 74;
 constexpr int64_t kPieceBytes = 256 << 20;   // of P
+constexpr int kJobStages = 4;                // what a tile's start and end cost, in stages of K = 64
 
 struct XentPlan {
     int64_t num_m, num_v, num_k;   // 256-wide tiles of T, V and K
@@ -206,12 +223,20 @@ XentPlan xent_plan(int64_t T, int64_t K, int64_t V) {
     p.pieces = (int)ceil_div(p.num_v, most);
     p.piece = ceil_div(p.num_v, p.pieces) * 256;
     p.pieces = (int)ceil_div(p.num_v * 256, p.piece);
-    // dx's jobs are cut along the vocabulary where whole they would outlast an even share of the
-    // launch's stages by much
+    // dx's jobs are cut along the vocabulary where that shortens the launch: the pairs' even share
+    // of its stages or the longest pair's dx jobs, and what the sums that each cut adds cost to write and read
     const int64_t nks = p.piece / 64, dx = p.num_m * p.num_k;
-    const int64_t total = dx * nks + p.piece / 256 * p.num_k * ceil_div(T, 64);
-    const int64_t share = std::max<int64_t>(16, total / (2 * kPairs));
-    p.splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, nks / share));
+    const int64_t dw = p.piece / 256 * p.num_k * (ceil_div(T, 64) + kJobStages);
+    double best = 0;
+    for (int s = 1; s <= 16 && s * 16 <= std::max<int64_t>(16, nks); ++s) {
+        const int64_t job = ceil_div(nks, s) + kJobStages;
+        const double share = (double)(dx * s * job + dw) / kPairs, longest = (double)(ceil_div(dx * s, kPairs) * job);
+        const double cost = std::max(share, longest) + (double)dx * s / 4;
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = s;
+        }
+    }
     return p;
 }
 
@@ -230,13 +255,14 @@ XentFwdWs xent_fwd_ws(const XentPlan &p, int64_t T, void *ws) {
 }
 struct XentBwdWs {
     __nv_bfloat16 *P;
-    float *acc;
+    float *acc, *top;
     size_t bytes;
 };
 XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, void *ws) {
     Carve c(ws);
     XentBwdWs w;
     w.P = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * p.piece * 2));
+    w.top = reinterpret_cast<float *>(c.take(sizeof(float)));
     w.acc = reinterpret_cast<float *>(c.take((size_t)p.splits * p.num_m * p.num_k * 65536 * sizeof(float)));
     w.bytes = c.used;
     return w;
@@ -257,23 +283,22 @@ cudaError_t launch_mm(const MmMaps &maps, const MmArgs &a, int64_t jobs, cudaStr
     });
     if (e != cudaSuccess) return e;
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(jobs, sm_count() / 2));
-    mm_pair_kernel<MODE><<<(unsigned)(2 * clusters), MmCfg::kThreads, MmCfg::kSmemBytes, s>>>(maps, a);
-    return cudaGetLastError();
+    return launch(mm_pair_kernel<MODE>, (unsigned)(2 * clusters), MmCfg::kThreads, MmCfg::kSmemBytes, s, maps, a);
 }
 
-cudaError_t launch_xent_loss(const MmArgs &a, int parts, float *loss, float *lse, cudaStream_t s) {
+cudaError_t launch_xent_loss(const MmArgs &a, int parts, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                             float *loss, float *lse, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    xent_loss_kernel<<<(unsigned)ceil_div(a.T, 32), 256, 0, s>>>(a, parts, loss, lse);
-    return cudaGetLastError();
+    return launch(xent_loss_kernel, (unsigned)ceil_div(a.T, 32), 1024, 0, s, a, parts,
+                  static_cast<const __nv_bfloat16 *>(x), ldx, static_cast<const __nv_bfloat16 *>(w), ldw, loss, lse);
 }
 
 cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     const int64_t n = (int64_t)a.T * ceil_div(a.K, 8);
     const int64_t blocks = std::min<int64_t>(ceil_div(n, 256), (int64_t)sm_count() * 16);
-    xent_dx_kernel<<<(unsigned)blocks, 256, 0, s>>>(a.acc, a.T, a.K, a.splits, (int64_t)a.dx_m * 256,
-                                                    (int64_t)a.dx_n * 256, static_cast<__nv_bfloat16 *>(dx), lddx);
-    return cudaGetLastError();
+    return launch(xent_dx_kernel, (unsigned)blocks, 256, 0, s, a.acc, a.top, a.T, a.K, a.splits,
+                  (int64_t)a.dx_m * 256, (int64_t)a.dx_n * 256, static_cast<__nv_bfloat16 *>(dx), lddx);
 }
 
 qt2_status xent_check(const void *x, const void *w, const int64_t *targets, int64_t T, int64_t K, int64_t V,
@@ -332,19 +357,16 @@ constexpr int kGradAlone = 8;          // chunks that one block reads faster tha
 template <int N>
 cudaError_t launch_grad_norm(const GradTable<N> &t, double *part, float *norm, int blocks, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    grad_norm_kernel<N><<<blocks, kGradThreads, 0, s>>>(t, part, norm);
-    return cudaGetLastError();
+    return launch(grad_norm_kernel<N>, blocks, kGradThreads, 0, s, t, part, norm);
 }
 cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    grad_norm_end_kernel<<<1, kGradThreads, 0, s>>>(part, n, norm);
-    return cudaGetLastError();
+    return launch(grad_norm_end_kernel, 1, kGradThreads, 0, s, part, n, norm);
 }
 template <int N>
 cudaError_t launch_grad_clip(const GradTable<N> &t, const float *norm, float max_norm, int blocks, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    grad_clip_kernel<N><<<blocks, kGradThreads, 0, s>>>(t, norm, max_norm);
-    return cudaGetLastError();
+    return launch(grad_clip_kernel<N>, blocks, kGradThreads, 0, s, t, norm, max_norm);
 }
 template <int N>
 int grad_blocks(const GradTable<N> &t) { return std::min<int>(t.first[t.count], kGradBlocks); }
@@ -516,7 +538,7 @@ qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targ
     a.num_n = (int)p.num_v;
     const cudaStream_t s = as_stream(stream);
     cudaError_t e = launch_mm<kLoss>(maps, a, p.num_m * p.num_v, s);
-    if (e == cudaSuccess) e = launch_xent_loss(a, 2 * a.num_n, loss, lse, s);
+    if (e == cudaSuccess) e = launch_xent_loss(a, 2 * a.num_n, x, ldx, w, ldw, loss, lse, s);
     return from_cuda(e);
 }
 
@@ -560,6 +582,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.dx_m = (int)p.num_m;
     a.dx_n = (int)p.num_k;
     a.acc = ws.acc;
+    a.top = ws.top;
     a.dw = dw;
     a.lddw = lddw;
     a.dw_f32 = dw_dtype == QT2_DTYPE_F32;
@@ -572,6 +595,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
         a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
         a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;
+        a.lead = (int)((a.vw / 64 / a.splits + kJobStages) / (ceil_div(T, 64) + kJobStages));
         if (!encode_bf16(&maps.p_k, ws.P, a.vw, T, a.vw, 128) || !encode_bf16(&maps.p_mn, ws.P, a.vw, T, a.vw, 64))
             return QT2_ERR_CUDA;
         cudaError_t e = launch_mm<kProbs>(maps, a, (int64_t)a.num_m * a.num_n, s);

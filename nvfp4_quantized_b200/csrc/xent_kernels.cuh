@@ -42,7 +42,7 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct MmCfg {
-    static constexpr int kStages = 6;
+    static constexpr int kStages = 7;
     static constexpr int kThreads = 384;
     static constexpr int kEpiWarp0 = 4;
     static constexpr int kEpiWarps = 8;
@@ -71,10 +71,12 @@ struct MmArgs {
     const float *lse, *dloss;   // kProbs
     float2 *part;          // kLoss: [2 * tiles of the vocabulary][T]
     float *hit;            // kLoss: the target's logit
+    float *top;            // kProbs writes, kGrads reads: the largest |dloss|
     __nv_bfloat16 *P;      // [T][vw]
     int num_m, num_n;      // kLoss, kProbs: tiles
     int dx_jobs, splits, dx_m, dx_n;   // kGrads: dx's jobs come first: (split, row tile, column tile)
-    int dw_jobs, add;      // add: dx's sums hold earlier pieces
+    int dw_jobs, lead;     // lead: dw jobs that a pair without an extra dx job is ahead
+    int add;               // dx's sums hold earlier pieces
     float *acc;            // [splits][256 dx_m][256 dx_n]
     void *dw;
     int64_t lddw;
@@ -87,19 +89,26 @@ struct MmJob {
     bool dw;
 };
 
+// The i-th job of pair c of `pairs`; false: it has no more.  Tiles go round the pairs in turn, so that
+// those in flight are neighbours and share operands in L2.  kGrads: dx's jobs, which are long, go
+// round first; the first dx_jobs % pairs pairs then have one more than the others, which run `lead`
+// of dw's short jobs before these join in (without it a 777-token step left pairs idle for a third of
+// the launch).
 template <int MODE>
-__device__ __forceinline__ MmJob mm_job(const MmArgs &a, int j) {
-    MmJob b;
+__device__ __forceinline__ bool mm_job(const MmArgs &a, int c, int pairs, int i, MmJob &b) {
     b.split = 0;
     b.dw = false;
     b.ks = 0;
     if (MODE != kGrads) {
         // along the tokens first: the tiles in flight then share all of x and few rows of w
+        const int j = c + i * pairs;
+        if (j >= a.num_m * a.num_n) return false;
         b.n = j / a.num_m;
         b.m = j - b.n * a.num_m;
         b.nk = (a.K + 63) >> 6;
-        return b;
+        return true;
     }
+    int j = c + i * pairs;
     if (j < a.dx_jobs) {
         const int nks = a.vw >> 6, tiles = a.dx_m * a.dx_n;
         b.split = j / tiles;
@@ -109,15 +118,21 @@ __device__ __forceinline__ MmJob mm_job(const MmArgs &a, int j) {
         const int lo = (int)((int64_t)nks * b.split / a.splits), hi = (int)((int64_t)nks * (b.split + 1) / a.splits);
         b.ks = lo;
         b.nk = hi - lo;
-        return b;
+        return true;
     }
-    j -= a.dx_jobs;
+    const int extra = a.dx_jobs % pairs;                         // pairs with one more dx job
+    const int k = i - a.dx_jobs / pairs - (c < extra ? 1 : 0);   // this pair's k-th dw job
+    if (c < extra)
+        j = a.lead * (pairs - extra) + k * pairs + c;
+    else
+        j = k < a.lead ? k * (pairs - extra) + c - extra : a.lead * (pairs - extra) + (k - a.lead) * pairs + c;
+    if (j >= a.dw_jobs) return false;
     const int nn = (a.K + 255) >> 8;
     b.dw = true;
     b.m = j / nn;
     b.n = j - b.m * nn;
     b.nk = (a.T + 63) >> 6;
-    return b;
+    return true;
 }
 
 // The row's target within the vocabulary, or -1.
@@ -126,9 +141,31 @@ __device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
     return (y == a.ignore || y < 0 || y >= a.V) ? -1 : (int)y;
 }
 
+// The largest finite |dloss| of a row with a target (1 where all are 0), the same in the epilogue's 256
+// threads.  P holds dloss as a share of it, so that equal ones (the mean of a loss) are exactly 1 there:
+// rounded to bf16 with P, one value for all rows would be off by up to 2^-8 in all of dx and dw.
+__device__ __forceinline__ float xent_top(const MmArgs &a, int thread) {
+    __shared__ float sh[8];
+    float m = 0.0f;
+    for (int t = thread; t < a.T; t += 256) {
+        const float g = fabsf(a.dloss[t]);
+        if (g < INFINITY && xent_target(a, t) >= 0) m = fmaxf(m, g);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((thread & 31) == 0) sh[thread >> 5] = m;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, sh[i]);
+    if (m == 0.0f) m = 1.0f;
+    if (thread == 0 && blockIdx.x == 0) *a.top = m;
+    return m;
+}
+
 // What becomes of a tile: the thread holds columns [col, col + 128) of the tile's row `row`.
 template <int MODE>
-__device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col) {
+__device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col,
+                                            float scale) {
     if (MODE == kLoss) {
         if (row >= a.T) return;
         const int valid = a.V - col;   // columns of the vocabulary from here on
@@ -161,7 +198,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
     } else if (MODE == kProbs) {
         if (row >= a.T) return;
         const int y = xent_target(a, row);
-        const float g = y < 0 ? 0.0f : a.dloss[row], sub = a.lse[row] * kLog2e;
+        const float g = y < 0 ? 0.0f : a.dloss[row] / scale, sub = a.lse[row] * kLog2e;
         const int at = y - (a.v0 + col), valid = a.V - (a.v0 + col);
         __nv_bfloat16 *dst = a.P + (int64_t)row * a.vw + col;
         if (!QT2_STORE_OK(dst, 256, a.P, (int64_t)a.T * a.vw * 2)) return;
@@ -214,11 +251,13 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
 #pragma unroll
             for (int i = 0; i < 128; i += 4) {
                 if (i + 4 <= n) {
-                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    *reinterpret_cast<float4 *>(dst + i) =
+                        make_float4(__uint_as_float(v[i]) * scale, __uint_as_float(v[i + 1]) * scale,
+                                    __uint_as_float(v[i + 2]) * scale, __uint_as_float(v[i + 3]) * scale);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (i + k < n) dst[i + k] = __uint_as_float(v[i + k]);
+                        if (i + k < n) dst[i + k] = __uint_as_float(v[i + k]) * scale;
                 }
             }
         } else {
@@ -230,15 +269,15 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                     uint32_t p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]),
-                                                                  __uint_as_float(v[i + 2 * k + 1]));
+                        __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]) * scale,
+                                                                  __uint_as_float(v[i + 2 * k + 1]) * scale);
                         p[k] = *reinterpret_cast<uint32_t *>(&b2);
                     }
                     *reinterpret_cast<uint4 *>(dst + i) = make_uint4(p[0], p[1], p[2], p[3]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (i + k < n) dst[i + k] = __float2bfloat16_rn(__uint_as_float(v[i + k]));
+                        if (i + k < n) dst[i + k] = __float2bfloat16_rn(__uint_as_float(v[i + k]) * scale);
                 }
             }
         }
@@ -260,7 +299,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
     const bool leader = rank == 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
-    const int jobs = MODE == kGrads ? a.dx_jobs + a.dw_jobs : a.num_m * a.num_n;
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
     const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = acc_full0 + 16;
 
@@ -283,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
     cluster_sync_all();   // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_dependency();
 
     int issued = 0;     // producer: stages whose loads were issued
     int mma_done = 0;   // MMA warp: stages whose MMAs were issued
@@ -290,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
         // -------------------------------------------------------------- producer (both CTAs)
         const uint32_t full_leader0 = mapa_shared(full0, 0);
         bool ok = true;
-        for (int j = cluster_id; j < jobs && ok; j += num_clusters) {
-            const MmJob b = mm_job<MODE>(a, j);
+        MmJob b;
+        for (int j = 0; ok && mm_job<MODE>(a, cluster_id, num_clusters, j, b); ++j) {
             const int am = b.m * 256 + (int)rank * 128, bn = b.n * 256 + (int)rank * 128;
             for (int ks = b.ks; ks < b.ks + b.nk; ++ks) {
                 const int it = issued, s = it % S;
@@ -328,9 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
         // groups 1 KB apart, a K = 16 step 32 bytes on.  MN-major: 64 (m or n) a 128-byte line,
         // one line a k, 8-k groups 1 KB apart, the next 64 (m or n) 8 KB on, a K = 16 step 2 KB on.
         bool ok = true;
-        int t_iter = 0;
-        for (int j = cluster_id; j < jobs && ok; j += num_clusters, ++t_iter) {
-            const MmJob b = mm_job<MODE>(a, j);
+        MmJob b;
+        for (int t_iter = 0; ok && mm_job<MODE>(a, cluster_id, num_clusters, t_iter, b); ++t_iter) {
             const int buf = t_iter & 1;
             if (t_iter >= 2 && !mbar_wait_warp(acc_empty0 + 8 * buf, ((t_iter >> 1) & 1) ^ 1)) break;
             tc_fence_after();
@@ -369,9 +407,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
         const int quad = warp & 3, ew = warp - Cfg::kEpiWarp0;
         const int cb = (ew >> 2) * 128;
         const uint32_t acc_empty_leader0 = mapa_shared(acc_empty0, 0);
-        int t_iter = 0;
-        for (int j = cluster_id; j < jobs; j += num_clusters, ++t_iter) {
-            const MmJob b = mm_job<MODE>(a, j);
+        float scale = 1.0f;   // kProbs, kGrads: the largest |dloss|
+        if (MODE == kProbs) scale = xent_top(a, threadIdx.x - 32 * Cfg::kEpiWarp0);
+        if (MODE == kGrads) scale = *a.top;
+        MmJob b;
+        for (int t_iter = 0; mm_job<MODE>(a, cluster_id, num_clusters, t_iter, b); ++t_iter) {
             const int buf = t_iter & 1;
             if (!mbar_wait_warp(acc_full0 + 8 * buf, (t_iter >> 1) & 1)) break;
             tc_fence_after();
@@ -386,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
-            mm_epilogue<MODE>(a, b, v, row, col);
+            mm_epilogue<MODE>(a, b, v, row, col, scale);
             __syncwarp();
         }
     }
@@ -414,41 +454,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, Cfg::kTmemCols);
 }
 
-// loss and lse from the tiles' (max, sum) pairs: lse = M + log sum_i s_i exp(m_i - M).  A block
-// takes 32 rows; its 8 warps share the pairs.
-__global__ void __launch_bounds__(256) xent_loss_kernel(const MmArgs a, int parts, float *loss, float *lse) {
-    const int t = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-    __shared__ float2 sh[8][32];
+// loss and lse from the tiles' (max, sum) pairs: lse = M + log sum_i s_i exp(m_i - M).  A block takes
+// 32 rows; its 32 warps share the pairs.  Then a warp a row forms the target's logit h again, in
+// fp32 with short sums: the tensor cores' long ones lose up to 1e-5 of it (K = 4096), which the loss
+// of a row that expects its target otherwise shows in full.  lse takes the exact h in the place of the
+// tile's h' too: lse + log(1 + exp(h' - lse) (exp(h - h') - 1)).
+__global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int parts, const __nv_bfloat16 *x, int64_t ldx,
+                                                         const __nv_bfloat16 *w, int64_t ldw, float *loss, float *lse) {
+    grid_dependency();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * 32 + lane;
+    __shared__ float2 sh[32][33];
     float m = -INFINITY, s = 0.0f;
     if (t < a.T) {
-        for (int i = slice; i < parts; i += 8) {
-            const float2 p = a.part[(int64_t)i * a.T + t];
-            const float n = fmaxf(m, p.x), ref = n == -INFINITY ? 0.0f : n;
-            s = s * __expf(m - ref) + p.y * __expf(p.x - ref);
+        for (int i = warp; i < parts; i += 4 * 32) {
+            float2 p[4];
+            float n = m;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                p[k] = i + 32 * k < parts ? a.part[(int64_t)(i + 32 * k) * a.T + t] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) n = fmaxf(n, p[k].x);
+            const float ref = n == -INFINITY ? 0.0f : n;
+            s *= __expf(m - ref);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s += p[k].y * __expf(p[k].x - ref);
             m = n;
         }
     }
-    sh[slice][threadIdx.x & 31] = make_float2(m, s);
+    sh[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (slice != 0 || t >= a.T) return;
-    float top = m;
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, sh[i][threadIdx.x].x);
+    const int row = blockIdx.x * 32 + warp;
+    if (row >= a.T) return;
+    const float2 p = sh[lane][warp];
+    float top = p.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    for (int i = 0; i < 8; ++i) sum += sh[i][threadIdx.x].y * __expf(sh[i][threadIdx.x].x - ref);
-    const float l = ref + logf(sum);
-    lse[t] = l;
-    const int64_t y = a.targets[t];
-    const int in = xent_target(a, t);
-    if (in < 0 && y != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
-    loss[t] = in < 0 ? 0.0f : l - a.hit[t];
+    float sum = p.y * __expf(p.x - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    float l = ref + logf(sum), out = 0.0f;
+    const int in = xent_target(a, row);
+    if (in >= 0) {
+        const __nv_bfloat16 *xr = x + (int64_t)row * ldx, *wr = w + (int64_t)in * ldw;
+        float h = 0.0f;
+        for (int k = lane * 8; k < a.K; k += 256) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(xr + k), v = *reinterpret_cast<const uint4 *>(wr + k);
+            const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+            float d = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (k + 2 * e < a.K) d = fmaf(bf16_lo(uw[e]), bf16_lo(vw[e]), d);
+                if (k + 2 * e + 1 < a.K) d = fmaf(bf16_hi(uw[e]), bf16_hi(vw[e]), d);
+            }
+            h += d;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
+        const float tile = a.hit[row], off = h - tile;
+        if (fabsf(off) < 1.0f) l += log1pf(__expf(tile - l) * expm1f(off));   // not for inf and NaN
+        out = l - h;
+    } else if (lane == 0 && a.targets[row] != a.ignore) {
+        set_device_error(QT2_ERR_INVALID_ARG);
+    }
+    if (lane == 0) {
+        lse[row] = l;
+        loss[row] = out;
+    }
 }
 
-// dx = the sum of the splits' fp32 sums, rounded to bf16.  One thread takes 8 columns of a row.
-__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, int T, int K, int splits, int64_t rows,
+// dx = the sum of the splits' fp32 sums times the largest |dloss|, rounded to bf16.  One thread takes 8 columns of a row.
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const float *top, int T, int K, int splits, int64_t rows,
                                                       int64_t ld, __nv_bfloat16 *dx, int64_t lddx) {
+    grid_dependency();
     const int vecs = (K + 7) >> 3;
     const int64_t n = (int64_t)T * vecs;
+    const float scale = *top;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t t = i / vecs;
         const int c = (int)(i - t * vecs) * 8;
@@ -459,6 +541,8 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, int T, i
             v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
             v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= scale;
         __nv_bfloat16 *dst = dx + t * lddx + c;
         const int valid = min(8, K - c);
         if (!QT2_STORE_OK(dst, valid * 2, dx, ((int64_t)(T - 1) * lddx + K) * 2)) continue;
