@@ -10,6 +10,9 @@
 //   kLoss   A = x, B = w rows; the tile of logits becomes one (max, sum of exp) pair a row and
 //           128 columns, and the target's logit where the tile holds it.
 //   kProbs  the same tile becomes the bf16 entries of P for one piece of the vocabulary.
+//           Fewer than 32 tokens (SWAP): A = w rows, B = x; a thread then holds one vocabulary entry of
+//           every token.  With so few rows of x as A, every pair's loads of a stage meet in the same few
+//           L2 lines (32000 x 2048: 44 us for 1 token, 38 us for 16, 32 us for 32; swapped 28, 32 and 35).
 //   kGrads  jobs of both gradient products in one launch: dx (A = P, B = w with the vocabulary
 //           contracted, so w is read transposed: an MN-major operand) added up over the pieces in
 //           fp32, and dw (A = P transposed, B = x transposed), whose rows are complete after their
@@ -20,6 +23,7 @@
 
 #include "qt2_device.cuh"
 #include "qt2_pair.cuh"
+#include "vec_device.cuh"
 
 namespace qt2 {
 
@@ -41,18 +45,21 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kSwapN = 32;   // SWAP: its tiles' columns, the least that a pair's MMA takes
+template <bool SWAP>
 struct MmCfg {
-    static constexpr int kStages = 7;
+    static constexpr int kStages = SWAP ? 11 : 7;
     static constexpr int kThreads = 384;
     static constexpr int kEpiWarp0 = 4;
     static constexpr int kEpiWarps = 8;
     static constexpr int kA = 128 * 64 * 2;   // own 128 rows of A, K = 64
-    static constexpr int kB = 128 * 64 * 2;   // own half of the 256 rows of B
+    static constexpr int kN = SWAP ? kSwapN : 256;
+    static constexpr int kB = kN / 2 * 64 * 2;   // own half of B's rows
     static constexpr int kStageBytes = kA + kB;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 512;
     static constexpr int kTmemCols = 512;     // two 256-column accumulators
-    // fp32 sums, bf16 A and B, M = 256 (pair), N = 256; bits 15 / 16: A / B is MN-major
-    static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (16u << 24);
+    // fp32 sums, bf16 A and B, M = 256 (pair), N = kN; bits 15 / 16: A / B is MN-major
+    static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kN / 8) << 17) | (16u << 24);
     static constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 };
 
@@ -70,17 +77,19 @@ struct MmArgs {
     int64_t ignore;
     const float *lse, *dloss;   // kProbs
     float2 *part;          // kLoss: [2 * tiles of the vocabulary][T]
-    float *hit;            // kLoss: the target's logit
+    const __nv_bfloat16 *x, *w;   // kLoss, for the targets' logits
+    int64_t ldx, ldw;
+    float *hit, *exact;    // kLoss: the target's logit as the tile has it, and formed in fp32
     float *top;            // kProbs writes, kGrads reads: the largest |dloss|
     __nv_bfloat16 *P;      // [T][vw]
-    int num_m, num_n;      // kLoss, kProbs: tiles
+    int num_m, num_n;      // kLoss, kProbs: tiles of the tokens and of the vocabulary
     int dx_jobs, splits, dx_m, dx_n;   // kGrads: dx's jobs come first: (split, row tile, column tile)
     int dw_jobs, lead;     // lead: dw jobs that a pair without an extra dx job is ahead
     int add;               // dx's sums hold earlier pieces
     float *acc;            // [splits][256 dx_m][256 dx_n]
     void *dw;
     int64_t lddw;
-    int dw_f32;
+    int dw_f32, dw_wide;   // dw_wide: its rows start 32-byte aligned
 };
 
 // One job: its tile, and the stages [ks, ks + nk) of its contraction.
@@ -139,6 +148,34 @@ __device__ __forceinline__ bool mm_job(const MmArgs &a, int c, int pairs, int i,
 __device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
     const int64_t y = a.targets[t];
     return (y == a.ignore || y < 0 || y >= a.V) ? -1 : (int)y;
+}
+
+// The target's logit again, in fp32 with short sums, by one warp: the tensor cores' long ones lose up
+// to 1e-5 of it (K = 4096), which the loss of a row that expects its target otherwise shows in full.
+__device__ __forceinline__ void xent_exact(const MmArgs &a, int64_t t, int y, int lane) {
+    const __nv_bfloat16 *x = a.x + t * a.ldx, *w = a.w + (int64_t)y * a.ldw;
+    float h = 0.0f;
+#pragma unroll 4
+    for (int k = lane * 8; k < a.K; k += 256) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(x + k), v = *reinterpret_cast<const uint4 *>(w + k);
+        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        float d = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k + 2 * e < a.K) d = fmaf(bf16_lo(uw[e]), bf16_lo(vw[e]), d);
+            if (k + 2 * e + 1 < a.K) d = fmaf(bf16_hi(uw[e]), bf16_hi(vw[e]), d);
+        }
+        h += d;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
+    if (lane == 0) a.exact[t] = h;
+}
+
+// Two (max, sum of exp) pairs as one.
+__device__ __forceinline__ float2 xent_join(const float2 &p, const float2 &q) {
+    const float m = fmaxf(p.x, q.x), ref = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, p.y * __expf(p.x - ref) + q.y * __expf(q.x - ref));
 }
 
 // The largest finite |dloss| of a row with a target (1 where all are 0), the same in the epilogue's 256
@@ -249,45 +286,139 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
             float *dst = static_cast<float *>(a.dw) + r * a.lddw + col;
             if (!QT2_STORE_OK(dst, n * 4, a.dw, extent * 4)) return;
 #pragma unroll
-            for (int i = 0; i < 128; i += 4) {
-                if (i + 4 <= n) {
-                    *reinterpret_cast<float4 *>(dst + i) =
-                        make_float4(__uint_as_float(v[i]) * scale, __uint_as_float(v[i + 1]) * scale,
-                                    __uint_as_float(v[i + 2]) * scale, __uint_as_float(v[i + 3]) * scale);
-                } else {
+            for (int i = 0; i < 128; i += 8) {
+                if (a.dw_wide && i + 8 <= n) {
+                    uint32_t p[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (i + k < n) dst[i + k] = __uint_as_float(v[i + k]) * scale;
+                    for (int k = 0; k < 8; ++k) p[k] = __float_as_uint(__uint_as_float(v[i + k]) * scale);
+                    st_global_v8(dst + i, p);
+                    continue;
+                }
+#pragma unroll
+                for (int j = i; j < i + 8; j += 4) {
+                    if (j + 4 <= n) {
+                        float f[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[j + k]) * scale;
+                        *reinterpret_cast<uint4 *>(dst + j) = pack(f);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (j + k < n) dst[j + k] = __uint_as_float(v[j + k]) * scale;
+                    }
                 }
             }
         } else {
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dw) + r * a.lddw + col;
             if (!QT2_STORE_OK(dst, n * 2, a.dw, extent * 2)) return;
 #pragma unroll
-            for (int i = 0; i < 128; i += 8) {
-                if (i + 8 <= n) {
-                    uint32_t p[4];
+            for (int i = 0; i < 128; i += 16) {
+                if (a.dw_wide && i + 16 <= n) {
+                    uint32_t p[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]) * scale,
                                                                   __uint_as_float(v[i + 2 * k + 1]) * scale);
                         p[k] = *reinterpret_cast<uint32_t *>(&b2);
                     }
-                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(p[0], p[1], p[2], p[3]);
-                } else {
+                    st_global_v8(dst + i, p);
+                    continue;
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (i + k < n) dst[i + k] = __float2bfloat16_rn(__uint_as_float(v[i + k]) * scale);
+                for (int j = i; j < i + 16; j += 8) {
+                    if (j + 8 <= n) {
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[j + k]) * scale;
+                        *reinterpret_cast<uint4 *>(dst + j) = pack(f);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (j + k < n) dst[j + k] = __float2bfloat16_rn(__uint_as_float(v[j + k]) * scale);
+                    }
                 }
             }
         }
     }
 }
 
+// SWAP: what a token's column needs, for the epilogue's threads: its target, and for kProbs lse and
+// dloss as a share of the largest.
+struct SwapToken {
+    int y;
+    float sub, g;
+};
+__device__ __forceinline__ SwapToken *swap_table() {
+    __shared__ SwapToken tokens[kSwapN];
+    return tokens;
+}
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
+__device__ __forceinline__ void swap_tokens(const MmArgs &a, int thread, float top) {
+    if (thread < kSwapN) {
+        SwapToken t{-1, 0.0f, 0.0f};
+        if (thread < a.T) {
+            t.y = xent_target(a, thread);
+            if (MODE == kProbs) {
+                t.sub = a.lse[thread] * kLog2e;
+                t.g = t.y < 0 ? 0.0f : a.dloss[thread] / top;
+            }
+        }
+        swap_table()[thread] = t;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// The epilogue with w's rows as the tile's rows: the thread has vocabulary entry `v` of the piece, for
+// 16 tokens from `first` on.  kLoss: the warp's 32 entries join the (max, sum of exp) that lane k keeps
+// for token first + k.  kProbs: 32 neighbours of a row of P a store.
+template <int MODE>
+__device__ __forceinline__ void swap_epilogue(const MmArgs &a, int v, int first, uint32_t taddr, int lane,
+                                              float2 &sum) {
+    const bool in = a.v0 + v < a.V;
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(taddr + first, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int t = first + k;
+        if (t >= a.T) continue;
+        const SwapToken token = swap_table()[t];
+        const float l = in ? __uint_as_float(r[k]) : -INFINITY;
+        if (MODE == kLoss) {
+            float m = l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float ref = m == -INFINITY ? 0.0f : m;
+            float s = ex2(fmaf(l, kLog2e, -ref * kLog2e));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (lane == k) sum = xent_join(sum, make_float2(m, s));
+            if (v == token.y) a.hit[t] = l;
+        } else {
+            float e = ex2(fmaf(l, kLog2e, -token.sub)) - (a.v0 + v == token.y ? 1.0f : 0.0f);
+            e = token.y < 0 || !in ? 0.0f : e * token.g;
+            __nv_bfloat16 *dst = a.P + (int64_t)t * a.vw + v;
+            if (QT2_STORE_OK(dst, 2, a.P, (int64_t)a.T * a.vw * 2)) *dst = __float2bfloat16_rn(e);
+        }
+    }
+}
+// kLoss: the four lane quadrants' sums together, one pair a token and block.
+__device__ __forceinline__ void swap_finish(const MmArgs &a, int ew, int lane, const float2 &sum) {
+    __shared__ float2 sh[4][kSwapN];
+    const int t = (ew >> 2) * 16 + lane;
+    if (lane < 16) sh[ew & 3][t] = sum;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if ((ew & 3) != 0 || lane >= 16 || t >= a.T) return;
+    float2 p = sh[0][t];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) p = xent_join(p, sh[q][t]);
+    a.part[(int64_t)blockIdx.x * a.T + t] = p;
+}
+
+template <int MODE, bool SWAP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThreads, 1)
     mm_pair_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
-    using Cfg = MmCfg;
+    using Cfg = MmCfg<SWAP>;
     constexpr int S = Cfg::kStages;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -343,7 +474,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
                 const int k = ks * 64;
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * Cfg::kStageBytes);
-                    if (MODE != kGrads) {
+                    if (SWAP) {
+                        tma_load_2d_pair(st, &maps.w_k, k, a.v0 + bn, fb);
+                        tma_load_2d_pair(st + Cfg::kA, &maps.x_k, k, (int)rank * (kSwapN / 2), fb);
+                    } else if (MODE != kGrads) {
                         tma_load_2d_pair(st, &maps.x_k, k, am, fb);
                         tma_load_2d_pair(st + Cfg::kA, &maps.w_k, k, a.v0 + bn, fb);
                     } else if (!b.dw) {
@@ -400,6 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
                 __syncwarp();
             }
         }
+    } else if (MODE == kLoss && (warp == 2 || warp == 3)) {
+        // -------------------------------------------------------------- the targets' logits, a warp a row
+        for (int64_t t = (int64_t)blockIdx.x * 2 + (warp & 1); t < a.T; t += (int64_t)gridDim.x * 2) {
+            const int y = xent_target(a, t);
+            if (y >= 0) xent_exact(a, t, y, lane);
+        }
     } else if (warp >= Cfg::kEpiWarp0) {
         // -------------------------------------------------------------- epilogue (both CTAs)
         // Warp w reads TMEM lane quadrant w % 4, columns [0, 128) for warps 4..7 and [128, 256)
@@ -409,12 +549,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
         const uint32_t acc_empty_leader0 = mapa_shared(acc_empty0, 0);
         float scale = 1.0f;   // kProbs, kGrads: the largest |dloss|
         if (MODE == kProbs) scale = xent_top(a, threadIdx.x - 32 * Cfg::kEpiWarp0);
+        if constexpr (SWAP) swap_tokens<MODE>(a, threadIdx.x - 32 * Cfg::kEpiWarp0, scale);
         if (MODE == kGrads) scale = *a.top;
+        float2 sum = make_float2(-INFINITY, 0.0f);   // SWAP, kLoss: lane k's token (ew >> 2) * 16 + k so far
         MmJob b;
         for (int t_iter = 0; mm_job<MODE>(a, cluster_id, num_clusters, t_iter, b); ++t_iter) {
             const int buf = t_iter & 1;
             if (!mbar_wait_warp(acc_full0 + 8 * buf, (t_iter >> 1) & 1)) break;
             tc_fence_after();
+            if constexpr (SWAP) {
+                swap_epilogue<MODE>(a, b.n * 256 + (int)rank * 128 + quad * 32 + lane, (ew >> 2) * 16,
+                                    tmem + ((uint32_t)(quad * 32) << 16) + 256 * buf, lane, sum);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
+                continue;
+            }
             const int row = b.m * 256 + (int)rank * 128 + quad * 32 + lane;
             const int col = b.n * 256 + cb;
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + 256 * buf + cb;
@@ -429,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
             mm_epilogue<MODE>(a, b, v, row, col, scale);
             __syncwarp();
         }
+        if constexpr (SWAP && MODE == kLoss) swap_finish(a, ew, lane, sum);
     }
     // Every role ends converged.  Only after a timeout can work still be in flight: the leader
     // waits (bounded) for the loads it issued past the last consumed stage and for the last
@@ -455,37 +606,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg::kThreads, 1)
 }
 
 // loss and lse from the tiles' (max, sum) pairs: lse = M + log sum_i s_i exp(m_i - M).  A block takes
-// 32 rows; its 32 warps share the pairs.  Then a warp a row forms the target's logit h again, in
-// fp32 with short sums: the tensor cores' long ones lose up to 1e-5 of it (K = 4096), which the loss
-// of a row that expects its target otherwise shows in full.  lse takes the exact h in the place of the
+// 32 rows; its 32 warps share the pairs.  lse takes the target's exact logit h in the place of the
 // tile's h' too: lse + log(1 + exp(h' - lse) (exp(h - h') - 1)).
-__global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int parts, const __nv_bfloat16 *x, int64_t ldx,
-                                                         const __nv_bfloat16 *w, int64_t ldw, float *loss, float *lse) {
+__global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int parts, float *loss, float *lse) {
     grid_dependency();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * 32 + lane;
+    const int t = blockIdx.x * 32 + lane, row = blockIdx.x * 32 + warp;
     __shared__ float2 sh[32][33];
+    // the row's own values, on their way while the pairs are read
+    const bool live = row < a.T;
+    const int in = live ? xent_target(a, row) : -1;
+    const float tile = in >= 0 ? a.hit[row] : 0.0f, exact = in >= 0 ? a.exact[row] : 0.0f;
     float m = -INFINITY, s = 0.0f;
     if (t < a.T) {
-        for (int i = warp; i < parts; i += 4 * 32) {
-            float2 p[4];
+        for (int i = warp; i < parts; i += 8 * 32) {
+            float2 p[8];
             float n = m;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
                 p[k] = i + 32 * k < parts ? a.part[(int64_t)(i + 32 * k) * a.T + t] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) n = fmaxf(n, p[k].x);
+            for (int k = 0; k < 8; ++k) n = fmaxf(n, p[k].x);
             const float ref = n == -INFINITY ? 0.0f : n;
             s *= __expf(m - ref);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s += p[k].y * __expf(p[k].x - ref);
+            for (int k = 0; k < 8; ++k) s += p[k].y * __expf(p[k].x - ref);
             m = n;
         }
     }
     sh[warp][lane] = make_float2(m, s);
     __syncthreads();
-    const int row = blockIdx.x * 32 + warp;
-    if (row >= a.T) return;
+    if (!live) return;
     const float2 p = sh[lane][warp];
     float top = p.x;
 #pragma unroll
@@ -494,34 +645,13 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int par
     float sum = p.y * __expf(p.x - ref);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    float l = ref + logf(sum), out = 0.0f;
-    const int in = xent_target(a, row);
-    if (in >= 0) {
-        const __nv_bfloat16 *xr = x + (int64_t)row * ldx, *wr = w + (int64_t)in * ldw;
-        float h = 0.0f;
-        for (int k = lane * 8; k < a.K; k += 256) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(xr + k), v = *reinterpret_cast<const uint4 *>(wr + k);
-            const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-            float d = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (k + 2 * e < a.K) d = fmaf(bf16_lo(uw[e]), bf16_lo(vw[e]), d);
-                if (k + 2 * e + 1 < a.K) d = fmaf(bf16_hi(uw[e]), bf16_hi(vw[e]), d);
-            }
-            h += d;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
-        const float tile = a.hit[row], off = h - tile;
-        if (fabsf(off) < 1.0f) l += log1pf(__expf(tile - l) * expm1f(off));   // not for inf and NaN
-        out = l - h;
-    } else if (lane == 0 && a.targets[row] != a.ignore) {
-        set_device_error(QT2_ERR_INVALID_ARG);
-    }
-    if (lane == 0) {
-        lse[row] = l;
-        loss[row] = out;
-    }
+    if (lane != 0) return;
+    float l = ref + logf(sum);
+    const float off = exact - tile;
+    if (in >= 0 && fabsf(off) < 1.0f) l += log1pf(__expf(tile - l) * expm1f(off));   // not for inf and NaN
+    lse[row] = l;
+    loss[row] = in >= 0 ? l - exact : 0.0f;
+    if (in < 0 && a.targets[row] != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
 }
 
 // dx = the sum of the splits' fp32 sums times the largest |dloss|, rounded to bf16.  One thread takes 8 columns of a row.

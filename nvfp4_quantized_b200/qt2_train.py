@@ -89,33 +89,27 @@ def _check(fn: str, status: int):
 def _ptrs(fn: str, *tensors):
     """Device pointers of tensors (None stays None); all of them on the current device."""
     dev = torch.cuda.current_device()
-    out = []
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
+        if t is not None and t.get_device() != dev:
             raise QT2Error(fn, QT2_ERR_DEVICE)
-        out.append(t.data_ptr())
-    return out
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _dtype(fn: str, *tensors) -> int:
     """The common element type of tensors (None is skipped); QT2_DTYPE_BF16 if there is none."""
     found = None
     for t in tensors:
-        if t is None:
+        if t is None or t.dtype is found:
             continue
-        d = _DTYPE.get(t.dtype)
-        if d is None or found not in (None, d):
+        if found is not None or t.dtype not in _DTYPE:
             raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-        found = d
-    return QT2_DTYPE_BF16 if found is None else found
+        found = t.dtype
+    return QT2_DTYPE_BF16 if found is None else _DTYPE[found]
 
 
 def _only(fn: str, dtype: torch.dtype, *tensors):
     for t in tensors:
-        if t is not None and t.dtype != dtype:
+        if t is not None and t.dtype is not dtype:
             raise QT2Error(fn, QT2_ERR_INVALID_ARG)
 
 
