@@ -17,7 +17,7 @@ namespace qt2 {
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 8;
 constexpr int kGradChunk = kGradThreads * kGradVecs;   // vectors a block takes at a time: 32 KB
-constexpr int kGradSmall = 32, kGradLarge = 512;       // tensors a launch's parameters hold
+constexpr int kGradSmall = 32, kGradMiddle = 256, kGradLarge = 1024;   // tensors a launch's parameters hold
 
 template <int N>
 struct GradTable {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const doubl
 
 // The chunks from the last to the first: what the norm's pass read last is still in L2.
 template <int N>
-__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradTable<N> t,
+__global__ void __launch_bounds__(kGradThreads, 3) grad_clip_kernel(const __grid_constant__ GradTable<N> t,
                                                                  const float *norm, float max_norm) {
     grid_dependency();
     const float q = max_norm / (*norm + 1e-6f), f = q > 1.0f ? 1.0f : q;   // a NaN stays

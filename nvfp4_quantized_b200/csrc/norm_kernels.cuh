@@ -173,6 +173,7 @@ struct NormArgs {
     int64_t rows, ldx, lddy, ldy;
     int cols, w_f32;
     int warps;           // forward: warps of a block that have rows
+    int slots;           // forward, groups of threads: rows on their way
     float eps;
     float *part;         // [splits][2][cols]
     int splits;
@@ -358,19 +359,21 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
 }
 
 // ---------------------------------------------------------------------------------------------
-// Forward, longer rows: a group of G threads a row, V vectors a thread, whose weights and biases stay
-// in registers; the next row comes by bulk copy while this one, in registers, is worked on.
+// Forward, longer rows: a group of G threads a row, V vectors a thread, one block of 1024 threads an SM.
+// Bulk copies bring the next rows into the group's `slots` in shared memory while this one, in
+// registers, is worked on.  Weights and biases: in registers where a thread has 16 columns (HOLD), else
+// in shared memory, once a block, as in layernorm_fwd_kernel.
 // ---------------------------------------------------------------------------------------------
-constexpr int kNormAhead = 3;   // rows on their way to a group, next to the one in registers
-template <class T, int G, int V>
-__global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(const NormArgs a) {
-    constexpr int E = kVec<T>, P = E / 2, kGroups = 1024 / G, S = kNormAhead;
-    extern __shared__ __align__(16) uint8_t rows_all[];   // [groups][S][row]
+template <class T, int G, int V, bool HOLD>
+__global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const NormArgs a) {
+    constexpr int E = kVec<T>, P = E / 2, Q = E / 4, kGroups = 1024 / G, kMost = 3;
+    extern __shared__ float4 weights[];   // !HOLD: [2 (weight, bias)][Q][G V]; then [groups][slots][row]
     __shared__ float sh_all[kGroups][2][32][1];
-    __shared__ __align__(8) uint64_t full_all[kGroups][S];
-    const int cols = a.cols, row_bytes = norm_row_bytes<T>(cols);
+    __shared__ __align__(8) uint64_t full_all[kGroups][kMost];
+    const int cols = a.cols, row_bytes = norm_row_bytes<T>(cols), slots = a.slots;
     const int group = threadIdx.x / G, lane = threadIdx.x % G, bar = group + 1;
-    const uint8_t *const ring = rows_all + (size_t)group * S * row_bytes;
+    const uint8_t *const ring =
+        reinterpret_cast<const uint8_t *>(weights + (HOLD ? 0 : 2 * Q * G * V)) + (size_t)group * slots * row_bytes;
     const uint32_t full0 = smem_u32(full_all[group]);
     const int64_t step = (int64_t)gridDim.x * kGroups;
     int64_t row = (int64_t)blockIdx.x * kGroups + group;
@@ -380,23 +383,38 @@ __global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(con
         bulk_load(smem_u32(ring + st * row_bytes), static_cast<const T *>(a.x) + r * a.ldx, row_bytes, full0 + 8 * st);
     };
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < slots; ++i) mbar_init(full0 + 8 * i, 1);
         fence_mbar_init();
     }
     grid_dependency();
     if (lane == 0)
-        for (int i = 0; i < S; ++i) issue(row + i * step, i);
-    uint64_t w[V][P], b[V][P];
+        for (int i = 0; i < slots; ++i) issue(row + i * step, i);
+    uint64_t w[HOLD ? V : 1][P], b[HOLD ? V : 1][P];
+    auto pairs = [&](const float (&f)[E], uint64_t (&p)[P]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (lane + i * G) * E;
-        float f[E];
-        load_weight(c < cols ? a.w : nullptr, a.w_f32, c, cols, 1.0f, f);
+        for (int e = 0; e < P; ++e) p[e] = f2(f[2 * e], f[2 * e + 1]);
+    };
+    if constexpr (HOLD) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) w[i][e] = f2(f[2 * e], f[2 * e + 1]);
-        load_weight(c < cols ? a.b : nullptr, a.w_f32, c, cols, 0.0f, f);
+        for (int i = 0; i < V; ++i) {
+            const int c = (lane + i * G) * E;
+            float f[E];
+            load_weight(c < cols ? a.w : nullptr, a.w_f32, c, cols, 1.0f, f);
+            pairs(f, w[i]);
+            load_weight(c < cols ? a.b : nullptr, a.w_f32, c, cols, 0.0f, f);
+            pairs(f, b[i]);
+        }
+    } else {
+        for (int i = threadIdx.x; i < G * V && i * E < cols; i += 1024) {
+            float f[E], g[E];
+            load_weight(a.w, a.w_f32, i * E, cols, 1.0f, f);
+            load_weight(a.b, a.w_f32, i * E, cols, 0.0f, g);
 #pragma unroll
-        for (int e = 0; e < P; ++e) b[i][e] = f2(f[2 * e], f[2 * e + 1]);
+            for (int q = 0; q < Q; ++q) {
+                weights[q * G * V + i] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                weights[(Q + q) * G * V + i] = make_float4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+            }
+        }
     }
     __syncthreads();
     int st = 0, phase = 0;
@@ -416,9 +434,9 @@ __global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(con
         }
         float s[1] = {f2_sum(s2)};
         row_sum<G>(s, sh_all[group], 0, bar);
-        // every thread has the row in registers: its slot takes the one S on
-        if (lane == 0 && ok) issue(row + S * step, st);
-        if (++st == S) {
+        // every thread has the row in registers: its slot takes the one `slots` on
+        if (lane == 0 && ok) issue(row + slots * step, st);
+        if (++st == slots) {
             st = 0;
             phase ^= 1;
         }
@@ -457,8 +475,19 @@ __global__ void __launch_bounds__(1024 / G *G, 1) layernorm_fwd_group_kernel(con
             uint64_t v[P];
             repack(raw[i]);
             pairs_of<T>(raw[i], v);
+            if constexpr (!HOLD) {
 #pragma unroll
-            for (int e = 0; e < P; ++e) v[e] = f2_fma(f2_mul(f2_add(v[e], neg), r2), w[i][e], b[i][e]);
+                for (int q = 0; q < Q; ++q) {
+                    const float4 p = weights[q * G * V + lane + i * G], r = weights[(Q + q) * G * V + lane + i * G];
+                    w[0][2 * q] = f2(p.x, p.y);
+                    w[0][2 * q + 1] = f2(p.z, p.w);
+                    b[0][2 * q] = f2(r.x, r.y);
+                    b[0][2 * q + 1] = f2(r.z, r.w);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                v[e] = f2_fma(f2_mul(f2_add(v[e], neg), r2), w[HOLD ? i : 0][e], b[HOLD ? i : 0][e]);
             float o[E];
             floats_of<E>(v, o);
             store_row(static_cast<T *>(a.y) + row * a.ldy, c, cols, o, a.y, (a.rows - 1) * a.ldy + cols);

@@ -86,19 +86,24 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     return launch(layernorm_fwd_kernel<T, V, B>, (unsigned)std::min(n, ceil_div(steps, b.warps)), 256, smem(b.warps),
                   s, b);
 }
-template <class T, int G>
+template <class T, int G, bool HOLD>
 cudaError_t launch_norm_fwd_group(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    constexpr int V = 16 / kVec<T>, kGroups = 1024 / G;
+    constexpr int V = (HOLD ? 16 : 32) / kVec<T>, kGroups = 1024 / G, kMost = 222 * 1024;
+    constexpr int kWeights = HOLD ? 0 : 2 * 32 * G * (int)sizeof(float);
+    static_assert(kWeights + kGroups * G * V * 16 <= kMost, "a row a group");
     static PerDeviceOnce once;
     const cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(layernorm_fwd_group_kernel<T, G, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kGroups * kNormAhead * norm_row_bytes<T>(16 * G));
+        return cudaFuncSetAttribute(layernorm_fwd_group_kernel<T, G, V, HOLD>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     });
     if (e != cudaSuccess) return e;
-    const int64_t blocks = std::min<int64_t>(sm_count(), ceil_div(a.rows, kGroups));
-    return launch(layernorm_fwd_group_kernel<T, G, V>, (unsigned)blocks, kGroups * G,
-                  kGroups * kNormAhead * norm_row_bytes<T>(a.cols), s, a);
+    NormArgs b = a;
+    const int rows = kGroups * norm_row_bytes<T>(a.cols);
+    b.slots = std::min(3, (kMost - kWeights) / rows);
+    return launch(layernorm_fwd_group_kernel<T, G, V, HOLD>,
+                  (unsigned)std::min<int64_t>(sm_count(), ceil_div(a.rows, kGroups)), 1024,
+                  kWeights + b.slots * rows, s, b);
 }
 template <class T>
 cudaError_t launch_norm_fwd_long(const NormArgs &a, cudaStream_t s) {
@@ -113,9 +118,15 @@ cudaError_t norm_fwd(const NormArgs &a, cudaStream_t s) {
     if (n <= 128) return launch_norm_fwd<T, 4, 2>(a, s);
     if (n <= 256) return launch_norm_fwd<T, 8, 1>(a, s);
     if (n <= 512) return launch_norm_fwd<T, 16, 1>(a, s);
-    if (a.cols <= 4096) return launch_norm_fwd_group<T, 256>(a, s);
-    if (a.cols <= 8192) return launch_norm_fwd_group<T, 512>(a, s);
-    if (a.cols <= 16384) return launch_norm_fwd_group<T, 1024>(a, s);
+    // bf16: 32 columns a thread, so that two groups more share an SM's barriers (8192 x 8192: 50 us, with 16
+    // columns and the weights in registers 68); fp32 has the bytes to cover them (16384 x 4096: 88 us, 93 with 32)
+    if constexpr (sizeof(T) == 2) {
+        if (a.cols <= 8192) return launch_norm_fwd_group<T, 256, false>(a, s);
+    } else {
+        if (a.cols <= 4096) return launch_norm_fwd_group<T, 256, true>(a, s);
+        if (a.cols <= 8192) return launch_norm_fwd_group<T, 512, true>(a, s);
+    }
+    if (a.cols <= 16384) return launch_norm_fwd_group<T, 1024, true>(a, s);
     return launch_norm_fwd_long<T>(a, s);
 }
 
@@ -356,7 +367,15 @@ int64_t grad_table(GradTable<N> &t, const qt2_grad *g, int64_t at, int64_t count
     }
     return at;
 }
-constexpr int kGradBlocks = 148 * 8;   // resident ones: more would not raise the bandwidth
+// A block takes about four chunks: short enough shares that the SMs finish together, whatever
+// the tensors' sizes, long enough that looking the tensor up does not show.  Of the norm's launch at most
+// kGradBlocks, which leave a partial sum each.
+constexpr int kGradBlocks = 148 * 32;
+template <int N>
+int grad_blocks(const GradTable<N> &t, int most) {
+    const int chunks = t.first[t.count];
+    return std::min(std::min(chunks, most), std::max(148 * 4, chunks / 4));
+}
 constexpr int kGradAlone = 8;          // chunks that one block reads faster than two launches take
 
 template <int N>
@@ -369,12 +388,10 @@ cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStr
     return launch(grad_norm_end_kernel, 1, kGradThreads, 0, s, part, n, norm);
 }
 template <int N>
-cudaError_t launch_grad_clip(const GradTable<N> &t, const float *norm, float max_norm, int blocks, cudaStream_t s) {
+cudaError_t launch_grad_clip(const GradTable<N> &t, const float *norm, float max_norm, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    return launch(grad_clip_kernel<N>, blocks, kGradThreads, 0, s, t, norm, max_norm);
+    return launch(grad_clip_kernel<N>, grad_blocks(t, INT32_MAX), kGradThreads, 0, s, t, norm, max_norm);
 }
-template <int N>
-int grad_blocks(const GradTable<N> &t) { return std::min<int>(t.first[t.count], kGradBlocks); }
 
 template <int N>
 cudaError_t grad_norm(const qt2_grad *grads, int64_t count, float *norm, double *part, cudaStream_t s) {
@@ -384,7 +401,7 @@ cudaError_t grad_norm(const qt2_grad *grads, int64_t count, float *norm, double 
         at = grad_table(t, grads, at, count);
         if (t.count == 0) break;
         const bool alone = n == 0 && at == count && t.first[t.count] <= kGradAlone;
-        const int blocks = alone ? 1 : grad_blocks(t);
+        const int blocks = alone ? 1 : grad_blocks(t, kGradBlocks);
         const cudaError_t e = launch_grad_norm(t, part + n, alone ? norm : nullptr, blocks, s);
         if (e != cudaSuccess || alone) return e;
         n += blocks;
@@ -397,7 +414,7 @@ cudaError_t grad_clip(const qt2_grad *grads, int64_t count, const float *norm, f
     for (int64_t at = 0; at < count;) {
         at = grad_table(t, grads, at, count);
         if (t.count == 0) break;
-        const cudaError_t e = launch_grad_clip(t, norm, max_norm, grad_blocks(t), s);
+        const cudaError_t e = launch_grad_clip(t, norm, max_norm, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -626,8 +643,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
 qt2_status qt2_grad_norm_workspace_size(const qt2_grad *grads, int64_t count, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
     if (const qt2_status st = grad_check(grads, count, false)) return st;
-    // a launch takes at least kGradSmall tensors, unless their chunks are more than it can count
-    *bytes = (size_t)(ceil_div(count, count <= kGradSmall ? kGradSmall : kGradLarge) + grad_over(grads, count)) *
+    *bytes = (size_t)(ceil_div(count, kGradLarge) + grad_over(grads, count)) *
              kGradBlocks * sizeof(double);
     return QT2_OK;
 }
@@ -642,8 +658,10 @@ qt2_status qt2_grad_norm(const qt2_grad *grads, int64_t count, float *norm, void
     if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
     if (const qt2_status st = check_device()) return st;
     double *part = static_cast<double *>(workspace);
-    return from_cuda(count <= kGradSmall ? grad_norm<kGradSmall>(grads, count, norm, part, as_stream(stream))
-                                         : grad_norm<kGradLarge>(grads, count, norm, part, as_stream(stream)));
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(count <= kGradSmall    ? grad_norm<kGradSmall>(grads, count, norm, part, s)
+                     : count <= kGradMiddle ? grad_norm<kGradMiddle>(grads, count, norm, part, s)
+                                            : grad_norm<kGradLarge>(grads, count, norm, part, s));
 }
 
 qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm, float max_norm,
@@ -653,8 +671,10 @@ qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm
     if (const qt2_status st = grad_check(grads, count, true)) return st;
     if (!aligned(norm, 4)) return QT2_ERR_ALIGN;
     if (const qt2_status st = check_device()) return st;
-    return from_cuda(count <= kGradSmall ? grad_clip<kGradSmall>(grads, count, norm, max_norm, as_stream(stream))
-                                         : grad_clip<kGradLarge>(grads, count, norm, max_norm, as_stream(stream)));
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(count <= kGradSmall    ? grad_clip<kGradSmall>(grads, count, norm, max_norm, s)
+                     : count <= kGradMiddle ? grad_clip<kGradMiddle>(grads, count, norm, max_norm, s)
+                                            : grad_clip<kGradLarge>(grads, count, norm, max_norm, s));
 }
 
 }  // extern "C"
