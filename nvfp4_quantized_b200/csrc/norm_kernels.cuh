@@ -21,7 +21,7 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-constexpr int kNormThreads = 256;   // of the kernels for rows too long for registers
+constexpr int kNormThreads = 512;   // of the kernels for rows too long for registers
 
 // 16 bytes of a row: 8 bf16 or 4 fp32 elements.
 template <class T>
@@ -206,6 +206,75 @@ __device__ __forceinline__ uint4 stage_vec(const uint4 *stage, int i, int cols) 
 // Keeps the compiler from holding a vector's unpacked values across this point: unpacking again is
 // cheaper than the registers (16 vectors of bf16 a lane would take 128).
 __device__ __forceinline__ void repack(uint4 &r) { asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)); }
+
+// ---------------------------------------------------------------------------------------------
+// Forward, rows of up to 16 vectors: G lanes of a warp a row, one vector a lane, B rows at a time, the
+// lane's weights and biases in registers.  (A warp a row leaves most lanes without work: 1048576 x 64
+// bf16 took 282 us.)
+// ---------------------------------------------------------------------------------------------
+template <class T, int G, int B>
+__global__ void __launch_bounds__(256) layernorm_fwd_short_kernel(const NormArgs a) {
+    constexpr int E = kVec<T>, P = E / 2, kGroups = 256 / G;
+    grid_dependency();
+    const int lane = threadIdx.x % G, group = threadIdx.x / G, c = lane * E;
+    float none[2][32][B], wf[E], bf[E];
+    load_weight(c < a.cols ? a.w : nullptr, a.w_f32, c, a.cols, 1.0f, wf);
+    load_weight(c < a.cols ? a.b : nullptr, a.w_f32, c, a.cols, 0.0f, bf);
+    const int64_t stride = (int64_t)gridDim.x * kGroups * B;
+    uint4 raw[B];
+    auto fetch = [&](int64_t r0) {
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            raw[k] = load_row(static_cast<const T *>(a.x) + (r0 + k) * a.ldx, c, a.cols, r0 + k < a.rows);
+    };
+    int64_t at = (int64_t)blockIdx.x * kGroups * B;
+    fetch(at + group * B);
+    // the trip count is the block's, not the group's: every lane of a warp meets the shuffles of row_sum
+    for (; at < a.rows; at += stride) {
+        const int64_t r0 = at + group * B;
+        uint64_t x[B][P];
+        float s[B], mean[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            pairs_of<T>(raw[k], x[k]);
+            uint64_t s2 = x[k][0];
+#pragma unroll
+            for (int e = 1; e < P; ++e) s2 = f2_add(s2, x[k][e]);
+            s[k] = f2_sum(s2);
+        }
+        fetch(r0 + stride);
+        row_sum<G>(s, none, 0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            mean[k] = s[k] / a.cols;
+            float q = 0.0f;
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const float2 v = f2_get(x[k][e]);
+                const float d0 = c + 2 * e < a.cols ? v.x - mean[k] : 0.0f;
+                const float d1 = c + 2 * e + 1 < a.cols ? v.y - mean[k] : 0.0f;
+                q = fmaf(d0, d0, fmaf(d1, d1, q));
+                x[k][e] = f2(d0, d1);
+            }
+            s[k] = q;
+        }
+        row_sum<G>(s, none, 0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (r0 + k >= a.rows) continue;
+            const float rstd = 1.0f / sqrtf(s[k] / a.cols + a.eps);
+            float o[E];
+            floats_of<E>(x[k], o);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(o[e] * rstd, wf[e], bf[e]);
+            store_row(static_cast<T *>(a.y) + (r0 + k) * a.ldy, c, a.cols, o, a.y, (a.rows - 1) * a.ldy + a.cols);
+            if (lane == 0) {
+                if (a.mean) a.mean[r0 + k] = mean[k];
+                if (a.rstd) a.rstd[r0 + k] = rstd;
+            }
+        }
+    }
+}
 
 // ---------------------------------------------------------------------------------------------
 // Forward, a warp a row (short rows: B of them at a time), V vectors of 16 bytes a lane: one read and one write of HBM, no barrier
@@ -631,26 +700,31 @@ __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a)
 // sum a column (from a block a group, 888 of them at 2048 columns, they cost 19 us of 87).  WHOLE: the
 // row's length is a multiple of the vector's, so that no vector has to be cut.
 // ---------------------------------------------------------------------------------------------
-// The parameters for rows of up to 16 G columns (8 G: half the vectors, twice the rows).  bf16: two
+// The parameters for rows of up to C G columns (C = 8: half the vectors, twice the rows).  bf16: two
 // rows share the loop's and the sums' instructions, and a deeper ring is worth more than more threads
 // (32768 x 2048: one row at a time 94 us, two 79 us; 640 threads and 2 slots 76 us, 512 and 3 slots less).
 // fp32 has half the instructions a byte, and twice the bytes to hold.
-template <class T, int G, bool HALF>
+// C = 32 columns a thread: the weights are in shared memory, which leaves room for two slots of a bf16 row
+// and one of an fp32 row.
+template <class T, int G, int C>
 struct NormRing {
     static constexpr bool k16 = sizeof(T) == 2;
-    static constexpr int V = (HALF ? 8 : 16) / kVec<T>;          // vectors a thread
-    static constexpr int B = (k16 ? 2 : 1) * (HALF ? 2 : 1);     // rows at a time
-    static constexpr int S = k16 || G == 512 ? 3 : 2;            // slots of B rows
+    static constexpr int V = C / kVec<T>;                             // vectors a thread
+    static constexpr int B = C == 32 ? 1 : (k16 ? 2 : 1) * 16 / C;    // rows at a time
+    static constexpr int S = C == 32 ? (k16 ? 2 : 1) : k16 || G == 512 ? 3 : 2;   // slots of B rows
     static constexpr int kGroups = (k16 || G == 512 ? 512 : 768) / G;
-    static constexpr int kColumns = (HALF ? 8 : 16) * G;
-    static constexpr int bytes(int cols) { return kGroups * S * B * 2 * norm_row_bytes<T>(cols); }
+    static constexpr int kColumns = C * G;
+    static constexpr bool kHold = C < 32;                             // weights in registers
+    static constexpr int kWeights = kHold ? 0 : kColumns * 4;         // bytes of them in shared memory
+    static constexpr int bytes(int cols) { return kWeights + kGroups * S * B * 2 * norm_row_bytes<T>(cols); }
 };
 
-template <class T, int G, bool HALF, bool WHOLE>
-__global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm_bwd_ring_kernel(const NormArgs a) {
-    using R = NormRing<T, G, HALF>;
-    constexpr int E = kVec<T>, P = E / 2, V = R::V, S = R::S, B = R::B, kGroups = R::kGroups;
-    extern __shared__ __align__(16) uint8_t ring_all[];   // [groups][S][B][2 (x, dy)][row]
+template <class T, int G, int C, bool WHOLE>
+__global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bwd_ring_kernel(const NormArgs a) {
+    using R = NormRing<T, G, C>;
+    constexpr int E = kVec<T>, P = E / 2, Q = E / 4, V = R::V, S = R::S, B = R::B, kGroups = R::kGroups;
+    extern __shared__ float4 weights[];   // !kHold: [Q][G V]; then the rings: [groups][S][B][2 (x, dy)][row]
+    uint8_t *const ring_all = reinterpret_cast<uint8_t *>(weights) + R::kWeights;
     __shared__ float sh_all[kGroups][2][32][2 * B];
     __shared__ __align__(8) uint64_t full_all[kGroups][S];
     const int cols = a.cols, rows = (int)a.rows, row_bytes = norm_row_bytes<T>(cols);
@@ -676,16 +750,35 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
     }
     grid_dependency();
     if (lane == 0)
-        for (int i = 0; i < S - 1; ++i) issue(first + i * step, i);
-    uint64_t w[V][P], dw2[V][P] = {}, db2[V][P] = {};
+        for (int i = 0; i < (S > 1 ? S - 1 : 1); ++i) issue(first + i * step, i);
+    uint64_t held[R::kHold ? V : 1][P], dw2[V][P] = {}, db2[V][P] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = (lane + i * G) * E;
         float f[E];
         load_weight(c < cols ? a.w : nullptr, a.w_f32, c, cols, 1.0f, f);
+        if constexpr (R::kHold) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) w[i][e] = f2(f[2 * e], f[2 * e + 1]);
+            for (int e = 0; e < P; ++e) held[i][e] = f2(f[2 * e], f[2 * e + 1]);
+        } else {   // one group: every thread reads back what it wrote
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                weights[q * G * V + lane + i * G] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        }
     }
+    auto weight = [&](int v, uint64_t (&w)[P]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (R::kHold) {
+                w[2 * q] = held[v][2 * q];
+                w[2 * q + 1] = held[v][2 * q + 1];
+            } else {
+                const float4 p = weights[q * G * V + lane + v * G];
+                w[2 * q] = f2(p.x, p.y);
+                w[2 * q + 1] = f2(p.z, p.w);
+            }
+        }
+    };
     __syncthreads();
     const float inv = 1.0f / cols;
     bool ok = true;   // after a wait that ran out (reported), the rest is not waited for
@@ -739,11 +832,12 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if ((lane + v * G) * E >= cols) continue;
-                uint64_t d[P], g[P];
+                uint64_t d[P], g[P], w[P];
                 read(k, v, d, g);
+                weight(v, w);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
-                    const uint64_t p = f2_mul(g[e], w[v][e]);
+                    const uint64_t p = f2_mul(g[e], w[e]);
                     s2 = f2_add(s2, p);
                     q2 = f2_fma(p, d[e], q2);
                     db2[v][e] = f2_add(db2[v][e], g[e]);
@@ -757,7 +851,7 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
         slot ^= 1;
         if (G == 32) __syncwarp();
         // every thread is past the rows before these: their slot takes the rows S - 1 steps ahead
-        if (lane == 0 && ok) issue(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
+        if (S > 1 && lane == 0 && ok) issue(row + (S - 1) * step, st == 0 ? S - 1 : st - 1);
         if (a.y) {
 #pragma unroll
             for (int k = 0; k < B; ++k) {
@@ -769,17 +863,22 @@ __global__ void __launch_bounds__(NormRing<T, G, HALF>::kGroups *G, 1) layernorm
                 for (int v = 0; v < V; ++v) {
                     const int c = (lane + v * G) * E;
                     if (c >= cols) continue;
-                    uint64_t d[P], g[P];
+                    uint64_t d[P], g[P], w[P];
                     read(k, v, d, g);
+                    weight(v, w);
 #pragma unroll
                     for (int e = 0; e < P; ++e)
-                        g[e] = f2_fma(f2_mul(g[e], w[v][e]), r2, f2_fma(d[e], m2p, m1p));
+                        g[e] = f2_fma(f2_mul(g[e], w[e]), r2, f2_fma(d[e], m2p, m1p));
                     float o[E];
                     floats_of<E>(g, o);
                     store_row<T, WHOLE>(static_cast<T *>(a.y) + (row + k) * a.ldy, c, cols, o, a.y,
                                         (a.rows - 1) * a.ldy + cols);
                 }
             }
+        }
+        if (S == 1) {   // the only slot is free when every thread has written its part of dx
+            group_sync<G>(bar);
+            if (lane == 0 && ok) issue(row + step, 0);
         }
         if (++st == S) {
             st = 0;
@@ -845,34 +944,50 @@ __global__ void __launch_bounds__(1024) layernorm_dw_kernel(const NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Rows too long for registers: a block a row, which it reads three times (from L2 after the first).
+// Rows too long for registers and shared memory: a block a row, which it reads again for each pass (from
+// L2 after the first).
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ float weight_at(const void *w, int f32, int c, float other) {
-    if (!w) return other;
-    return f32 ? static_cast<const float *>(w)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
-}
-
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const NormArgs a) {
     grid_dependency();
+    constexpr int E = kVec<T>;
     __shared__ float sh[2][32][1];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
-    T *y = static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy;
     float s[1] = {0.0f};
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) s[0] += to_f32(x[c]);
+#pragma unroll 4
+    for (int c = threadIdx.x * E; c < a.cols; c += kNormThreads * E) {
+        float v[E], t = 0.0f;
+        unpack(load_row(x, c, a.cols, true), v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) t += v[e];
+        s[0] += t;
+    }
     row_sum<kNormThreads>(s, sh, 0);
     const float mean = s[0] / a.cols;
     s[0] = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float d = to_f32(x[c]) - mean;
-        s[0] = fmaf(d, d, s[0]);
+#pragma unroll 4
+    for (int c = threadIdx.x * E; c < a.cols; c += kNormThreads * E) {
+        float v[E], t = 0.0f;
+        unpack(load_row(x, c, a.cols, true), v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float d = c + e < a.cols ? v[e] - mean : 0.0f;
+            t = fmaf(d, d, t);
+        }
+        s[0] += t;
     }
     row_sum<kNormThreads>(s, sh, 1);
     const float rstd = 1.0f / sqrtf(s[0] / a.cols + a.eps);
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float h = (to_f32(x[c]) - mean) * rstd;
-        const float o = fmaf(h, weight_at(a.w, a.w_f32, c, 1.0f), weight_at(a.b, a.w_f32, c, 0.0f));
-        if (QT2_STORE_OK(y + c, sizeof(T), a.y, ((a.rows - 1) * a.ldy + a.cols) * sizeof(T))) y[c] = from_f32<T>(o);
+#pragma unroll 2
+    for (int c = threadIdx.x * E; c < a.cols; c += kNormThreads * E) {
+        float v[E], w[E], b[E];
+        unpack(load_row(x, c, a.cols, true), v);
+        load_weight(a.w, a.w_f32, c, a.cols, 1.0f, w);
+        load_weight(a.b, a.w_f32, c, a.cols, 0.0f, b);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+        store_row(static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy, c, a.cols, v, a.y,
+                  (a.rows - 1) * a.ldy + a.cols);
     }
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[blockIdx.x] = mean;
@@ -883,40 +998,68 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const 
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_dx_long_kernel(const NormArgs a) {
     grid_dependency();
+    constexpr int E = kVec<T>;
     __shared__ float sh[2][32][2];
     const T *x = static_cast<const T *>(a.x) + (int64_t)blockIdx.x * a.ldx;
     const T *dy = static_cast<const T *>(a.dy) + (int64_t)blockIdx.x * a.lddy;
-    T *dx = static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy;
     const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
     float s[2] = {};
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * weight_at(a.w, a.w_f32, c, 1.0f);
-        s[0] += g;
-        s[1] = fmaf(g, h, s[1]);
+#pragma unroll 2
+    for (int c = threadIdx.x * E; c < a.cols; c += kNormThreads * E) {
+        float v[E], g[E], w[E], t = 0.0f, q = 0.0f;
+        unpack(load_row(x, c, a.cols, true), v);
+        unpack(load_row(dy, c, a.cols, true), g);   // zero behind the row's end
+        load_weight(a.w, a.w_f32, c, a.cols, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float p = g[e] * w[e];
+            t += p;
+            q = fmaf(p, (v[e] - mean) * rstd, q);
+        }
+        s[0] += t;
+        s[1] += q;
     }
     row_sum<kNormThreads>(s, sh, 0);
     const float m1 = s[0] / a.cols, m2 = s[1] / a.cols;
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) {
-        const float h = (to_f32(x[c]) - mean) * rstd, g = to_f32(dy[c]) * weight_at(a.w, a.w_f32, c, 1.0f);
-        if (QT2_STORE_OK(dx + c, sizeof(T), a.y, ((a.rows - 1) * a.ldy + a.cols) * sizeof(T)))
-            dx[c] = from_f32<T>(rstd * (g - m1 - h * m2));
+#pragma unroll 2
+    for (int c = threadIdx.x * E; c < a.cols; c += kNormThreads * E) {
+        float v[E], g[E], w[E];
+        unpack(load_row(x, c, a.cols, true), v);
+        unpack(load_row(dy, c, a.cols, true), g);
+        load_weight(a.w, a.w_f32, c, a.cols, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = rstd * (g[e] * w[e] - m1 - (v[e] - mean) * rstd * m2);
+        store_row(static_cast<T *>(a.y) + (int64_t)blockIdx.x * a.ldy, c, a.cols, v, a.y,
+                  (a.rows - 1) * a.ldy + a.cols);
     }
 }
 
-// Partial sums of dw and db over rows split, split + splits, ...: one thread a column.
+// Partial sums of dw and db over rows split, split + splits, ...: one vector a thread.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) layernorm_dw_long_kernel(const NormArgs a) {
     grid_dependency();
-    const int c = blockIdx.x * kNormThreads + threadIdx.x;
+    constexpr int E = kVec<T>;
+    const int c = (blockIdx.x * kNormThreads + threadIdx.x) * E;
     if (c >= a.cols) return;
-    float dw = 0.0f, db = 0.0f;
+    float dw[E] = {}, db[E] = {};
+#pragma unroll 4
     for (int64_t r = blockIdx.y; r < a.rows; r += a.splits) {
-        const float g = to_f32(static_cast<const T *>(a.dy)[r * a.lddy + c]);
-        db += g;
-        dw = fmaf(g, (to_f32(static_cast<const T *>(a.x)[r * a.ldx + c]) - a.mean[r]) * a.rstd[r], dw);
+        float v[E], g[E];
+        unpack(load_row(static_cast<const T *>(a.x) + r * a.ldx, c, a.cols, true), v);
+        unpack(load_row(static_cast<const T *>(a.dy) + r * a.lddy, c, a.cols, true), g);
+        const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            db[e] += g[e];
+            dw[e] = fmaf(g[e], (v[e] - mean) * rstd, dw[e]);
+        }
     }
-    a.part[((int64_t)blockIdx.y * 2) * a.cols + c] = dw;
-    a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = db;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (c + e >= a.cols) continue;
+        a.part[(int64_t)blockIdx.y * 2 * a.cols + c + e] = dw[e];
+        a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c + e] = db[e];
+    }
 }
 
 }  // namespace qt2

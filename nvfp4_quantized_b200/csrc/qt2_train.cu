@@ -86,6 +86,18 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     return launch(layernorm_fwd_kernel<T, V, B>, (unsigned)std::min(n, ceil_div(steps, b.warps)), 256, smem(b.warps),
                   s, b);
 }
+template <class T, int G>
+cudaError_t launch_norm_fwd_short(const NormArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    constexpr int B = 4;
+    static PerDeviceOnce once;
+    static std::atomic<int> blocks[kMaxDevices];
+    int64_t n = 0;
+    const cudaError_t e = resident_blocks(once, blocks, layernorm_fwd_short_kernel<T, G, B>, 256, 0, &n);
+    if (e != cudaSuccess) return e;
+    return launch(layernorm_fwd_short_kernel<T, G, B>, (unsigned)std::min(n, ceil_div(a.rows, 256 / G * B)), 256, 0, s,
+                  a);
+}
 template <class T, int G, bool HOLD>
 cudaError_t launch_norm_fwd_group(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
@@ -113,6 +125,9 @@ cudaError_t launch_norm_fwd_long(const NormArgs &a, cudaStream_t s) {
 template <class T>
 cudaError_t norm_fwd(const NormArgs &a, cudaStream_t s) {
     const int64_t n = ceil_div(a.cols, kVec<T>);   // 16-byte vectors a row
+    if (n <= 4) return launch_norm_fwd_short<T, 4>(a, s);
+    if (n <= 8) return launch_norm_fwd_short<T, 8>(a, s);
+    if (n <= 16) return launch_norm_fwd_short<T, 16>(a, s);
     if (n <= 32) return launch_norm_fwd<T, 1, 4>(a, s);
     if (n <= 64) return launch_norm_fwd<T, 2, 4>(a, s);
     if (n <= 128) return launch_norm_fwd<T, 4, 2>(a, s);
@@ -143,14 +158,15 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
         using R = decltype(r);
         return NormBwdPlan{32, R::kGroups * R::B, 148};
     };
-    NormBwdPlan p = cols <= 64     ? NormBwdPlan{8, 64, 148 * 2}
-                    : cols <= 256  ? ring(NormRing<T, 32, true>{})
-                    : cols <= 512  ? ring(NormRing<T, 32, false>{})
-                    : cols <= 1024 ? ring(NormRing<T, 64, false>{})
-                    : cols <= 2048 ? ring(NormRing<T, 128, false>{})
-                    : cols <= 4096 ? ring(NormRing<T, 256, false>{})
-                    : cols <= 8192 ? ring(NormRing<T, 512, false>{})
-                                   : NormBwdPlan{0, 16, 64};
+    NormBwdPlan p = cols <= 64      ? NormBwdPlan{8, 64, 148 * 2}
+                    : cols <= 256   ? ring(NormRing<T, 32, 8>{})
+                    : cols <= 512   ? ring(NormRing<T, 32, 16>{})
+                    : cols <= 1024  ? ring(NormRing<T, 64, 16>{})
+                    : cols <= 2048  ? ring(NormRing<T, 128, 16>{})
+                    : cols <= 4096  ? ring(NormRing<T, 256, 16>{})
+                    : cols <= 8192  ? ring(NormRing<T, 512, 16>{})
+                    : cols <= 16384 ? ring(NormRing<T, 512, 32>{})
+                                    : NormBwdPlan{0, 16, 64};
     const int64_t steps = ceil_div(rows, p.step);
     p.blocks = (int)ceil_div(steps, ceil_div(steps, p.blocks));
     return p;
@@ -161,23 +177,23 @@ cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     return launch(layernorm_bwd_kernel<T, G, V, B>, (unsigned)a.splits, 256, 0, s, a);
 }
-template <class T, int G, bool HALF, bool WHOLE>
+template <class T, int G, int C, bool WHOLE>
 cudaError_t launch_norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    using R = NormRing<T, G, HALF>;
+    using R = NormRing<T, G, C>;
     static PerDeviceOnce once;
     const cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>,
+        return cudaFuncSetAttribute(layernorm_bwd_ring_kernel<T, G, C, WHOLE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, R::bytes(R::kColumns));
     });
     if (e != cudaSuccess) return e;
-    return launch(layernorm_bwd_ring_kernel<T, G, HALF, WHOLE>, (unsigned)a.splits, R::kGroups * G, R::bytes(a.cols),
+    return launch(layernorm_bwd_ring_kernel<T, G, C, WHOLE>, (unsigned)a.splits, R::kGroups * G, R::bytes(a.cols),
                   s, a);
 }
-template <class T, int G, bool HALF>
+template <class T, int G, int C>
 cudaError_t norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
-    return a.cols % kVec<T> ? launch_norm_bwd_ring<T, G, HALF, false>(a, s)
-                            : launch_norm_bwd_ring<T, G, HALF, true>(a, s);
+    return a.cols % kVec<T> ? launch_norm_bwd_ring<T, G, C, false>(a, s)
+                            : launch_norm_bwd_ring<T, G, C, true>(a, s);
 }
 cudaError_t launch_norm_dw(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
@@ -191,7 +207,7 @@ cudaError_t launch_norm_dx_long(const NormArgs &a, cudaStream_t s) {
 template <class T>
 cudaError_t launch_norm_dw_long(const NormArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads), (unsigned)a.splits);
+    const dim3 grid((unsigned)ceil_div(a.cols, kNormThreads * kVec<T>), (unsigned)a.splits);
     return launch(layernorm_dw_long_kernel<T>, grid, kNormThreads, 0, s, a);
 }
 template <class T>
@@ -202,12 +218,13 @@ cudaError_t norm_bwd(const NormArgs &a, int threads, cudaStream_t s) {
         if (e == cudaSuccess && a.y) e = launch_norm_dx_long<T>(a, s);
     } else {
         e = a.cols <= 64     ? launch_norm_bwd<T, 8, 8 / kVec<T>, 2>(a, s)
-            : a.cols <= 256  ? norm_bwd_ring<T, 32, true>(a, s)
-            : a.cols <= 512  ? norm_bwd_ring<T, 32, false>(a, s)
-            : a.cols <= 1024 ? norm_bwd_ring<T, 64, false>(a, s)
-            : a.cols <= 2048 ? norm_bwd_ring<T, 128, false>(a, s)
-            : a.cols <= 4096 ? norm_bwd_ring<T, 256, false>(a, s)
-                             : norm_bwd_ring<T, 512, false>(a, s);
+            : a.cols <= 256  ? norm_bwd_ring<T, 32, 8>(a, s)
+            : a.cols <= 512  ? norm_bwd_ring<T, 32, 16>(a, s)
+            : a.cols <= 1024 ? norm_bwd_ring<T, 64, 16>(a, s)
+            : a.cols <= 2048 ? norm_bwd_ring<T, 128, 16>(a, s)
+            : a.cols <= 4096 ? norm_bwd_ring<T, 256, 16>(a, s)
+            : a.cols <= 8192 ? norm_bwd_ring<T, 512, 16>(a, s)
+                             : norm_bwd_ring<T, 512, 32>(a, s);
     }
     if (e == cudaSuccess && a.part) e = launch_norm_dw(a, s);
     return e;
