@@ -7,7 +7,8 @@
  * Conventions are those of qt2.h (device pointers owned by the caller, work enqueued on `stream`,
  * arguments validated on the host before any launch, negative qt2_status on error, no allocation,
  * no abort, one NVTX range per call), with these differences:
- *   - Dimensions are any positive ints below 2^30, not multiples of 128.  Matrices are row-major
+ *   - Dimensions are any positive ints below 2^30, not multiples of 128 (a matrix of the head loss
+ *     has fewer than 2^44 elements).  Matrices are row-major
  *     with a leading dimension that is a multiple of 8 elements and at least the row's length,
  *     and 16-byte aligned bases.  Elements between a row's length and its leading dimension are
  *     neither used nor written.
@@ -85,7 +86,9 @@ QT2_API qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64
  *   dx = P w  [T][K] bf16,  dw = P^T x  [V][K] of type dw_dtype.
  * The logits are formed again, a piece of the vocabulary at a time; the piece's P is held in bf16
  * (rounded once, 2^-8 at most relative to each entry) in the workspace while the tensor cores
- * multiply it, with fp32 sums over the whole of V (dx) and T (dw).  A zero row of P still
+ * multiply it, with fp32 sums over the whole of V (dx) and T (dw).  dloss enters P as a share of its
+ * largest finite magnitude, which dx and dw are multiplied by at the end in fp32: equal dloss (a
+ * mean) is not rounded.  Targets outside [0, V) count as ignore_index and are not reported again.  A zero row of P still
  * multiplies its row of x: x must be finite in rows without a target, too.
  * dx or dw may be NULL (not wanted), not both.
  * Workspace: qt2_linear_xent_bwd_workspace_size() bytes, 256-byte aligned.
@@ -101,9 +104,10 @@ QT2_API qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64
  * (>= 0) elements of type dtype, aligned to its element only; `out`, of the same size, type and
  * alignment rule, receives the clipped gradient and may be `grad` itself (it is not used by
  * qt2_grad_norm and may then be NULL).  The list is read on the host during the call.
+ * The outputs of two entries must not overlap, nor an output the gradient of another entry.
  *   qt2_grad_norm: *norm = sqrt(sum over all elements of g^2), without overflow or underflow of
- *     the squares for any finite fp32 values; squares are summed in fp32 over at most 8 elements,
- *     then in fp64.
+ *     the squares for any finite fp32 values (inf where the norm itself exceeds fp32); squares are
+ *     summed in fp32 over at most 8 elements, then in fp64.
  *     Workspace: qt2_grad_norm_workspace_size() bytes, 256-byte aligned.
  *   qt2_grad_clip: out = g * min(1, max_norm / (*norm + 1e-6)), max_norm >= 0, *norm read on the
  *     device (so that ranks can combine their norms between the two calls).  A NaN norm makes

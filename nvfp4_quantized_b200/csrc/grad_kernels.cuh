@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     sum = grad_block_sum(sum);
     if (threadIdx.x == 0) {
         if (norm)
-            *norm = (float)sqrt(sum);
+            put(norm, 0, 1, (float)sqrt(sum));
         else
-            part[blockIdx.x] = sum;
+            put(part, (int64_t)blockIdx.x, (int64_t)gridDim.x, sum);
     }
 }
 
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const doubl
     double sum = 0.0;
     for (int i = threadIdx.x; i < n; i += kGradThreads) sum += part[i];
     sum = grad_block_sum(sum);
-    if (threadIdx.x == 0) *norm = (float)sqrt(sum);
+    if (threadIdx.x == 0) put(norm, 0, 1, (float)sqrt(sum));
 }
 
 // The chunks from the last to the first: what the norm's pass read last is still in L2.

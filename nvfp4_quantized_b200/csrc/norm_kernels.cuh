@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(256) layernorm_fwd_short_kernel(const NormArgs
             for (int e = 0; e < E; ++e) o[e] = fmaf(o[e] * rstd, wf[e], bf[e]);
             store_row(static_cast<T *>(a.y) + (r0 + k) * a.ldy, c, a.cols, o, a.y, (a.rows - 1) * a.ldy + a.cols);
             if (lane == 0) {
-                if (a.mean) a.mean[r0 + k] = mean[k];
-                if (a.rstd) a.rstd[r0 + k] = rstd;
+                if (a.mean) put(a.mean, (int64_t)(r0 + k), a.rows, mean[k]);
+                if (a.rstd) put(a.rstd, (int64_t)(r0 + k), a.rows, rstd);
             }
         }
     }
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
                 raw[k][i] = load_row(reinterpret_cast<const T *>(stage + k * 32 * V), (lane + i * 32) * E, a.cols,
                                      row + k < a.rows);
         __syncwarp();
-        if (lane == 0 && ok) issue(row + stride);
+        if (lane == 0 && ok) issue(row + stride);   // (none follows a wait that ran out)
         float s[B], mean[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(256, V *B < 16 ? 3 : 2) layernorm_fwd_kernel(c
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 if (row + k >= a.rows) continue;
-                if (a.mean) a.mean[row + k] = mean[k];
-                if (a.rstd) a.rstd[row + k] = s[k];
+                if (a.mean) put(a.mean, (int64_t)(row + k), a.rows, mean[k]);
+                if (a.rstd) put(a.rstd, (int64_t)(row + k), a.rows, s[k]);
             }
         }
     }
@@ -486,10 +486,13 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const Norm
         }
     }
     __syncthreads();
-    int st = 0, phase = 0;
+    int st = 0, phase = 0, left = 0;
     bool ok = true;   // after a wait that ran out (reported), the rest is not waited for
     for (; row < a.rows; row += step) {
-        if (ok) ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        if (ok) {
+            ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+            left = ok ? 0 : slots - 1;
+        }
         const uint4 *const stage = reinterpret_cast<const uint4 *>(ring + st * row_bytes);
         uint4 raw[V];
         uint64_t s2 = 0;
@@ -509,6 +512,9 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const Norm
             st = 0;
             phase ^= 1;
         }
+        // after a wait that ran out: the copies that were on their way behind it, before the block ends
+        if (left > 0 && lane == 0 && row + step < a.rows) mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        if (left > 0) --left;
         const float mean = s[0] / cols;
         const uint64_t neg = f2(-mean, -mean);
         s2 = 0;
@@ -562,8 +568,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const Norm
             store_row(static_cast<T *>(a.y) + row * a.ldy, c, cols, o, a.y, (a.rows - 1) * a.ldy + cols);
         }
         if (lane == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
+            if (a.mean) put(a.mean, (int64_t)(row), a.rows, mean);
+            if (a.rstd) put(a.rstd, (int64_t)(row), a.rows, rstd);
         }
     }
 }
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a)
             float t = 0.0f;
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) t += sum[q][c];
-            part[which * a.cols + c] = t;
+            put(a.part, part - a.part + which * a.cols + c, (int64_t)a.splits * 2 * a.cols, t);
         }
     }
 }
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
         }
     };
     stats(first);
-    int st = 0, phase = 0, slot = 0;
+    int st = 0, phase = 0, slot = 0, left = 0;
     for (int row = first; row < rows; row += step) {
 #pragma unroll
         for (int k = 0; k < B; ++k) {
@@ -799,7 +805,10 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
             rstd[k] = next_rstd[k];
         }
         stats(row + step);
-        if (ok) ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        if (ok) {
+            ok = mbar_wait(full0 + 8 * st, (uint32_t)phase);
+            left = ok ? 0 : S - 2;
+        }
         const uint4 *const px = reinterpret_cast<const uint4 *>(ring + st * B * 2 * row_bytes);
         // pairs of x - mean and of dy of row k's vector v; zeros behind the row's end
         auto read = [&](int k, int v, uint64_t (&d)[P], uint64_t (&g)[P]) {
@@ -884,6 +893,9 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
             st = 0;
             phase ^= 1;
         }
+        // after a wait that ran out: the copies that were on their way behind it, before the block ends
+        if (left > 0 && lane == 0 && row + step < rows) mbar_wait(full0 + 8 * st, (uint32_t)phase);
+        if (left > 0) --left;
     }
     if (!a.part) return;
     // the rings' rows are all read: every group leaves its sums at the start of its ring
@@ -909,7 +921,7 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
 #pragma unroll
         for (int q = 0; q < kGroups; ++q)
             t += reinterpret_cast<const float *>(ring_all + (size_t)q * S * B * 2 * row_bytes)[c];
-        part[c] = t;
+        put(a.part, part - a.part + c, (int64_t)a.splits * 2 * cols, t);
     }
 }
 
@@ -990,8 +1002,8 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_long_kernel(const 
                   (a.rows - 1) * a.ldy + a.cols);
     }
     if (threadIdx.x == 0) {
-        if (a.mean) a.mean[blockIdx.x] = mean;
-        if (a.rstd) a.rstd[blockIdx.x] = rstd;
+        if (a.mean) put(a.mean, (int64_t)(blockIdx.x), a.rows, mean);
+        if (a.rstd) put(a.rstd, (int64_t)(blockIdx.x), a.rows, rstd);
     }
 }
 
@@ -1057,8 +1069,9 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_dw_long_kernel(const N
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (c + e >= a.cols) continue;
-        a.part[(int64_t)blockIdx.y * 2 * a.cols + c + e] = dw[e];
-        a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c + e] = db[e];
+        const int64_t at = (int64_t)blockIdx.y * 2 * a.cols + c + e, n = (int64_t)a.splits * 2 * a.cols;
+        put(a.part, at, n, dw[e]);
+        put(a.part, at + a.cols, n, db[e]);
     }
 }
 

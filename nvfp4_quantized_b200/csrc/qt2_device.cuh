@@ -42,6 +42,12 @@ __device__ __noinline__ bool store_in_bounds(const void *p, uint64_t bytes, cons
 #define QT2_STORE_OK(p, bytes, base, extent) ((void)(p), (void)(bytes), (void)(base), (void)(extent), true)
 #endif
 
+// *p = v, one element of an array of n at base.
+template <class T>
+__device__ __forceinline__ void put(T *base, int64_t i, int64_t n, const T &v) {
+    if (QT2_STORE_OK(base + i, sizeof(T), base, n * (int64_t)sizeof(T))) base[i] = v;
+}
+
 // Upper bound of any single wait inside a kernel (ns).  A correct launch never comes close.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 

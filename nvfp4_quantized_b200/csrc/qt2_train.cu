@@ -321,9 +321,9 @@ cudaError_t launch_mm(const MmMaps &maps, const MmArgs &a, int64_t jobs, cudaStr
     return launch(mm_pair_kernel<MODE, SWAP>, (unsigned)(2 * clusters), MmCfg<SWAP>::kThreads, MmCfg<SWAP>::kSmemBytes, s, maps, a);
 }
 
-cudaError_t launch_xent_loss(const MmArgs &a, int parts, float *loss, float *lse, cudaStream_t s) {
+cudaError_t launch_xent_loss(const MmArgs &a, float *loss, float *lse, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    return launch(xent_loss_kernel, (unsigned)ceil_div(a.T, 32), 1024, 0, s, a, parts, loss, lse);
+    return launch(xent_loss_kernel, (unsigned)ceil_div(a.T, 32), 1024, 0, s, a, loss, lse);
 }
 
 cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t s) {
@@ -334,10 +334,15 @@ cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t
                   (int64_t)a.dx_m * 256, (int64_t)a.dx_n * 256, static_cast<__nv_bfloat16 *>(dx), lddx);
 }
 
+// T, K and V, and x's and w's elements (which bound the workspaces' sizes) below 2^44.
+bool xent_dims_ok(int64_t T, int64_t K, int64_t V) {
+    return dim_ok(T) && dim_ok(K) && dim_ok(V) && T * K < (int64_t(1) << 44) && V * K < (int64_t(1) << 44);
+}
+
 qt2_status xent_check(const void *x, const void *w, const int64_t *targets, int64_t T, int64_t K, int64_t V,
                       int64_t ldx, int64_t ldw) {
     if (!x || !w || !targets) return QT2_ERR_INVALID_ARG;
-    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V) || !ld_shape_ok(ldx, K) || !ld_shape_ok(ldw, K)) return QT2_ERR_SHAPE;
+    if (!xent_dims_ok(T, K, V) || !ld_shape_ok(ldx, K) || !ld_shape_ok(ldw, K)) return QT2_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(targets, 8) || ldx % 8 || ldw % 8) return QT2_ERR_ALIGN;
     return QT2_OK;
 }
@@ -546,7 +551,7 @@ qt2_status qt2_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int x_
 
 qt2_status qt2_linear_xent_fwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
-    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V)) return QT2_ERR_SHAPE;
+    if (!xent_dims_ok(T, K, V)) return QT2_ERR_SHAPE;
     *bytes = xent_fwd_ws(xent_plan(T, K, V), T, nullptr).bytes;
     return QT2_OK;
 }
@@ -574,6 +579,7 @@ qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targ
     a.targets = targets;
     a.ignore = ignore_index;
     a.part = ws.part;
+    a.parts = p.parts;
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.w = static_cast<const __nv_bfloat16 *>(w);
     a.ldx = ldx;
@@ -585,13 +591,13 @@ qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targ
     const cudaStream_t s = as_stream(stream);
     cudaError_t e = p.swap ? launch_mm<kLoss, true>(maps, a, p.num_v, s)
                              : launch_mm<kLoss, false>(maps, a, p.num_m * p.num_v, s);
-    if (e == cudaSuccess) e = launch_xent_loss(a, p.parts, loss, lse, s);
+    if (e == cudaSuccess) e = launch_xent_loss(a, loss, lse, s);
     return from_cuda(e);
 }
 
 qt2_status qt2_linear_xent_bwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
-    if (!dim_ok(T) || !dim_ok(K) || !dim_ok(V)) return QT2_ERR_SHAPE;
+    if (!xent_dims_ok(T, K, V)) return QT2_ERR_SHAPE;
     *bytes = xent_bwd_ws(xent_plan(T, K, V), T, nullptr).bytes;
     return QT2_OK;
 }

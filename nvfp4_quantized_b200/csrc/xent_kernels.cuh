@@ -76,7 +76,8 @@ struct MmArgs {
     const int64_t *targets;
     int64_t ignore;
     const float *lse, *dloss;   // kProbs
-    float2 *part;          // kLoss: [2 * tiles of the vocabulary][T]
+    float2 *part;          // kLoss: [parts][T]
+    int parts;
     const __nv_bfloat16 *x, *w;   // kLoss, for the targets' logits
     int64_t ldx, ldw;
     float *hit, *exact;    // kLoss: the target's logit as the tile has it, and formed in fp32
@@ -169,7 +170,7 @@ __device__ __forceinline__ void xent_exact(const MmArgs &a, int64_t t, int y, in
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
-    if (lane == 0) a.exact[t] = h;
+    if (lane == 0) put(a.exact, t, (int64_t)a.T, h);
 }
 
 // Two (max, sum of exp) pairs as one.
@@ -195,7 +196,7 @@ __device__ __forceinline__ float xent_top(const MmArgs &a, int thread) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, sh[i]);
     if (m == 0.0f) m = 1.0f;
-    if (thread == 0 && blockIdx.x == 0) *a.top = m;
+    if (thread == 0 && blockIdx.x == 0) put(a.top, 0, 1, m);
     return m;
 }
 
@@ -223,14 +224,14 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
             s2 += ex2(fmaf(__uint_as_float(v[i + 2]), kLog2e, -sub));
             s3 += ex2(fmaf(__uint_as_float(v[i + 3]), kLog2e, -sub));
         }
-        a.part[(int64_t)(col >> 7) * a.T + row] = make_float2(m, (s0 + s1) + (s2 + s3));
+        put(a.part, (int64_t)(col >> 7) * a.T + row, (int64_t)a.parts * a.T, make_float2(m, (s0 + s1) + (s2 + s3)));
         const int y = xent_target(a, row) - col;
         if (y >= 0 && y < 128) {
             float h = 0.0f;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
                 if (i == y) h = __uint_as_float(v[i]);
-            a.hit[row] = h;
+            put(a.hit, (int64_t)row, (int64_t)a.T, h);
         }
     } else if (MODE == kProbs) {
         if (row >= a.T) return;
@@ -393,7 +394,7 @@ __device__ __forceinline__ void swap_epilogue(const MmArgs &a, int v, int first,
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (lane == k) sum = xent_join(sum, make_float2(m, s));
-            if (v == token.y) a.hit[t] = l;
+            if (v == token.y) put(a.hit, (int64_t)t, (int64_t)a.T, l);
         } else {
             float e = ex2(fmaf(l, kLog2e, -token.sub)) - (a.v0 + v == token.y ? 1.0f : 0.0f);
             e = token.y < 0 || !in ? 0.0f : e * token.g;
@@ -412,7 +413,7 @@ __device__ __forceinline__ void swap_finish(const MmArgs &a, int ew, int lane, c
     float2 p = sh[0][t];
 #pragma unroll
     for (int q = 1; q < 4; ++q) p = xent_join(p, sh[q][t]);
-    a.part[(int64_t)blockIdx.x * a.T + t] = p;
+    put(a.part, (int64_t)blockIdx.x * a.T + t, (int64_t)a.parts * a.T, p);
 }
 
 template <int MODE, bool SWAP>
@@ -608,7 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
 // loss and lse from the tiles' (max, sum) pairs: lse = M + log sum_i s_i exp(m_i - M).  A block takes
 // 32 rows; its 32 warps share the pairs.  lse takes the target's exact logit h in the place of the
 // tile's h' too: lse + log(1 + exp(h' - lse) (exp(h - h') - 1)).
-__global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int parts, float *loss, float *lse) {
+__global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, float *loss, float *lse) {
+    const int parts = a.parts;
     grid_dependency();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * 32 + lane, row = blockIdx.x * 32 + warp;
@@ -649,8 +651,8 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, int par
     float l = ref + logf(sum);
     const float off = exact - tile;
     if (in >= 0 && fabsf(off) < 1.0f) l += log1pf(__expf(tile - l) * expm1f(off));   // not for inf and NaN
-    lse[row] = l;
-    loss[row] = in >= 0 ? l - exact : 0.0f;
+    put(lse, (int64_t)row, (int64_t)a.T, l);
+    put(loss, (int64_t)row, (int64_t)a.T, in >= 0 ? l - exact : 0.0f);
     if (in < 0 && a.targets[row] != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
 }
 

@@ -230,6 +230,22 @@ class GradList:
             if g.get_device() != self.device or o.get_device() != self.device:
                 raise QT2Error("GradList", QT2_ERR_DEVICE)
             d.grad, d.out, d.numel, d.dtype = g.data_ptr(), o.data_ptr(), g.numel(), kind
+        # what one entry writes and another reads or writes too has no one value
+        spans = []
+        for d, g in zip(self.c, self.grads):
+            n = g.numel() * g.element_size()
+            if n:
+                spans.append((d.out, d.out + n, True))
+                if d.grad != d.out:
+                    spans.append((d.grad, d.grad + n, False))
+        written = read = 0   # ends of what has been seen
+        for lo, hi, writes in sorted(spans):
+            if lo < written or (writes and lo < read):
+                raise QT2Error("GradList", QT2_ERR_INVALID_ARG)
+            if writes:
+                written = max(written, hi)
+            else:
+                read = max(read, hi)
         self.address = ctypes.addressof(self.c)
 
 

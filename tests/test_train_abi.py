@@ -140,7 +140,7 @@ def test_workspace_queries(L):
     small, large = (tr.qt2_linear_xent_bwd_workspace_size(4096, 1024, v) for v in (65536, 1 << 20))
     assert large <= small + (64 << 20)
     for f in (tr.qt2_linear_xent_fwd_workspace_size, tr.qt2_linear_xent_bwd_workspace_size):
-        for dims in ((0, 1, 1), (1, -1, 1), (1, 1, 1 << 30)):
+        for dims in ((0, 1, 1), (1, -1, 1), (1, 1, 1 << 30), ((1 << 29), (1 << 29), 1), (1, 1 << 20, 1 << 24)):
             with pytest.raises(qt2.QT2Error) as e:
                 f(*dims)
             assert e.value.status == SHAPE
@@ -186,7 +186,7 @@ def test_injected_failures_at_every_site(L, name):
 def test_binding_refuses_types_before_the_call(monkeypatch):
     """Wrong element types and tensors of another device raise without reaching the library."""
     f, h, i = torch.zeros(8), torch.zeros(8, dtype=torch.float16), torch.zeros(8, dtype=torch.int32)
-    b = torch.zeros(8, dtype=torch.bfloat16)
+    b, g, long = torch.zeros(8, dtype=torch.bfloat16), torch.zeros(8), torch.zeros(16)
     cases = [
         lambda: tr.qt2_layernorm_fwd(h, 1, 8, 8, f, f, 1e-5, h, 8, f, f),
         lambda: tr.qt2_layernorm_fwd(f, 1, 8, 8, f, b, 1e-5, f, 8, f, f),
@@ -198,11 +198,17 @@ def test_binding_refuses_types_before_the_call(monkeypatch):
         lambda: tr.qt2_linear_xent_bwd(b, b, i.long(), f, f, 1, 8, 1, 8, 8, -100, b, 8, b, F32, 8, f, 32),
         lambda: tr.GradList([h]), lambda: tr.GradList([f], [b]), lambda: tr.GradList([f], []),
         lambda: tr.GradList([f], [torch.zeros(7)]), lambda: tr.GradList([torch.zeros(4, 4).t()]),
+        # what one entry writes, another reads or writes
+        lambda: tr.GradList([f, f]), lambda: tr.GradList([f, g], [f, f]), lambda: tr.GradList([f, g], [g, f]),
+        lambda: tr.GradList([long[:8]], [long[4:12]]), lambda: tr.GradList([long[:8], f], [f, long[7:15]]),
     ]
     for k, case in enumerate(cases):
         with pytest.raises(qt2.QT2Error) as e:
             case()
         assert e.value.status == ARG, k
+    tr.GradList([f, f], [g, torch.zeros(8)])   # read twice, written apart
+    tr.GradList([long[:8], long[8:]], [g, f])
+    tr.GradList([long[:8], long[8:]])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)   # CPU tensors are on no CUDA device
     with pytest.raises(qt2.QT2Error) as e:
         tr.qt2_layernorm_fwd(f, 1, 8, 8, f, f, 1e-5, f, 8, f, f)
