@@ -109,8 +109,8 @@ __device__ __forceinline__ double grad_block_sum(double sum) {
     return sum;
 }
 
-// part[blockIdx.x] = the sum of squares of the block's chunks, or (norm given: the only block of
-// the only launch) the norm itself.
+// part[blockIdx.x] = the sum of squares of the block's chunks, or (norm given: the blocks are one
+// cluster, and the launch the only one) the norm itself.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double *part,
                                                                  float *norm) {
@@ -132,12 +132,22 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
         }
     }
     sum = grad_block_sum(sum);
-    if (threadIdx.x == 0) {
-        if (norm)
-            put(norm, 0, 1, (float)sqrt(sum));
-        else
-            put(part, (int64_t)blockIdx.x, (int64_t)gridDim.x, sum);
+    if (!norm) {
+        if (threadIdx.x == 0) put(part, (int64_t)blockIdx.x, (int64_t)gridDim.x, sum);
+        return;
     }
+    __shared__ double mine;
+    if (threadIdx.x == 0) mine = sum;
+    cluster_sync_all();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        sum = 0.0;
+        for (uint32_t q = 0; q < gridDim.x; ++q) {
+            const uint32_t at = mapa_shared(smem_u32(&mine), q);
+            sum += __hiloint2double((int)ld_shared_cluster_u32(at + 4), (int)ld_shared_cluster_u32(at));
+        }
+        put(norm, 0, 1, (float)sqrt(sum));
+    }
+    cluster_sync_all();   // no block leaves while the first reads its sum
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_norm_end_kernel(const double *part, int n, float *norm) {

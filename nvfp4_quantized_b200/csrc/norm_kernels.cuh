@@ -175,8 +175,9 @@ struct NormArgs {
     int warps;           // forward: warps of a block that have rows
     int slots;           // forward, groups of threads: rows on their way
     float eps;
-    float *part;         // [splits][2][cols]
+    float *part;         // [splits][2][cols]; backward: null where neither dw nor db is wanted
     int splits;
+    int cluster;         // backward: the blocks of the launch are one cluster of so many, which needs no part
     void *dw, *db;
 };
 
@@ -574,6 +575,16 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const Norm
     }
 }
 
+// Column c of dw, or of db, where it is wanted.
+__device__ __forceinline__ void norm_put_weight(const NormArgs &a, bool bias, int c, float v) {
+    void *out = bias ? a.db : a.dw;
+    if (!out) return;
+    if (a.w_f32)
+        put(static_cast<float *>(out), (int64_t)c, (int64_t)a.cols, v);
+    else
+        put(static_cast<__nv_bfloat16 *>(out), (int64_t)c, (int64_t)a.cols, __float2bfloat16_rn(v));
+}
+
 // ---------------------------------------------------------------------------------------------
 // Backward, rows of up to 64 columns, one read of x and dy and one write of dx: G threads of a warp
 // a row, V vectors a thread, B rows at a time; the next rows are on their way while these are reduced and written.  A thread keeps its
@@ -915,14 +926,28 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
         }
     }
     __syncthreads();
-    float *part = a.part + (int64_t)blockIdx.x * 2 * cols;
+    float *const sums = reinterpret_cast<float *>(ring_all);   // the first group's: becomes the block's
     for (int c = threadIdx.x; c < 2 * cols; c += kGroups * G) {
         float t = 0.0f;
 #pragma unroll
         for (int q = 0; q < kGroups; ++q)
             t += reinterpret_cast<const float *>(ring_all + (size_t)q * S * B * 2 * row_bytes)[c];
-        put(a.part, part - a.part + c, (int64_t)a.splits * 2 * cols, t);
+        if (a.cluster)
+            sums[c] = t;
+        else
+            put(a.part, (int64_t)blockIdx.x * 2 * cols + c, (int64_t)a.splits * 2 * cols, t);
     }
+    if (!a.cluster) return;
+    // few rows: the launch is one cluster, whose blocks add up their sums a share of the columns each
+    cluster_sync_all();
+    const int rank = (int)cluster_ctarank();
+    for (int c = rank * kGroups * G + (int)threadIdx.x; c < 2 * cols; c += a.cluster * kGroups * G) {
+        float t = 0.0f;
+        for (int q = 0; q < a.cluster; ++q)
+            t += __uint_as_float(ld_shared_cluster_u32(mapa_shared(smem_u32(sums + c), q)));
+        norm_put_weight(a, c >= cols, c >= cols ? c - cols : c, t);
+    }
+    cluster_sync_all();   // no block leaves while another reads its sums
 }
 
 // dw (blockIdx.y = 0) or db: the sum of the partial sums, 32 columns a block, 32 slices of the
@@ -946,13 +971,7 @@ __global__ void __launch_bounds__(1024) layernorm_dw_kernel(const NormArgs a) {
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     const int d = blockIdx.x * 32 + slice;
     if ((threadIdx.x & 31) != 0 || d >= a.cols) return;
-    if (!QT2_STORE_OK(static_cast<uint8_t *>(out) + (int64_t)d * (a.w_f32 ? 4 : 2), a.w_f32 ? 4 : 2, out,
-                      (int64_t)a.cols * (a.w_f32 ? 4 : 2)))
-        return;
-    if (a.w_f32)
-        static_cast<float *>(out)[d] = t;
-    else
-        static_cast<__nv_bfloat16 *>(out)[d] = __float2bfloat16_rn(t);
+    norm_put_weight(a, blockIdx.y, d, t);
 }
 
 // ---------------------------------------------------------------------------------------------

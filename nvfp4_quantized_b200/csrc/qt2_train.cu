@@ -37,9 +37,9 @@ struct Same {
     using type = T;
 };
 template <class... P>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                   const typename Same<P>::type &...args) {
-    cudaLaunchAttribute attr[1];
+cudaError_t launch_cluster(void (*kernel)(P...), int cluster, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                           const typename Same<P>::type &...args) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
@@ -47,11 +47,22 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cu
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     c.attrs = attr;
-    c.numAttrs = 1;
+    c.numAttrs = cluster ? 2 : 1;   // 0: the kernel's own cluster, or none
     void *list[] = {const_cast<void *>(static_cast<const void *>(&args))...};
     return cudaLaunchKernelExC(&c, reinterpret_cast<const void *>(kernel), list);
 }
+template <class... P>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   const typename Same<P>::type &...args) {
+    return launch_cluster(kernel, 0, grid, threads, smem, s, args...);
+}
+
+// Blocks of a launch that is one cluster, for n shares of work.
+int cluster_blocks(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; }
 
 // ------------------------------------------------------------------------------- layer norm
 // Resident blocks of a kernel on this device, asked once a device.
@@ -149,16 +160,18 @@ cudaError_t norm_fwd(const NormArgs &a, cudaStream_t s) {
 // and its blocks: resident ones, since every block leaves a partial
 // sum of dw and db, and no more of them than it takes for every one to run as many steps (rows too
 // long: the slices of the rows that dw and db are summed in).
+// Rows of at most one step of eight blocks: one cluster of blocks, which add up dw and db themselves
+// (1 x 2048 bf16: 7.9 us, two launches 10.0; with two steps, 128 x 2048, 10.7 and 10.0).
 struct NormBwdPlan {
-    int threads, step, blocks;
+    int threads, step, blocks, cluster;
 };
 template <class T>
 NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
     auto ring = [](auto r) {
         using R = decltype(r);
-        return NormBwdPlan{32, R::kGroups * R::B, 148};
+        return NormBwdPlan{32, R::kGroups * R::B, 148, 0};
     };
-    NormBwdPlan p = cols <= 64      ? NormBwdPlan{8, 64, 148 * 2}
+    NormBwdPlan p = cols <= 64      ? NormBwdPlan{8, 64, 148 * 2, 0}
                     : cols <= 256   ? ring(NormRing<T, 32, 8>{})
                     : cols <= 512   ? ring(NormRing<T, 32, 16>{})
                     : cols <= 1024  ? ring(NormRing<T, 64, 16>{})
@@ -166,9 +179,14 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
                     : cols <= 4096  ? ring(NormRing<T, 256, 16>{})
                     : cols <= 8192  ? ring(NormRing<T, 512, 16>{})
                     : cols <= 16384 ? ring(NormRing<T, 512, 32>{})
-                                    : NormBwdPlan{0, 16, 64};
+                                    : NormBwdPlan{0, 16, 64, 0};
     const int64_t steps = ceil_div(rows, p.step);
     p.blocks = (int)ceil_div(steps, ceil_div(steps, p.blocks));
+    p.cluster = 0;
+    if (p.threads == 32 && steps <= 8) {
+        p.cluster = cluster_blocks(steps);
+        p.blocks = p.cluster;
+    }
     return p;
 }
 
@@ -187,8 +205,8 @@ cudaError_t launch_norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, R::bytes(R::kColumns));
     });
     if (e != cudaSuccess) return e;
-    return launch(layernorm_bwd_ring_kernel<T, G, C, WHOLE>, (unsigned)a.splits, R::kGroups * G, R::bytes(a.cols),
-                  s, a);
+    return launch_cluster(layernorm_bwd_ring_kernel<T, G, C, WHOLE>, a.cluster, (unsigned)a.splits, R::kGroups * G,
+                          R::bytes(a.cols), s, a);
 }
 template <class T, int G, int C>
 cudaError_t norm_bwd_ring(const NormArgs &a, cudaStream_t s) {
@@ -226,7 +244,7 @@ cudaError_t norm_bwd(const NormArgs &a, int threads, cudaStream_t s) {
             : a.cols <= 8192 ? norm_bwd_ring<T, 512, 16>(a, s)
                              : norm_bwd_ring<T, 512, 32>(a, s);
     }
-    if (e == cudaSuccess && a.part) e = launch_norm_dw(a, s);
+    if (e == cudaSuccess && a.part && !a.cluster) e = launch_norm_dw(a, s);
     return e;
 }
 
@@ -236,6 +254,9 @@ constexpr int kPairs = 74;
 // Of P.  8192 tokens, hidden 4096, vocabulary 128000, backward: pieces of 64 MB 20.3 ms, 256 MB 19.3 ms,
 // 512 MB 19.0 ms, 1 GB 18.8 ms (fewer passes over the sums of dx, fewer uneven ends of launches).
 constexpr int64_t kPieceBytes = 512 << 20;
+// Of x, what a group of the tokens' tiles shares while the vocabulary goes by: it has to stay in L2 (8192
+// tokens, hidden 4096: x in one group of 64 MB 5.68 ms, in two of 32 MB 5.44 ms, in four 5.84 ms, forward).
+constexpr int64_t kGroupBytes = 32 << 20;
 constexpr int kJobStages = 4;                // what a tile's start and end cost, in stages of K = 64
 
 struct XentPlan {
@@ -398,12 +419,14 @@ int grad_blocks(const GradTable<N> &t, int most) {
     const int chunks = t.first[t.count];
     return std::min(std::min(chunks, most), std::max(148 * 4, chunks / 4));
 }
-constexpr int kGradAlone = 8;          // chunks that one block reads faster than two launches take
+// Up to so many chunks the launch is one cluster of as many blocks, which forms the norm itself (40 chunks on
+// eight blocks: 16.3 us for norm and clipping, with a launch for the end 12.5).
+constexpr int kGradAlone = 8;
 
 template <int N>
 cudaError_t launch_grad_norm(const GradTable<N> &t, double *part, float *norm, int blocks, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    return launch(grad_norm_kernel<N>, blocks, kGradThreads, 0, s, t, part, norm);
+    return launch_cluster(grad_norm_kernel<N>, norm ? blocks : 0, blocks, kGradThreads, 0, s, t, part, norm);
 }
 cudaError_t launch_grad_norm_end(const double *part, int n, float *norm, cudaStream_t s) {
     QT2_LAUNCH_SITE();
@@ -423,7 +446,7 @@ cudaError_t grad_norm(const qt2_grad *grads, int64_t count, float *norm, double 
         at = grad_table(t, grads, at, count);
         if (t.count == 0) break;
         const bool alone = n == 0 && at == count && t.first[t.count] <= kGradAlone;
-        const int blocks = alone ? 1 : grad_blocks(t, kGradBlocks);
+        const int blocks = alone ? cluster_blocks(t.first[t.count]) : grad_blocks(t, kGradBlocks);
         const cudaError_t e = launch_grad_norm(t, part + n, alone ? norm : nullptr, blocks, s);
         if (e != cudaSuccess || alone) return e;
         n += blocks;
@@ -542,6 +565,7 @@ qt2_status qt2_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int x_
     const NormBwdPlan p = x_dtype == QT2_DTYPE_F32 ? norm_bwd_plan<float>(rows, cols)
                                                    : norm_bwd_plan<__nv_bfloat16>(rows, cols);
     a.splits = p.blocks;
+    a.cluster = p.cluster;
     a.dw = dweight;
     a.db = dbias;
     const cudaStream_t s = as_stream(stream);
@@ -587,6 +611,7 @@ qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targ
     a.hit = ws.hit;
     a.exact = ws.exact;
     a.num_m = (int)p.num_m;
+    a.group_m = (int)std::min<int64_t>(p.num_m, std::max<int64_t>(8, kGroupBytes / (512 * K)));
     a.num_n = (int)p.num_v;
     const cudaStream_t s = as_stream(stream);
     cudaError_t e = p.swap ? launch_mm<kLoss, true>(maps, a, p.num_v, s)
@@ -632,6 +657,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.dloss = dloss;
     a.P = ws.P;
     a.num_m = (int)p.num_m;
+    a.group_m = (int)std::min<int64_t>(p.num_m, std::max<int64_t>(8, kGroupBytes / (512 * K)));
     a.splits = p.splits;
     a.dx_m = (int)p.num_m;
     a.dx_n = (int)p.num_k;

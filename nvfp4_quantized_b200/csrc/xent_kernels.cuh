@@ -84,6 +84,7 @@ struct MmArgs {
     float *top;            // kProbs writes, kGrads reads: the largest |dloss|
     __nv_bfloat16 *P;      // [T][vw]
     int num_m, num_n;      // kLoss, kProbs: tiles of the tokens and of the vocabulary
+    int group_m;           // of the tokens' tiles, those that go with each tile of the vocabulary in turn
     int dx_jobs, splits, dx_m, dx_n;   // kGrads: dx's jobs come first: (split, row tile, column tile)
     int dw_jobs, lead;     // lead: dw jobs that a pair without an extra dx job is ahead
     int add;               // dx's sums hold earlier pieces
@@ -110,11 +111,13 @@ __device__ __forceinline__ bool mm_job(const MmArgs &a, int c, int pairs, int i,
     b.dw = false;
     b.ks = 0;
     if (MODE != kGrads) {
-        // along the tokens first: the tiles in flight then share all of x and few rows of w
-        const int j = c + i * pairs;
+        // along the tokens first, in groups of tiles: those in flight share the group's part of x and few rows of w
+        int j = c + i * pairs;
         if (j >= a.num_m * a.num_n) return false;
-        b.n = j / a.num_m;
-        b.m = j - b.n * a.num_m;
+        const int group = j / (a.group_m * a.num_n), first = group * a.group_m, rows = min(a.group_m, a.num_m - first);
+        j -= first * a.num_n;
+        b.n = j / rows;
+        b.m = first + j - b.n * rows;
         b.nk = (a.K + 63) >> 6;
         return true;
     }
