@@ -155,7 +155,11 @@ static qt2_status check_device() {
     return ok ? QT2_OK : QT2_ERR_DEVICE;
 }
 
-static qt2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QT2_OK : QT2_ERR_CUDA; }
+static qt2_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return QT2_OK;
+    cudaGetLastError();   // reported here, not by the caller's next CUDA call
+    return QT2_ERR_CUDA;
+}
 
 // Bump allocator over the caller's workspace.
 struct Carve {

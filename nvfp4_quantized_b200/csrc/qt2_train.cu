@@ -682,7 +682,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         cudaError_t e = p.swap ? launch_mm<kProbs, true>(maps, a, a.num_n, s)
                                  : launch_mm<kProbs, false>(maps, a, (int64_t)a.num_m * a.num_n, s);
         if (e == cudaSuccess) e = launch_mm<kGrads, false>(maps, a, (int64_t)a.dx_jobs + a.dw_jobs, s);
-        if (e != cudaSuccess) return QT2_ERR_CUDA;
+        if (e != cudaSuccess) return from_cuda(e);
     }
     if (!dx) return QT2_OK;
     a.splits = p.splits;

@@ -43,7 +43,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// exp(d) of a difference: taken before the factor log2(e), which would round numbers as large as the
+// logits (at 1e7 to halves).
+__device__ __forceinline__ float exp_of(float d) { return ex2(d * 1.4426950408889634f); }
 
 constexpr int kSwapN = 32;   // SWAP: its tiles' columns, the least that a pair's MMA takes
 template <bool SWAP>
@@ -218,14 +220,14 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
         float m = __uint_as_float(v[0]);
 #pragma unroll
         for (int i = 1; i < 128; ++i) m = fmaxf(m, __uint_as_float(v[i]));
-        const float sub = (m == -INFINITY ? 0.0f : m) * kLog2e;
+        const float ref = m == -INFINITY ? 0.0f : m;
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 128; i += 4) {
-            s0 += ex2(fmaf(__uint_as_float(v[i]), kLog2e, -sub));
-            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), kLog2e, -sub));
-            s2 += ex2(fmaf(__uint_as_float(v[i + 2]), kLog2e, -sub));
-            s3 += ex2(fmaf(__uint_as_float(v[i + 3]), kLog2e, -sub));
+            s0 += exp_of(__uint_as_float(v[i]) - ref);
+            s1 += exp_of(__uint_as_float(v[i + 1]) - ref);
+            s2 += exp_of(__uint_as_float(v[i + 2]) - ref);
+            s3 += exp_of(__uint_as_float(v[i + 3]) - ref);
         }
         put(a.part, (int64_t)(col >> 7) * a.T + row, (int64_t)a.parts * a.T, make_float2(m, (s0 + s1) + (s2 + s3)));
         const int y = xent_target(a, row) - col;
@@ -239,7 +241,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
     } else if (MODE == kProbs) {
         if (row >= a.T) return;
         const int y = xent_target(a, row);
-        const float g = y < 0 ? 0.0f : a.dloss[row] / scale, sub = a.lse[row] * kLog2e;
+        const float g = y < 0 ? 0.0f : a.dloss[row] / scale, lse = a.lse[row];
         const int at = y - (a.v0 + col), valid = a.V - (a.v0 + col);
         __nv_bfloat16 *dst = a.P + (int64_t)row * a.vw + col;
         if (!QT2_STORE_OK(dst, 256, a.P, (int64_t)a.T * a.vw * 2)) return;
@@ -252,7 +254,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int c = i + k + q;
-                    e[q] = ex2(fmaf(__uint_as_float(v[c]), kLog2e, -sub)) - (c == at ? 1.0f : 0.0f);
+                    e[q] = exp_of(__uint_as_float(v[c]) - lse) - (c == at ? 1.0f : 0.0f);
                     e[q] = (y < 0 || c >= valid) ? 0.0f : e[q] * g;
                 }
                 __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
@@ -350,7 +352,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
 // dloss as a share of the largest.
 struct SwapToken {
     int y;
-    float sub, g;
+    float lse, g;
 };
 __device__ __forceinline__ SwapToken *swap_table() {
     __shared__ SwapToken tokens[kSwapN];
@@ -363,7 +365,7 @@ __device__ __forceinline__ void swap_tokens(const MmArgs &a, int thread, float t
         if (thread < a.T) {
             t.y = xent_target(a, thread);
             if (MODE == kProbs) {
-                t.sub = a.lse[thread] * kLog2e;
+                t.lse = a.lse[thread];
                 t.g = t.y < 0 ? 0.0f : a.dloss[thread] / top;
             }
         }
@@ -393,13 +395,13 @@ __device__ __forceinline__ void swap_epilogue(const MmArgs &a, int v, int first,
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const float ref = m == -INFINITY ? 0.0f : m;
-            float s = ex2(fmaf(l, kLog2e, -ref * kLog2e));
+            float s = exp_of(l - ref);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (lane == k) sum = xent_join(sum, make_float2(m, s));
             if (v == token.y) put(a.hit, (int64_t)t, (int64_t)a.T, l);
         } else {
-            float e = ex2(fmaf(l, kLog2e, -token.sub)) - (a.v0 + v == token.y ? 1.0f : 0.0f);
+            float e = exp_of(l - token.lse) - (a.v0 + v == token.y ? 1.0f : 0.0f);
             e = token.y < 0 || !in ? 0.0f : e * token.g;
             __nv_bfloat16 *dst = a.P + (int64_t)t * a.vw + v;
             if (QT2_STORE_OK(dst, 2, a.P, (int64_t)a.T * a.vw * 2)) *dst = __float2bfloat16_rn(e);
@@ -651,17 +653,24 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, float *
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane != 0) return;
-    float l = ref + logf(sum);
+    // the loss from differences, so that it is as exact in rows of large logits
+    const float log_sum = logf(sum);
+    float l = ref + log_sum, out = (ref - tile) + log_sum;
     const float off = exact - tile;
-    if (in >= 0 && fabsf(off) < 1.0f) l += log1pf(__expf(tile - l) * expm1f(off));   // not for inf and NaN
+    if (in >= 0 && fabsf(off) < 16.0f) {   // not where one of them is inf or NaN
+        const float more = log1pf(__expf(-out) * expm1f(off));
+        l += more;
+        out += more - off;
+    }
     put(lse, (int64_t)row, (int64_t)a.T, l);
-    put(loss, (int64_t)row, (int64_t)a.T, in >= 0 ? l - exact : 0.0f);
+    put(loss, (int64_t)row, (int64_t)a.T, in >= 0 ? out : 0.0f);
     if (in < 0 && a.targets[row] != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
 }
 
-// dx = the sum of the splits' fp32 sums times the largest |dloss|, rounded to bf16.  One thread takes 8 columns of a row.
-__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const float *top, int T, int K, int splits, int64_t rows,
-                                                      int64_t ld, __nv_bfloat16 *dx, int64_t lddx) {
+// dx = the sum of the splits' fp32 sums times the largest |dloss|, rounded to bf16.  One thread takes 8
+// columns of a row.
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const float *top, int T, int K, int splits,
+                                                      int64_t rows, int64_t ld, __nv_bfloat16 *dx, int64_t lddx) {
     grid_dependency();
     const int vecs = (K + 7) >> 3;
     const int64_t n = (int64_t)T * vecs;
@@ -682,13 +691,7 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const fl
         const int valid = min(8, K - c);
         if (!QT2_STORE_OK(dst, valid * 2, dx, ((int64_t)(T - 1) * lddx + K) * 2)) continue;
         if (valid == 8) {
-            uint32_t p[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                p[k] = *reinterpret_cast<uint32_t *>(&b2);
-            }
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<uint4 *>(dst) = pack(v);
         } else {
             for (int k = 0; k < valid; ++k) dst[k] = __float2bfloat16_rn(v[k]);
         }

@@ -113,3 +113,68 @@ def test_step_in_a_graph_and_two_at_once():
     for s, w in zip((a, b), want):
         assert all(torch.equal(t, v) for t, v in zip(s.outputs(), w))
     assert qt2.qt2_device_status() == 0 and tr.qt2_train_device_status() == 0
+
+
+def test_between_copies_and_fills_in_a_graph():
+    """Nodes that are no kernels before and after each call of a captured graph."""
+    a = Step(3)
+    a.run()
+    want = [t.clone() for t in a.outputs()]
+    x = a.x.clone()
+    ws, n = a.ws, a.ws.numel()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        a.n1.zero_()
+        a.x.copy_(x)
+        tr.qt2_layernorm_fwd(a.x, M, D, D, a.g1, a.b1, EPS, a.n1, D, a.m1, a.r1)
+        qt2.qt2_linear_fwd(a.n1, a.w, M, D, H, a.z, ws, n)
+        tr.qt2_layernorm_fwd(a.z, M, H, H, a.g2, a.b2, EPS, a.n2, H, a.m2, a.r2)
+        a.loss.zero_()
+        tr.qt2_linear_xent_fwd(a.n2, a.head, a.y, M, H, V, H, H, IGN, a.loss, a.lse, ws, n)
+        ws.zero_()
+        tr.qt2_linear_xent_bwd(a.n2, a.head, a.y, a.lse, a.dloss, M, H, V, H, H, IGN, a.dn2, H, a.dhead, 1, H, ws, n)
+        keep = a.dn2.clone()
+        a.norm.zero_()
+        tr.qt2_grad_norm(a.grads, a.norm, ws, n)
+        norm = a.norm.clone()
+        a.norm.fill_(5.0)
+    a.x.zero_(), a.loss.fill_(9.0)
+    dn2 = a.dn2.clone()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a.loss, want[0]) and torch.equal(keep, dn2) and (a.norm == 5.0).all()
+    exact = sum(t.double().square().sum() for t in a.grads.grads).sqrt().item()
+    assert abs(norm.item() - exact) <= REL * exact
+
+
+def test_calls_from_several_threads():
+    """Host threads that call at once, each on a stream and workspace of its own."""
+    import threading
+    steps = [Step(k) for k in range(4)]
+    want = []
+    for s in steps:
+        s.run()
+        want.append([t.clone() for t in s.outputs()])
+        for t in s.outputs():
+            t.fill_(3.0)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(s):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    s.run()
+        except Exception as e:   # reported by the test, not lost with the thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(s,)) for s in steps]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for s, w in zip(steps, want):
+        assert all(torch.equal(a, b) for a, b in zip(s.outputs(), w))

@@ -228,3 +228,22 @@ def test_same_bits_again_on_two_streams_and_in_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first[0], outs[0]))
     assert tr.qt2_train_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_huge_logits(T):
+    """Logits of up to 1e7, where the tensor cores' sums are off by up to some units: a row that expects
+    its target has no loss.  (What remains is log1p(expm1(d)) - d of that d, here below 16: expm1 and
+    log1p are within 2 steps each, 2^-22 relative.)"""
+    K, V = 2048, 700
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = (torch.randn((V, K), generator=g, device="cuda") * 64).to(BF)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    x = w[y].clone()
+    loss, lse = forward(x, w, y)
+    (l, s), (el, es) = ref.xent(x, w, y, IGN)
+    ref.check(lse, s, es)
+    ref.check(loss, l, el)
+    assert (loss.abs() <= 18 * 2.0 ** -21).all()
+    dx, dw = backward(x, w, y, lse, torch.ones(T, device="cuda"))
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
