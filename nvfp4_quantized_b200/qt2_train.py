@@ -9,6 +9,7 @@ a tensor that is not on the current CUDA device, or of a type that the call does
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -216,36 +217,37 @@ class GradList:
     buffers that stay where they are; it keeps the tensors alive."""
 
     def __init__(self, grads, outs=None):
+        fn = "GradList"
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
-        self.count = len(self.grads)
-        self.c = (GradC * max(1, self.count))()
-        self.device = self.grads[0].get_device() if self.grads else -1
-        if len(self.outs) != self.count:
-            raise QT2Error("GradList", QT2_ERR_INVALID_ARG)
-        for d, g, o in zip(self.c, self.grads, self.outs):
-            kind = _dtype("GradList", g, o)
-            if g.numel() != o.numel() or not g.is_contiguous() or not o.is_contiguous():
-                raise QT2Error("GradList", QT2_ERR_INVALID_ARG)
-            if g.get_device() != self.device or o.get_device() != self.device:
-                raise QT2Error("GradList", QT2_ERR_DEVICE)
-            d.grad, d.out, d.numel, d.dtype = g.data_ptr(), o.data_ptr(), g.numel(), kind
+        self.count = n = len(self.grads)
+        both = self.grads if outs is None else self.grads + self.outs
+        kinds = [_DTYPE.get(t.dtype) for t in both]
+        if len(self.outs) != n or None in kinds or not all([t.is_contiguous() for t in both]):
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        devices = {t.get_device() for t in both}
+        if len(devices) > 1:
+            raise QT2Error(fn, QT2_ERR_DEVICE)
+        self.device = devices.pop() if devices else -1
+        at, numel = [t.data_ptr() for t in both], [t.numel() for t in both]
+        out = 0 if outs is None else n   # where the outputs begin
+        if numel[:n] != numel[out:] or kinds[:n] != kinds[out:]:
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
         # what one entry writes and another reads or writes too has no one value
-        spans = []
-        for d, g in zip(self.c, self.grads):
-            n = g.numel() * g.element_size()
-            if n:
-                spans.append((d.out, d.out + n, True))
-                if d.grad != d.out:
-                    spans.append((d.grad, d.grad + n, False))
+        spans = [(p, p + m * (4 if k else 2), 1) for p, m, k in zip(at[out:], numel, kinds) if m]
+        if out:
+            spans += [(p, p + m * (4 if k else 2), 0) for p, q, m, k in zip(at, at[n:], numel, kinds) if m and p != q]
+        spans.sort()
         written = read = 0   # ends of what has been seen
-        for lo, hi, writes in sorted(spans):
+        for lo, hi, writes in spans:
             if lo < written or (writes and lo < read):
-                raise QT2Error("GradList", QT2_ERR_INVALID_ARG)
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
             if writes:
-                written = max(written, hi)
-            else:
-                read = max(read, hi)
+                written = hi
+            elif hi > read:
+                read = hi
+        rows = array.array("q", [v for row in zip(at[:n], at[out:], numel, kinds) for v in row] or [0] * 4)
+        self.c = (GradC * max(1, n)).from_buffer(rows)   # the type is the lower half of the last number
         self.address = ctypes.addressof(self.c)
 
 
