@@ -3,6 +3,11 @@
 //   mean = sum x / C, rstd = 1/sqrt(sum (x - mean)^2 / C + eps), y = (x - mean) rstd w + b
 //   h = (x - mean) rstd, a = dy w:  dx = rstd (a - sum a / C - h sum(a h) / C)
 //   dw = sum_r dy h, db = sum_r dy
+//
+// HBM bounds all of it from some MB on, launches below.  Measured (B200, inputs larger than L2, a copy of as
+// many bytes at 6.0-6.4 TB/s): forward 16384 x 4096 bf16 50 us (5.4 TB/s), 32768 x 2048 bf16 46 us (5.9),
+// 16384 x 4096 fp32 85 us (6.3); backward 32768 x 2048 bf16 62 us for dx (6.4), 69 us with dw and db,
+// 16384 x 4096 fp32 121 and 127 us (6.7), 4096 x 16384 bf16 83 and 99 us (4.9).
 #pragma once
 
 #include <cuda_bf16.h>
