@@ -258,6 +258,8 @@ constexpr int64_t kPieceBytes = 512 << 20;
 // tokens, hidden 4096: x in one group of 64 MB 5.68 ms, in two of 32 MB 5.44 ms, in four 5.84 ms, forward).
 constexpr int64_t kGroupBytes = 32 << 20;
 constexpr int kJobStages = 4;                // what a tile's start and end cost, in stages of K = 64
+// A tile of dw takes its stages, or as long as its 128 KB (bf16) take to HBM: six stages' time.
+int64_t dw_job(int64_t T) { return std::max<int64_t>(ceil_div(T, 64), 6) + kJobStages; }
 
 struct XentPlan {
     int64_t num_m, num_v, num_k;   // 256-wide tiles of T, V and K
@@ -281,7 +283,7 @@ XentPlan xent_plan(int64_t T, int64_t K, int64_t V) {
     // dx's jobs are cut along the vocabulary where that shortens the launch: the pairs' even share
     // of its stages or the longest pair's dx jobs, and what the sums that each cut adds cost to write and read
     const int64_t nks = p.piece / 64, dx = p.num_m * p.num_k;
-    const int64_t dw = p.piece / 256 * p.num_k * (ceil_div(T, 64) + kJobStages);
+    const int64_t dw = p.piece / 256 * p.num_k * dw_job(T);
     double best = 0;
     for (int s = 1; s <= 16 && s * 16 <= std::max<int64_t>(16, nks); ++s) {
         const int64_t job = ceil_div(nks, s) + kJobStages;
@@ -676,7 +678,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
         a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
         a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;
-        a.lead = (int)((a.vw / 64 / a.splits + kJobStages) / (ceil_div(T, 64) + kJobStages));
+        a.lead = (int)((a.vw / 64 / a.splits + kJobStages) / dw_job(T));
         if (!encode_bf16(&maps.p_k, ws.P, a.vw, T, a.vw, 128) || !encode_bf16(&maps.p_mn, ws.P, a.vw, T, a.vw, 64))
             return QT2_ERR_CUDA;
         cudaError_t e = p.swap ? launch_mm<kProbs, true>(maps, a, a.num_n, s)
