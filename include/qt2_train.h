@@ -88,8 +88,9 @@ QT2_API qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64
  * (rounded once, 2^-8 at most relative to each entry) in the workspace while the tensor cores
  * multiply it, with fp32 sums over the whole of V (dx) and T (dw).  dloss enters P as a share of its
  * largest finite magnitude, which dx and dw are multiplied by at the end in fp32: equal dloss (a
- * mean) is not rounded.  Targets outside [0, V) count as ignore_index and are not reported again.  A zero row of P still
- * multiplies its row of x: x must be finite in rows without a target, too.
+ * mean) is not rounded.  Rows without a target add nothing to dw, whatever x holds there (inf and NaN
+ * included), and have dx 0 for finite w.  Targets outside [0, V) count as ignore_index and are not
+ * reported again.
  * dx or dw may be NULL (not wanted), not both.
  * Workspace: qt2_linear_xent_bwd_workspace_size() bytes, 256-byte aligned.
  * --------------------------------------------------------------------------------------- */

@@ -4,8 +4,8 @@
 //   h = (x - mean) rstd, a = dy w:  dx = rstd (a - sum a / C - h sum(a h) / C)
 //   dw = sum_r dy h, db = sum_r dy
 //
-// HBM bounds all of it from some MB on, launches below.  Measured (B200, inputs larger than L2, a copy of as
-// many bytes at 6.0-6.4 TB/s): forward 16384 x 4096 bf16 50 us (5.4 TB/s), 32768 x 2048 bf16 46 us (5.9),
+// HBM bounds all of it from some MB on, launches below.  Measured (B200, inputs larger than L2, a copy
+// of as many bytes at 6.0-6.4 TB/s): forward 16384 x 4096 bf16 50 us (5.4 TB/s), 32768 x 2048 bf16 46 us (5.9),
 // 16384 x 4096 fp32 85 us (6.3); backward 32768 x 2048 bf16 62 us for dx (6.4), 69 us with dw and db,
 // 16384 x 4096 fp32 121 and 127 us (6.7), 4096 x 16384 bf16 83 and 99 us (4.9).
 #pragma once
@@ -17,8 +17,6 @@
 
 namespace qt2 {
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <class T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -42,8 +40,8 @@ __device__ __forceinline__ void load_weight(const void *w, int f32, int c, int c
     } else if (f32) {
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-            const float4 q = c + e < cols ? __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + e))
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + e);
+            const float4 q = c + e < cols ? __ldg(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
         }
     } else if constexpr (E == 8) {
@@ -283,13 +281,13 @@ __global__ void __launch_bounds__(256) layernorm_fwd_short_kernel(const NormArgs
 }
 
 // ---------------------------------------------------------------------------------------------
-// Forward, a warp a row (short rows: B of them at a time), V vectors of 16 bytes a lane: one read and one write of HBM, no barrier
-// between rows.  A bulk copy brings a warp's next row into its part of shared memory while this row,
-// in packed registers, goes through its three passes (mean, squared differences, result): without
-// it every warp waits for its row, then computes, and HBM idles meanwhile (16384 x 4096 bf16: 58 us).
-// Weights and biases wait in shared memory as fp32, the vectors' first and second halves apart, so
-// that a warp's 16-byte reads touch every bank once; read from global memory for each row they
-// cost more L1 wavefronts than the row itself.
+// Forward, a warp a row (short rows: B of them at a time), V vectors of 16 bytes a lane: one read and
+// one write of HBM, no barrier between rows.  A bulk copy brings a warp's next row into its part of
+// shared memory while this row, in packed registers, goes through its three passes (mean, squared
+// differences, result): without it every warp waits for its row, then computes, and HBM idles meanwhile
+// (16384 x 4096 bf16: 58 us).  Weights and biases wait in shared memory as fp32, the vectors' first and
+// second halves apart, so that a warp's 16-byte reads touch every bank once; read from global memory
+// for each row they cost more L1 wavefronts than the row itself.
 // ---------------------------------------------------------------------------------------------
 template <class T>
 __host__ __device__ inline int norm_row_bytes(int cols) { return (cols * (int)sizeof(T) + 15) / 16 * 16; }
@@ -540,7 +538,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_group_kernel(const Norm
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     const float2 x = f2_get(v[e]);
-                    const uint64_t d = f2(c + 2 * e < cols ? x.x - mean : 0.0f, c + 2 * e + 1 < cols ? x.y - mean : 0.0f);
+                    const uint64_t d = f2(c + 2 * e < cols ? x.x - mean : 0.0f,
+                                          c + 2 * e + 1 < cols ? x.y - mean : 0.0f);
                     s2 = f2_fma(d, d, s2);
                 }
             }
@@ -591,12 +590,12 @@ __device__ __forceinline__ void norm_put_weight(const NormArgs &a, bool bias, in
 }
 
 // ---------------------------------------------------------------------------------------------
-// Backward, rows of up to 64 columns, one read of x and dy and one write of dx: G threads of a warp
-// a row, V vectors a thread, B rows at a time; the next rows are on their way while these are reduced and written.  A thread keeps its
-// columns (and their weights) for all of the block's rows and sums their dw and db in registers; a
-// block leaves one partial sum a column, which layernorm_dw_kernel adds up.  With d = x - mean
-// the row's sums are sum(a) and sum(a d), and
-//   dx = rstd a - (rstd^3 sum(a d) / C) d - rstd sum(a) / C.
+// Backward, rows of up to 64 columns, one read of x and dy and one write of dx: G threads of a warp a
+// row, V vectors a thread, B rows at a time; the next rows are on their way while these are reduced and
+// written.  A thread keeps its columns (and their weights) for all of the block's rows and sums their
+// dw and db in registers; a block leaves one partial sum a column, which layernorm_dw_kernel adds up.
+// With d = x - mean the row's sums are sum(a) and sum(a d), and dx = rstd a - (rstd^3 sum(a d) / C) d -
+// rstd sum(a) / C.
 // ---------------------------------------------------------------------------------------------
 template <class T, int G, int V, int B>
 __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a) {

@@ -67,7 +67,8 @@ int cluster_blocks(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8;
 // ------------------------------------------------------------------------------- layer norm
 // Resident blocks of a kernel on this device, asked once a device.
 template <class F>
-cudaError_t resident_blocks(PerDeviceOnce &once, std::atomic<int> *blocks, F kernel, int threads, int smem, int64_t *n) {
+cudaError_t resident_blocks(PerDeviceOnce &once, std::atomic<int> *blocks, F kernel, int threads, int smem,
+                            int64_t *n) {
     const cudaError_t e = once.run([&] {
         int v = 0;
         const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, smem);
@@ -86,7 +87,8 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
     auto smem = [](int warps) { return 32 * V * 16 * (8 / (int)sizeof(T) + B * warps); };
     int64_t n = 0;
     cudaError_t e = attr.run([&] {
-        return cudaFuncSetAttribute(layernorm_fwd_kernel<T, V, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(8));
+        return cudaFuncSetAttribute(layernorm_fwd_kernel<T, V, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    smem(8));
     });
     if (e == cudaSuccess) e = resident_blocks(once, blocks, layernorm_fwd_kernel<T, V, B>, 256, smem(8), &n);
     if (e != cudaSuccess) return e;
@@ -312,14 +314,15 @@ XentFwdWs xent_fwd_ws(const XentPlan &p, int64_t T, void *ws) {
     return w;
 }
 struct XentBwdWs {
-    __nv_bfloat16 *P;
+    __nv_bfloat16 *P, *xs;
     float *acc, *top;
     size_t bytes;
 };
-XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, void *ws) {
+XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, int64_t K, void *ws) {
     Carve c(ws);
     XentBwdWs w;
     w.P = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * p.piece * 2));
+    w.xs = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * ceil_div(K, 64) * 128));
     w.top = reinterpret_cast<float *>(c.take(sizeof(float)));
     w.acc = reinterpret_cast<float *>(c.take((size_t)p.splits * p.num_m * p.num_k * 65536 * sizeof(float)));
     w.bytes = c.used;
@@ -341,7 +344,8 @@ cudaError_t launch_mm(const MmMaps &maps, const MmArgs &a, int64_t jobs, cudaStr
     });
     if (e != cudaSuccess) return e;
     const int64_t clusters = std::min<int64_t>(jobs, kPairs);
-    return launch(mm_pair_kernel<MODE, SWAP>, (unsigned)(2 * clusters), MmCfg<SWAP>::kThreads, MmCfg<SWAP>::kSmemBytes, s, maps, a);
+    return launch(mm_pair_kernel<MODE, SWAP>, (unsigned)(2 * clusters), MmCfg<SWAP>::kThreads,
+                  MmCfg<SWAP>::kSmemBytes, s, maps, a);
 }
 
 cudaError_t launch_xent_loss(const MmArgs &a, float *loss, float *lse, cudaStream_t s) {
@@ -625,7 +629,7 @@ qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64_t *targ
 qt2_status qt2_linear_xent_bwd_workspace_size(int64_t T, int64_t K, int64_t V, size_t *bytes) {
     if (!bytes) return QT2_ERR_INVALID_ARG;
     if (!xent_dims_ok(T, K, V)) return QT2_ERR_SHAPE;
-    *bytes = xent_bwd_ws(xent_plan(T, K, V), T, nullptr).bytes;
+    *bytes = xent_bwd_ws(xent_plan(T, K, V), T, K, nullptr).bytes;
     return QT2_OK;
 }
 
@@ -641,12 +645,12 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         (dw && (!aligned(dw, 16) || lddw % 8)))
         return QT2_ERR_ALIGN;
     const XentPlan p = xent_plan(T, K, V);
-    if (const qt2_status st = check_workspace(workspace, ws_bytes, xent_bwd_ws(p, T, nullptr).bytes)) return st;
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, xent_bwd_ws(p, T, K, nullptr).bytes)) return st;
     if (const qt2_status st = check_device()) return st;
-    const XentBwdWs ws = xent_bwd_ws(p, T, workspace);
+    const XentBwdWs ws = xent_bwd_ws(p, T, K, workspace);
     MmMaps maps{};
     if (!encode_bf16(&maps.x_k, x, K, T, ldx, p.swap ? kSwapN / 2 : 128) ||
-        !encode_bf16(&maps.w_k, w, K, V, ldw, 128) || !encode_bf16(&maps.x_mn, x, K, T, ldx, 64) ||
+        !encode_bf16(&maps.w_k, w, K, V, ldw, 128) || !encode_bf16(&maps.x_mn, ws.xs, K, T, ceil_div(K, 64) * 64, 64) ||
         !encode_bf16(&maps.w_mn, w, K, V, ldw, 64))
         return QT2_ERR_CUDA;
     MmArgs a{};
@@ -665,6 +669,9 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.dx_n = (int)p.num_k;
     a.acc = ws.acc;
     a.top = ws.top;
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.ldx = ldx;
+    a.ldxs = ceil_div(K, 64) * 64;
     a.dw = dw;
     a.lddw = lddw;
     a.dw_f32 = dw_dtype == QT2_DTYPE_F32;
@@ -675,6 +682,7 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         a.vw = (int)std::min<int64_t>(p.piece, p.num_v * 256 - a.v0);
         a.num_n = a.vw / 256;
         a.add = i > 0;
+        a.xs = dw && i == 0 ? ws.xs : nullptr;
         a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
         a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
         a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;

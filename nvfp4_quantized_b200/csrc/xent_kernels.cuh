@@ -15,8 +15,8 @@
 //           L2 lines (32000 x 2048: 44 us for 1 token, 38 us for 16, 32 us for 32; swapped 28, 32 and 35).
 //   kGrads  jobs of both gradient products in one launch: dx (A = P, B = w with the vocabulary
 //           contracted, so w is read transposed: an MN-major operand) added up over the pieces in
-//           fp32, and dw (A = P transposed, B = x transposed), whose rows are complete after their
-//           piece.
+//           fp32, and dw (A = P transposed, B = a copy of x transposed), whose rows are complete
+//           after their piece.
 //
 // Tensor cores bound it, and over longer times the power limit: at 2048 x 2048 x 32000 the tensor pipes
 // are active for 95 / 93 / 97% of the three kernels' cycles; forward 4096 x 2048 x 50257 0.50 ms at full
@@ -86,8 +86,10 @@ struct MmArgs {
     const float *lse, *dloss;   // kProbs
     float2 *part;          // kLoss: [parts][T]
     int parts;
-    const __nv_bfloat16 *x, *w;   // kLoss, for the targets' logits
+    const __nv_bfloat16 *x, *w;   // kLoss, for the targets' logits; kProbs, x for its copy
     int64_t ldx, ldw;
+    __nv_bfloat16 *xs;     // kProbs, first piece, where dw is wanted: x with zeros in rows without a target
+    int64_t ldxs;
     float *hit, *exact;    // kLoss: the target's logit as the tile has it, and formed in fp32
     float *top;            // kProbs writes, kGrads reads: the largest |dloss|
     __nv_bfloat16 *P;      // [T][vw]
@@ -182,6 +184,18 @@ __device__ __forceinline__ void xent_exact(const MmArgs &a, int64_t t, int y, in
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
     if (lane == 0) put(a.exact, t, (int64_t)a.T, h);
+}
+
+// Row t of x, or zeros where it has no target: what a padded row holds, inf and NaN among it, must not
+// reach dw through a product with a zero of P.  (The copy's rows start 128-byte aligned.)
+__device__ __forceinline__ void xent_copy(const MmArgs &a, int64_t t, int lane) {
+    const bool live = xent_target(a, t) >= 0;
+#pragma unroll 4
+    for (int k = lane * 8; k < a.K; k += 256) {
+        const uint4 v = live ? *reinterpret_cast<const uint4 *>(a.x + t * a.ldx + k) : make_uint4(0, 0, 0, 0);
+        __nv_bfloat16 *dst = a.xs + t * a.ldxs + k;
+        if (QT2_STORE_OK(dst, 16, a.xs, (int64_t)a.T * a.ldxs * 2)) *reinterpret_cast<uint4 *>(dst) = v;
+    }
 }
 
 // Two (max, sum of exp) pairs as one.
@@ -552,6 +566,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
             const int y = xent_target(a, t);
             if (y >= 0) xent_exact(a, t, y, lane);
         }
+    } else if (MODE == kProbs && a.xs && (warp == 2 || warp == 3)) {
+        // -------------------------------------------------------------- x for dw, a warp a row
+        for (int64_t t = (int64_t)blockIdx.x * 2 + (warp & 1); t < a.T; t += (int64_t)gridDim.x * 2)
+            xent_copy(a, t, lane);
     } else if (warp >= Cfg::kEpiWarp0) {
         // -------------------------------------------------------------- epilogue (both CTAs)
         // Warp w reads TMEM lane quadrant w % 4, columns [0, 128) for warps 4..7 and [128, 256)

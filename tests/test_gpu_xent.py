@@ -106,9 +106,15 @@ def test_rows_without_a_target():
     loss2, lse2 = forward(x, w, y)
     dx2, dw2 = backward(x, w, y, lse2, dloss)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and (loss2[::3] == 0).all() and (dx2[::3] == 0).all()
+    # nor does what x holds there reach a gradient
+    bad = ref.rows_like(300, 64, BF, fill=float("nan"))[0].copy_(x)
+    bad[::6], bad[3::6] = float("nan"), float("inf")
+    loss3, lse3 = forward(bad, w, y)
+    dx3, dw3 = backward(bad, w, y, lse3, dloss)
+    assert torch.equal(loss3, loss2) and torch.equal(dx3, dx2) and torch.equal(dw3, dw2)
     y[:] = IGN
-    loss, lse = forward(x, w, y)
-    dx, dw = backward(x, w, y, lse, dloss)
+    loss, lse = forward(bad, w, y)
+    dx, dw = backward(bad, w, y, lse, dloss)
     assert (loss == 0).all() and (dx == 0).all() and (dw == 0).all()
     assert tr.qt2_train_device_status() == 0
 
