@@ -84,11 +84,11 @@ QT2_API qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64
  * Gradient of sum_t dloss_t loss_t, from the forward pass's lse and the same inputs:
  *   P_tv = dloss_t * (exp(l_tv - lse_t) - [v = target(t)])   (0 in rows without a target),
  *   dx = P w  [T][K] bf16,  dw = P^T x  [V][K] of type dw_dtype.
- * The logits are formed again, a piece of the vocabulary at a time; the piece's P is held in bf16
- * (rounded once, 2^-8 at most relative to each entry) in the workspace while the tensor cores
- * multiply it, with fp32 sums over the whole of V (dx) and T (dw).  dloss enters P as a share of its
- * largest finite magnitude, which dx and dw are multiplied by at the end in fp32: equal dloss (a
- * mean) is not rounded.  Rows without a target add nothing to dw, whatever x holds there (inf and NaN
+ * The logits are formed again, a piece of the vocabulary at a time; the piece's P, each row divided
+ * by the probability that is not its target's, is held in bf16 (rounded once, 2^-8 at most relative
+ * to each entry, the target's entry exact) in the workspace while the tensor cores multiply it, with
+ * fp32 sums over the whole of V (dx) and T (dw).  dloss and that factor multiply dx's rows in fp32, and
+ * x's for dw (rounded to bf16 an element at a time).  Rows without a target add nothing to dw, whatever x holds there (inf and NaN
  * included), and have dx 0 for finite w.  Targets outside [0, V) count as ignore_index and are not
  * reported again.
  * dx or dw may be NULL (not wanted), not both.

@@ -315,7 +315,8 @@ XentFwdWs xent_fwd_ws(const XentPlan &p, int64_t T, void *ws) {
 }
 struct XentBwdWs {
     __nv_bfloat16 *P, *xs;
-    float *acc, *top;
+    XentRow *rows;
+    float *acc;
     size_t bytes;
 };
 XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, int64_t K, void *ws) {
@@ -323,7 +324,7 @@ XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, int64_t K, void *ws) {
     XentBwdWs w;
     w.P = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * p.piece * 2));
     w.xs = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * ceil_div(K, 64) * 128));
-    w.top = reinterpret_cast<float *>(c.take(sizeof(float)));
+    w.rows = reinterpret_cast<XentRow *>(c.take((size_t)T * sizeof(XentRow)));
     w.acc = reinterpret_cast<float *>(c.take((size_t)p.splits * p.num_m * p.num_k * 65536 * sizeof(float)));
     w.bytes = c.used;
     return w;
@@ -353,11 +354,16 @@ cudaError_t launch_xent_loss(const MmArgs &a, float *loss, float *lse, cudaStrea
     return launch(xent_loss_kernel, (unsigned)ceil_div(a.T, 32), 1024, 0, s, a, loss, lse);
 }
 
+cudaError_t launch_xent_rows(const MmArgs &a, const float *lse, const float *dloss, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    return launch(xent_rows_kernel, (unsigned)ceil_div(a.T, 8), 256, 0, s, a, lse, dloss);
+}
+
 cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     const int64_t n = (int64_t)a.T * ceil_div(a.K, 8);
     const int64_t blocks = std::min<int64_t>(ceil_div(n, 256), (int64_t)sm_count() * 16);
-    return launch(xent_dx_kernel, (unsigned)blocks, 256, 0, s, a.acc, a.top, a.T, a.K, a.splits,
+    return launch(xent_dx_kernel, (unsigned)blocks, 256, 0, s, a.acc, a.rows, a.T, a.K, a.splits,
                   (int64_t)a.dx_m * 256, (int64_t)a.dx_n * 256, static_cast<__nv_bfloat16 *>(dx), lddx);
 }
 
@@ -659,8 +665,6 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.V = (int)V;
     a.targets = targets;
     a.ignore = ignore_index;
-    a.lse = lse;
-    a.dloss = dloss;
     a.P = ws.P;
     a.num_m = (int)p.num_m;
     a.group_m = (int)std::min<int64_t>(p.num_m, std::max<int64_t>(8, kGroupBytes / (512 * K)));
@@ -668,21 +672,24 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.dx_m = (int)p.num_m;
     a.dx_n = (int)p.num_k;
     a.acc = ws.acc;
-    a.top = ws.top;
+    a.rows = ws.rows;
+    a.xs = dw ? ws.xs : nullptr;
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.ldx = ldx;
     a.ldxs = ceil_div(K, 64) * 64;
+    a.w = static_cast<const __nv_bfloat16 *>(w);
+    a.ldw = ldw;
     a.dw = dw;
     a.lddw = lddw;
     a.dw_f32 = dw_dtype == QT2_DTYPE_F32;
     a.dw_wide = aligned(dw, 32) && lddw * (a.dw_f32 ? 4 : 2) % 32 == 0;
     const cudaStream_t s = as_stream(stream);
+    if (const cudaError_t e = launch_xent_rows(a, lse, dloss, s)) return from_cuda(e);
     for (int i = 0; i < p.pieces; ++i) {
         a.v0 = (int)(i * p.piece);
         a.vw = (int)std::min<int64_t>(p.piece, p.num_v * 256 - a.v0);
         a.num_n = a.vw / 256;
         a.add = i > 0;
-        a.xs = dw && i == 0 ? ws.xs : nullptr;
         a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
         a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
         a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;

@@ -1,7 +1,13 @@
 // xent_kernels.cuh -- the head's softmax cross entropy without its logits.
 //
 //   l = x w^T, lse_t = log sum_v exp l_tv, loss_t = lse_t - l_t,y(t)          (forward)
-//   P_tv = dloss_t (exp(l_tv - lse_t) - [v = y(t)]), dx = P w, dw = P^T x     (backward)
+//   G_tv = dloss_t (exp(l_tv - lse_t) - [v = y(t)]), dx = G w, dw = G^T x     (backward)
+//
+// The tensor cores take G as c_t P_tv: with q_t = 1 - exp(l_t,y(t) - lse_t), the rest of the row's
+// probability, c_t = dloss_t q_t and P_tv = exp(l_tv - lse_t) / q_t, -1 at the target.  P's largest entry
+// is then exact in bf16 and the others' roundings independent; c_t multiplies dx's rows in fp32, and
+// x's for dw (c x in bf16, rounded an element at a time).  Rounded as it stands, G's entry at the
+// target is off by up to 2^-8 in all of dx's row, and equal dloss in all rows alike.
 //
 // All three products are bf16 with fp32 sums on the tensor cores, in one persistent kernel shape
 // (mm_pair_kernel): a pair of SMs forms 256x256 tiles with tcgen05.mma.cta_group::2, each SM
@@ -78,20 +84,24 @@ struct MmMaps {
     CUtensorMap x_k, w_k, p_k, x_mn, w_mn, p_mn;
 };
 
+// What the backward pass needs of a row: lse, 1 / q (0: no target), P's entry at the target, c.
+struct __align__(16) XentRow {
+    float lse, inv, at, c;
+};
+
 struct MmArgs {
     int T, K, V;
     int v0, vw;            // the piece: its first vocabulary entry and its width (a multiple of 256)
     const int64_t *targets;
     int64_t ignore;
-    const float *lse, *dloss;   // kProbs
     float2 *part;          // kLoss: [parts][T]
     int parts;
-    const __nv_bfloat16 *x, *w;   // kLoss, for the targets' logits; kProbs, x for its copy
+    const __nv_bfloat16 *x, *w;   // for the targets' logits
     int64_t ldx, ldw;
-    __nv_bfloat16 *xs;     // kProbs, first piece, where dw is wanted: x with zeros in rows without a target
+    __nv_bfloat16 *xs;     // backward, where dw is wanted: c x, zeros in rows without a target
     int64_t ldxs;
+    XentRow *rows;         // backward: [T]
     float *hit, *exact;    // kLoss: the target's logit as the tile has it, and formed in fp32
-    float *top;            // kProbs writes, kGrads reads: the largest |dloss|
     __nv_bfloat16 *P;      // [T][vw]
     int num_m, num_n;      // kLoss, kProbs: tiles of the tokens and of the vocabulary
     int group_m;           // of the tokens' tiles, those that go with each tile of the vocabulary in turn
@@ -166,7 +176,7 @@ __device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
 
 // The target's logit again, in fp32 with short sums, by one warp: the tensor cores' long ones lose up
 // to 1e-5 of it (K = 4096), which the loss of a row that expects its target otherwise shows in full.
-__device__ __forceinline__ void xent_exact(const MmArgs &a, int64_t t, int y, int lane) {
+__device__ __forceinline__ float xent_exact(const MmArgs &a, int64_t t, int y, int lane) {
     const __nv_bfloat16 *x = a.x + t * a.ldx, *w = a.w + (int64_t)y * a.ldw;
     float h = 0.0f;
 #pragma unroll 4
@@ -183,16 +193,39 @@ __device__ __forceinline__ void xent_exact(const MmArgs &a, int64_t t, int y, in
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
-    if (lane == 0) put(a.exact, t, (int64_t)a.T, h);
+    return h;
 }
 
-// Row t of x, or zeros where it has no target: what a padded row holds, inf and NaN among it, must not
-// reach dw through a product with a zero of P.  (The copy's rows start 128-byte aligned.)
-__device__ __forceinline__ void xent_copy(const MmArgs &a, int64_t t, int lane) {
-    const bool live = xent_target(a, t) >= 0;
+// Backward, before the pieces: what each row needs (XentRow), and c x for dw.  A warp a row.  What
+// a row without a target holds, inf and NaN among it, must not reach dw through a product with a zero of
+// P: its copy is zero.
+__global__ void __launch_bounds__(256) xent_rows_kernel(const MmArgs a, const float *lse, const float *dloss) {
+    grid_dependency();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const int y = xent_target(a, t);
+    XentRow r{lse[t], 0.0f, 0.0f, 0.0f};
+    if (y >= 0) {
+        // q from the exponent's difference; at least 2^-24, what a sum of fp32 probabilities resolves
+        const float q = -expm1f(xent_exact(a, t, y, lane) - r.lse), least = q < 0x1p-24f ? 0x1p-24f : q;
+        r.inv = 1.0f / least;
+        r.at = -(q < 0.0f ? 0.0f : q) * r.inv;
+        if (q >= 0x1p-24f) r.at = -1.0f;
+        r.c = dloss[t] * least;
+    }
+    if (lane == 0) put(a.rows, t, (int64_t)a.T, r);
+    if (!a.xs) return;
 #pragma unroll 4
     for (int k = lane * 8; k < a.K; k += 256) {
-        const uint4 v = live ? *reinterpret_cast<const uint4 *>(a.x + t * a.ldx + k) : make_uint4(0, 0, 0, 0);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (y >= 0) {
+            float f[8];
+            unpack(*reinterpret_cast<const uint4 *>(a.x + t * a.ldx + k), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= r.c;
+            v = pack(f);
+        }
         __nv_bfloat16 *dst = a.xs + t * a.ldxs + k;
         if (QT2_STORE_OK(dst, 16, a.xs, (int64_t)a.T * a.ldxs * 2)) *reinterpret_cast<uint4 *>(dst) = v;
     }
@@ -204,31 +237,9 @@ __device__ __forceinline__ float2 xent_join(const float2 &p, const float2 &q) {
     return make_float2(m, p.y * __expf(p.x - ref) + q.y * __expf(q.x - ref));
 }
 
-// The largest finite |dloss| of a row with a target (1 where all are 0), the same in the epilogue's 256
-// threads.  P holds dloss as a share of it, so that equal ones (the mean of a loss) are exactly 1 there:
-// rounded to bf16 with P, one value for all rows would be off by up to 2^-8 in all of dx and dw.
-__device__ __forceinline__ float xent_top(const MmArgs &a, int thread) {
-    __shared__ float sh[8];
-    float m = 0.0f;
-    for (int t = thread; t < a.T; t += 256) {
-        const float g = fabsf(a.dloss[t]);
-        if (g < INFINITY && xent_target(a, t) >= 0) m = fmaxf(m, g);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((thread & 31) == 0) sh[thread >> 5] = m;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, sh[i]);
-    if (m == 0.0f) m = 1.0f;
-    if (thread == 0 && blockIdx.x == 0) put(a.top, 0, 1, m);
-    return m;
-}
-
 // What becomes of a tile: the thread holds columns [col, col + 128) of the tile's row `row`.
 template <int MODE>
-__device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col,
-                                            float scale) {
+__device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col) {
     if (MODE == kLoss) {
         if (row >= a.T) return;
         const int valid = a.V - col;   // columns of the vocabulary from here on
@@ -261,7 +272,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
     } else if (MODE == kProbs) {
         if (row >= a.T) return;
         const int y = xent_target(a, row);
-        const float g = y < 0 ? 0.0f : a.dloss[row] / scale, lse = a.lse[row];
+        const XentRow r = a.rows[row];
         const int at = y - (a.v0 + col), valid = a.V - (a.v0 + col);
         __nv_bfloat16 *dst = a.P + (int64_t)row * a.vw + col;
         if (!QT2_STORE_OK(dst, 256, a.P, (int64_t)a.T * a.vw * 2)) return;
@@ -274,8 +285,8 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int c = i + k + q;
-                    e[q] = exp_of(__uint_as_float(v[c]) - lse) - (c == at ? 1.0f : 0.0f);
-                    e[q] = (y < 0 || c >= valid) ? 0.0f : e[q] * g;
+                    e[q] = exp_of(__uint_as_float(v[c]) - r.lse) * r.inv;
+                    e[q] = c == at ? r.at : (y < 0 || c >= valid) ? 0.0f : e[q];
                 }
                 __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
                 p[k >> 1] = *reinterpret_cast<uint32_t *>(&b2);
@@ -316,7 +327,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                 if (a.dw_wide && i + 8 <= n) {
                     uint32_t p[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) p[k] = __float_as_uint(__uint_as_float(v[i + k]) * scale);
+                    for (int k = 0; k < 8; ++k) p[k] = __float_as_uint(__uint_as_float(v[i + k]));
                     st_global_v8(dst + i, p);
                     continue;
                 }
@@ -325,12 +336,12 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                     if (j + 4 <= n) {
                         float f[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[j + k]) * scale;
+                        for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[j + k]);
                         *reinterpret_cast<uint4 *>(dst + j) = pack(f);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (j + k < n) dst[j + k] = __uint_as_float(v[j + k]) * scale;
+                            if (j + k < n) dst[j + k] = __uint_as_float(v[j + k]);
                     }
                 }
             }
@@ -343,8 +354,8 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                     uint32_t p[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]) * scale,
-                                                                  __uint_as_float(v[i + 2 * k + 1]) * scale);
+                        __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]),
+                                                                  __uint_as_float(v[i + 2 * k + 1]));
                         p[k] = *reinterpret_cast<uint32_t *>(&b2);
                     }
                     st_global_v8(dst + i, p);
@@ -355,12 +366,12 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                     if (j + 8 <= n) {
                         float f[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[j + k]) * scale;
+                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[j + k]);
                         *reinterpret_cast<uint4 *>(dst + j) = pack(f);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            if (j + k < n) dst[j + k] = __float2bfloat16_rn(__uint_as_float(v[j + k]) * scale);
+                            if (j + k < n) dst[j + k] = __float2bfloat16_rn(__uint_as_float(v[j + k]));
                     }
                 }
             }
@@ -368,26 +379,22 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
     }
 }
 
-// SWAP: what a token's column needs, for the epilogue's threads: its target, and for kProbs lse and
-// dloss as a share of the largest.
+// SWAP: what a token's column needs, for the epilogue's threads.
 struct SwapToken {
     int y;
-    float lse, g;
+    XentRow row;
 };
 __device__ __forceinline__ SwapToken *swap_table() {
     __shared__ SwapToken tokens[kSwapN];
     return tokens;
 }
 template <int MODE>
-__device__ __forceinline__ void swap_tokens(const MmArgs &a, int thread, float top) {
+__device__ __forceinline__ void swap_tokens(const MmArgs &a, int thread) {
     if (thread < kSwapN) {
-        SwapToken t{-1, 0.0f, 0.0f};
+        SwapToken t{-1, {}};
         if (thread < a.T) {
             t.y = xent_target(a, thread);
-            if (MODE == kProbs) {
-                t.lse = a.lse[thread];
-                t.g = t.y < 0 ? 0.0f : a.dloss[thread] / top;
-            }
+            if (MODE == kProbs) t.row = a.rows[thread];
         }
         swap_table()[thread] = t;
     }
@@ -421,8 +428,8 @@ __device__ __forceinline__ void swap_epilogue(const MmArgs &a, int v, int first,
             if (lane == k) sum = xent_join(sum, make_float2(m, s));
             if (v == token.y) put(a.hit, (int64_t)t, (int64_t)a.T, l);
         } else {
-            float e = exp_of(l - token.lse) - (a.v0 + v == token.y ? 1.0f : 0.0f);
-            e = token.y < 0 || !in ? 0.0f : e * token.g;
+            float e = exp_of(l - token.row.lse) * token.row.inv;
+            e = a.v0 + v == token.y ? token.row.at : token.y < 0 || !in ? 0.0f : e;
             __nv_bfloat16 *dst = a.P + (int64_t)t * a.vw + v;
             if (QT2_STORE_OK(dst, 2, a.P, (int64_t)a.T * a.vw * 2)) *dst = __float2bfloat16_rn(e);
         }
@@ -564,12 +571,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
         // -------------------------------------------------------------- the targets' logits, a warp a row
         for (int64_t t = (int64_t)blockIdx.x * 2 + (warp & 1); t < a.T; t += (int64_t)gridDim.x * 2) {
             const int y = xent_target(a, t);
-            if (y >= 0) xent_exact(a, t, y, lane);
+            if (y < 0) continue;
+            const float h = xent_exact(a, t, y, lane);
+            if (lane == 0) put(a.exact, t, (int64_t)a.T, h);
         }
-    } else if (MODE == kProbs && a.xs && (warp == 2 || warp == 3)) {
-        // -------------------------------------------------------------- x for dw, a warp a row
-        for (int64_t t = (int64_t)blockIdx.x * 2 + (warp & 1); t < a.T; t += (int64_t)gridDim.x * 2)
-            xent_copy(a, t, lane);
     } else if (warp >= Cfg::kEpiWarp0) {
         // -------------------------------------------------------------- epilogue (both CTAs)
         // Warp w reads TMEM lane quadrant w % 4, columns [0, 128) for warps 4..7 and [128, 256)
@@ -577,10 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
         const int quad = warp & 3, ew = warp - Cfg::kEpiWarp0;
         const int cb = (ew >> 2) * 128;
         const uint32_t acc_empty_leader0 = mapa_shared(acc_empty0, 0);
-        float scale = 1.0f;   // kProbs, kGrads: the largest |dloss|
-        if (MODE == kProbs) scale = xent_top(a, threadIdx.x - 32 * Cfg::kEpiWarp0);
-        if constexpr (SWAP) swap_tokens<MODE>(a, threadIdx.x - 32 * Cfg::kEpiWarp0, scale);
-        if (MODE == kGrads) scale = *a.top;
+        if constexpr (SWAP) swap_tokens<MODE>(a, threadIdx.x - 32 * Cfg::kEpiWarp0);
         float2 sum = make_float2(-INFINITY, 0.0f);   // SWAP, kLoss: lane k's token (ew >> 2) * 16 + k so far
         MmJob b;
         for (int t_iter = 0; mm_job<MODE>(a, cluster_id, num_clusters, t_iter, b); ++t_iter) {
@@ -606,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
-            mm_epilogue<MODE>(a, b, v, row, col, scale);
+            mm_epilogue<MODE>(a, b, v, row, col);
             __syncwarp();
         }
         if constexpr (SWAP && MODE == kLoss) swap_finish(a, ew, lane, sum);
@@ -691,17 +693,16 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, float *
     if (in < 0 && a.targets[row] != a.ignore) set_device_error(QT2_ERR_INVALID_ARG);
 }
 
-// dx = the sum of the splits' fp32 sums times the largest |dloss|, rounded to bf16.  One thread takes 8
-// columns of a row.
-__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const float *top, int T, int K, int splits,
+// dx = c times the sum of the splits' fp32 sums, rounded to bf16.  One thread takes 8 columns of a row.
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const XentRow *row, int T, int K, int splits,
                                                       int64_t rows, int64_t ld, __nv_bfloat16 *dx, int64_t lddx) {
     grid_dependency();
     const int vecs = (K + 7) >> 3;
     const int64_t n = (int64_t)T * vecs;
-    const float scale = *top;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t t = i / vecs;
         const int c = (int)(i - t * vecs) * 8;
+        const float factor = row[t].c;
         float v[8] = {};
         for (int s = 0; s < splits; ++s) {
             const float4 *src = reinterpret_cast<const float4 *>(acc + (s * rows + t) * ld + c);
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float *acc, const fl
             v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= scale;
+        for (int k = 0; k < 8; ++k) v[k] *= factor;
         __nv_bfloat16 *dst = dx + t * lddx + c;
         const int valid = min(8, K - c);
         if (!QT2_STORE_OK(dst, valid * 2, dx, ((int64_t)(T - 1) * lddx + K) * 2)) continue;
