@@ -9,6 +9,11 @@ namespace qt2 {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same where the barrier passes on nothing but TMEM, whose accesses tcgen05.fence::before_thread_sync
+// orders: a release would also wait until this thread's earlier stores to global memory are acknowledged.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // TMA 2D tile load into this CTA's shared memory whose completion is reported to an mbarrier
 // of either CTA of the pair (cta_group::2); no multicast.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int32_t x, int32_t y,

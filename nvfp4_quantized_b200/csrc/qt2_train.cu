@@ -260,8 +260,8 @@ constexpr int64_t kPieceBytes = 512 << 20;
 // tokens, hidden 4096: x in one group of 64 MB 5.68 ms, in two of 32 MB 5.44 ms, in four 5.84 ms, forward).
 constexpr int64_t kGroupBytes = 32 << 20;
 constexpr int kJobStages = 4;                // what a tile's start and end cost, in stages of K = 64
-// A tile of dw takes its stages, or as long as its 128 KB (bf16) take to HBM: six stages' time.
-int64_t dw_job(int64_t T) { return std::max<int64_t>(ceil_div(T, 64), 6) + kJobStages; }
+// A tile of dw takes its stages, or as long as its 128 KB (bf16) take to leave: 2.2 us in all, eight stages' time.
+int64_t dw_job(int64_t T) { return std::max<int64_t>(ceil_div(T, 64), 4) + kJobStages; }
 
 struct XentPlan {
     int64_t num_m, num_v, num_k;   // 256-wide tiles of T, V and K
@@ -283,14 +283,17 @@ XentPlan xent_plan(int64_t T, int64_t K, int64_t V) {
     p.piece = ceil_div(p.num_v, p.pieces) * 256;
     p.pieces = (int)ceil_div(p.num_v * 256, p.piece);
     // dx's jobs are cut along the vocabulary where that shortens the launch: the pairs' even share
-    // of its stages or the longest pair's dx jobs, and what the sums that each cut adds cost to write and read
+    // of its stages or the longest pair's dx jobs, and what the sums that each cut adds cost to write and read.
+    // An eighth of those jobs besides: while they run on some of the pairs, these read w no faster than their MMAs
+    // take it, and what comes after them is levelled by estimate (16 tokens, hidden 4096, vocabulary 64000: two cuts
+    // 338 us, four 299, nine 301).
     const int64_t nks = p.piece / 64, dx = p.num_m * p.num_k;
     const int64_t dw = p.piece / 256 * p.num_k * dw_job(T);
     double best = 0;
     for (int s = 1; s <= 16 && s * 16 <= std::max<int64_t>(16, nks); ++s) {
         const int64_t job = ceil_div(nks, s) + kJobStages;
         const double share = (double)(dx * s * job + dw) / kPairs, longest = (double)(ceil_div(dx * s, kPairs) * job);
-        const double cost = std::max(share, longest) + (double)dx * s / 4;
+        const double cost = std::max(share, longest) + longest / 8 + (double)dx * s * std::min<int64_t>(T, 256) / 1024;
         if (s == 1 || cost < best) {
             best = cost;
             p.splits = s;

@@ -237,6 +237,72 @@ __device__ __forceinline__ float2 xent_join(const float2 &p, const float2 &q) {
     return make_float2(m, p.y * __expf(p.x - ref) + q.y * __expf(q.x - ref));
 }
 
+// Four lanes hold 128 bytes each of four neighbouring rows, as 4 chunks of 32 bytes: chunk q of all four rows
+// goes to lane q, so that a store of the warp writes 128 bytes of 8 rows and not 32 bytes of 32.  `dst`: the first
+// of the four rows; `rows`: how many of them exist; `wide`: rows start 32-byte aligned.  All lanes take part.
+__device__ __forceinline__ void store_rows(uint32_t (&p)[32], char *dst, int64_t pitch, int64_t rows, bool wide,
+                                           int lane, const void *base, int64_t extent) {
+#pragma unroll
+    for (int step = 1; step < 4; step *= 2) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & step) continue;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                uint32_t &lo = p[j * 8 + w], &hi = p[(j + step) * 8 + w];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, step);
+                if (up)
+                    lo = got;
+                else
+                    hi = got;
+            }
+        }
+    }
+    dst += (lane & 3) * 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, dst += pitch) {
+        if (i >= rows || !QT2_STORE_OK(dst, 32, base, extent)) continue;
+        uint32_t v[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v[w] = p[i * 8 + w];
+        if (wide) {
+            st_global_v8(dst, v);
+        } else {
+            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+// dw's rows `first` on, from a tile whose 128 columns from `col` on all exist.
+__device__ __forceinline__ void dw_rows(const MmArgs &a, uint32_t (&v)[128], int64_t first, int64_t rows, int col,
+                                        int lane, int64_t extent) {
+    const int e = a.dw_f32 ? 4 : 2;
+    char *dst = static_cast<char *>(a.dw) + (first * a.lddw + col) * e;
+    const int64_t pitch = a.lddw * e;
+    if (a.dw_f32) {
+#pragma unroll
+        for (int i = 0; i < 128; i += 32) {
+            uint32_t p[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) p[k] = v[i + k];
+            store_rows(p, dst + i * 4, pitch, rows, a.dw_wide, lane, a.dw, extent * 4);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 128; i += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+            p[k] = *reinterpret_cast<uint32_t *>(&b2);
+        }
+        store_rows(p, dst + i * 2, pitch, rows, a.dw_wide, lane, a.dw, extent * 2);
+    }
+}
+
 // What becomes of a tile: the thread holds columns [col, col + 128) of the tile's row `row`.
 template <int MODE>
 __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uint32_t (&v)[128], int row, int col) {
@@ -295,6 +361,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
         }
     } else if (!b.dw) {
         const int64_t ld = (int64_t)a.dx_n * 256;
+        if (row >= a.T) return;
         float *dst = a.acc + ((int64_t)b.split * a.dx_m * 256 + row) * ld + col;
         if (!QT2_STORE_OK(dst, 512, a.acc, (int64_t)a.splits * a.dx_m * 256 * ld * 4)) return;
 #pragma unroll
@@ -317,8 +384,14 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
     } else {
         const int64_t r = (int64_t)a.v0 + row;
         const int n = min(128, a.K - col);   // columns of dw from here on
-        if (row >= a.vw || r >= a.V || n <= 0) return;
         const int64_t extent = (int64_t)(a.V - 1) * a.lddw + a.K;
+        if (n == 128) {
+            const int lane = row & 31;
+            const int64_t first = r - (lane & 3), rows = min((int64_t)a.vw - row, a.V - r) + (lane & 3);
+            dw_rows(a, v, first, rows, col, lane, extent);
+            return;
+        }
+        if (row >= a.vw || r >= a.V || n <= 0) return;
         if (a.dw_f32) {
             float *dst = static_cast<float *>(a.dw) + r * a.lddw + col;
             if (!QT2_STORE_OK(dst, n * 4, a.dw, extent * 4)) return;
@@ -594,7 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
                                     tmem + ((uint32_t)(quad * 32) << 16) + 256 * buf, lane, sum);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
+                if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
                 continue;
             }
             const int row = b.m * 256 + (int)rank * 128 + quad * 32 + lane;
@@ -607,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(acc_empty_leader0 + 8 * buf);
+            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
             mm_epilogue<MODE>(a, b, v, row, col);
             __syncwarp();
         }
