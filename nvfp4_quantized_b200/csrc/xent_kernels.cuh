@@ -336,28 +336,28 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
             put(a.hit, (int64_t)row, (int64_t)a.T, h);
         }
     } else if (MODE == kProbs) {
-        if (row >= a.T) return;
-        const int y = xent_target(a, row);
-        const XentRow r = a.rows[row];
+        // rows behind the last token take part in the exchange, with no store of their own
+        const int lane = row & 31, q = lane & 3, rows = a.T - row + q;
+        const int y = row < a.T ? xent_target(a, row) : -1;
+        const XentRow r = row < a.T ? a.rows[row] : XentRow{};
         const int at = y - (a.v0 + col), valid = a.V - (a.v0 + col);
-        __nv_bfloat16 *dst = a.P + (int64_t)row * a.vw + col;
-        if (!QT2_STORE_OK(dst, 256, a.P, (int64_t)a.T * a.vw * 2)) return;
+        char *dst = reinterpret_cast<char *>(a.P) + ((int64_t)(row - q) * a.vw + col) * 2;
 #pragma unroll
-        for (int i = 0; i < 128; i += 16) {
-            uint32_t p[8];
+        for (int i = 0; i < 128; i += 64) {
+            uint32_t p[32];
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
+            for (int k = 0; k < 64; k += 2) {
                 float e[2];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int c = i + k + q;
-                    e[q] = exp_of(__uint_as_float(v[c]) - r.lse) * r.inv;
-                    e[q] = c == at ? r.at : (y < 0 || c >= valid) ? 0.0f : e[q];
+                for (int u = 0; u < 2; ++u) {
+                    const int c = i + k + u;
+                    e[u] = exp_of(__uint_as_float(v[c]) - r.lse) * r.inv;
+                    e[u] = c == at ? r.at : (y < 0 || c >= valid) ? 0.0f : e[u];
                 }
                 __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
                 p[k >> 1] = *reinterpret_cast<uint32_t *>(&b2);
             }
-            st_global_v8(dst + i, p);
+            store_rows(p, dst + i * 2, (int64_t)a.vw * 2, rows, true, lane, a.P, (int64_t)a.T * a.vw * 2);
         }
     } else if (!b.dw) {
         const int64_t ld = (int64_t)a.dx_n * 256;
