@@ -70,8 +70,9 @@ QT2_API qt2_status qt2_layernorm_bwd(const void *dy, int64_t lddy, const void *x
  * targets [T] (int64):
  *   lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_t,target(t).
  * The logits are formed piece by piece of the vocabulary on the tensor cores (fp32 sums) and never
- * stored.  loss and lse [T] are fp32; rows whose target is ignore_index have loss 0 (their lse is
- * still written).  Any other target outside [0, V) is treated as ignore_index and
+ * stored; the target's logit is formed again in fp32.  loss and lse [T] are fp32 and, as the tensor
+ * cores' sums truncate, off by about 1e-6 relative at K = 4096.  Rows whose target is ignore_index have
+ * loss 0 (their lse is still written).  Any other target outside [0, V) is treated as ignore_index and
  * reported as QT2_ERR_INVALID_ARG through qt2_train_device_status.
  * Workspace: qt2_linear_xent_fwd_workspace_size() bytes, 256-byte aligned.
  * --------------------------------------------------------------------------------------- */
@@ -88,9 +89,9 @@ QT2_API qt2_status qt2_linear_xent_fwd(const void *x, const void *w, const int64
  * by the probability that is not its target's, is held in bf16 (rounded once, 2^-8 at most relative
  * to each entry, the target's entry exact) in the workspace while the tensor cores multiply it, with
  * fp32 sums over the whole of V (dx) and T (dw).  dloss and that factor multiply dx's rows in fp32, and
- * x's for dw (rounded to bf16 an element at a time).  Rows without a target add nothing to dw, whatever x holds there (inf and NaN
- * included), and have dx 0 for finite w.  Targets outside [0, V) count as ignore_index and are not
- * reported again.
+ * x's for dw (rounded to bf16 an element at a time).  Rows without a target add nothing to dw, whatever
+ * x holds there (inf and NaN included), and have dx 0 for finite w.  Targets outside [0, V) count as
+ * ignore_index and are not reported again.
  * dx or dw may be NULL (not wanted), not both.
  * Workspace: qt2_linear_xent_bwd_workspace_size() bytes, 256-byte aligned.
  * --------------------------------------------------------------------------------------- */

@@ -237,11 +237,36 @@ __device__ __forceinline__ float2 xent_join(const float2 &p, const float2 &q) {
     return make_float2(m, p.y * __expf(p.x - ref) + q.y * __expf(q.x - ref));
 }
 
-// Four lanes hold 128 bytes each of four neighbouring rows, as 4 chunks of 32 bytes: chunk q of all four rows
-// goes to lane q, so that a store of the warp writes 128 bytes of 8 rows and not 32 bytes of 32.  `dst`: the first
-// of the four rows; `rows`: how many of them exist; `wide`: rows start 32-byte aligned.  All lanes take part.
-__device__ __forceinline__ void store_rows(uint32_t (&p)[32], char *dst, int64_t pitch, int64_t rows, bool wide,
-                                           int lane, const void *base, int64_t extent) {
+// 32 bytes; wide: 32-byte aligned (else 16).
+__device__ __forceinline__ void store_chunk(char *dst, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        st_global_v8(dst, v);
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+// A warp's 32 rows of 128 bytes, one a lane.  `dst`: the first of the four rows of the lane and its neighbours;
+// `rows`: how many of these four exist.  `exchange`: chunk q of 32 bytes of all four rows goes to lane q first, so
+// that a store of the warp writes 128 bytes of 8 rows and not 32 bytes of 32.  That is for tiles of at most
+// kExchangeStages, which wait for their stores; in longer ones the 32 shuffles are in the way of the MMAs'
+// operands (dw alone: 128 x 128 x 200000 92 us without and 68 with it, 512 x 512 x 128000 185 and 155; 1536 x 1536 x
+// 100000 677 and 773).  All lanes take part.
+constexpr int kExchangeStages = 8;
+__device__ __forceinline__ void store_rows(uint32_t (&p)[32], char *dst, int64_t pitch, int64_t rows, bool exchange,
+                                           bool wide, int lane, const void *base, int64_t extent) {
+    if (!exchange) {
+        dst += (lane & 3) * pitch;
+        if ((lane & 3) >= rows || !QT2_STORE_OK(dst, 128, base, extent)) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) v[w] = p[j * 8 + w];
+            store_chunk(dst + 32 * j, v, wide);
+        }
+        return;
+    }
 #pragma unroll
     for (int step = 1; step < 4; step *= 2) {
         const bool up = lane & step;
@@ -266,18 +291,13 @@ __device__ __forceinline__ void store_rows(uint32_t (&p)[32], char *dst, int64_t
         uint32_t v[8];
 #pragma unroll
         for (int w = 0; w < 8; ++w) v[w] = p[i * 8 + w];
-        if (wide) {
-            st_global_v8(dst, v);
-        } else {
-            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-        }
+        store_chunk(dst, v, wide);
     }
 }
 
 // dw's rows `first` on, from a tile whose 128 columns from `col` on all exist.
 __device__ __forceinline__ void dw_rows(const MmArgs &a, uint32_t (&v)[128], int64_t first, int64_t rows, int col,
-                                        int lane, int64_t extent) {
+                                        bool exchange, int lane, int64_t extent) {
     const int e = a.dw_f32 ? 4 : 2;
     char *dst = static_cast<char *>(a.dw) + (first * a.lddw + col) * e;
     const int64_t pitch = a.lddw * e;
@@ -287,7 +307,7 @@ __device__ __forceinline__ void dw_rows(const MmArgs &a, uint32_t (&v)[128], int
             uint32_t p[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) p[k] = v[i + k];
-            store_rows(p, dst + i * 4, pitch, rows, a.dw_wide, lane, a.dw, extent * 4);
+            store_rows(p, dst + i * 4, pitch, rows, exchange, a.dw_wide, lane, a.dw, extent * 4);
         }
         return;
     }
@@ -299,7 +319,7 @@ __device__ __forceinline__ void dw_rows(const MmArgs &a, uint32_t (&v)[128], int
             __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
             p[k] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        store_rows(p, dst + i * 2, pitch, rows, a.dw_wide, lane, a.dw, extent * 2);
+        store_rows(p, dst + i * 2, pitch, rows, exchange, a.dw_wide, lane, a.dw, extent * 2);
     }
 }
 
@@ -357,7 +377,8 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
                 __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
                 p[k >> 1] = *reinterpret_cast<uint32_t *>(&b2);
             }
-            store_rows(p, dst + i * 2, (int64_t)a.vw * 2, rows, true, lane, a.P, (int64_t)a.T * a.vw * 2);
+            store_rows(p, dst + i * 2, (int64_t)a.vw * 2, rows, b.nk <= kExchangeStages, true, lane, a.P,
+                       (int64_t)a.T * a.vw * 2);
         }
     } else if (!b.dw) {
         const int64_t ld = (int64_t)a.dx_n * 256;
@@ -388,7 +409,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
         if (n == 128) {
             const int lane = row & 31;
             const int64_t first = r - (lane & 3), rows = min((int64_t)a.vw - row, a.V - r) + (lane & 3);
-            dw_rows(a, v, first, rows, col, lane, extent);
+            dw_rows(a, v, first, rows, col, b.nk <= kExchangeStages, lane, extent);
             return;
         }
         if (row >= a.vw || r >= a.V || n <= 0) return;
