@@ -253,3 +253,12 @@ def test_huge_logits(T):
     assert (loss.abs() <= 18 * 2.0 ** -21).all()
     dx, dw = backward(x, w, y, lse, torch.ones(T, device="cuda"))
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+@pytest.mark.parametrize("dwd", [BF, FP])
+@pytest.mark.parametrize("shape", [(511, 512, 1003), (513, 520, 1002), (6, 136, 301), (39, 272, 257), (577, 136, 777)])
+def test_rows_that_end_inside_a_group_of_four(shape, dwd):
+    """Lanes exchange parts of four neighbouring rows of P and dw before they store them, in tiles of 512 contracted
+    elements at most: both ways, with T and V no multiples of four, rows 16 and 32 bytes aligned."""
+    check_all(*make(*shape, seed=sum(shape)), dwd=dwd)
+    assert tr.qt2_train_device_status() == 0
