@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i) {
             const int64_t v = c.lo + threadIdx.x + i * kGradThreads;
-            r[i] = v < c.hi ? __ldg(reinterpret_cast<const uint4 *>(c.base) + v) : make_uint4(0, 0, 0, 0);
+            r[i] = v < c.hi ? *(reinterpret_cast<const uint4 *>(c.base) + v) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i) {

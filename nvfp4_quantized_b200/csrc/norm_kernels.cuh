@@ -31,7 +31,9 @@ template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
 // Elements [c, c + E) of a weight vector of either type (`other` where there is none).  No 16 bytes
-// without an element of the vector are touched.
+// without an element of the vector are touched.  Plain loads, as everywhere in these kernels: the kernel
+// before this one may have written the vector while this one was already resident, and a read-only load
+// is not bound by the wait for it.
 template <int E>
 __device__ __forceinline__ void load_weight(const void *w, int f32, int c, int cols, float other, float (&v)[E]) {
     if (!w) {
@@ -41,13 +43,13 @@ __device__ __forceinline__ void load_weight(const void *w, int f32, int c, int c
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
             const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + e);
-            const float4 q = c + e < cols ? __ldg(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 q = c + e < cols ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
         }
     } else if constexpr (E == 8) {
-        unpack(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c)), v);
+        unpack(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c), v);
     } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(w) + c));
+        const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(w) + c);
         v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
     }
     if (c + E > cols) {   // what lies behind the vector may be NaN

@@ -232,7 +232,9 @@ __device__ __forceinline__ bool elect_one() {
 // ------------------------------------------------------------------------------------------
 // Programmatic dependent launch: a kernel launched with it may start while the one before it in the
 // stream still runs, and waits here, before its first access to global memory, until that one has
-// completed and its writes are visible; the kernel itself lets its successor start at once.
+// completed and its writes are visible; the kernel itself lets its successor start at once.  What the
+// kernel reads may therefore be written during its life: no read-only (non-coherent) loads, which are
+// not bound by the wait.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dependency() {
     asm volatile("griddepcontrol.launch_dependents;");
