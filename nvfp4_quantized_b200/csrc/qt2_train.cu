@@ -260,8 +260,11 @@ constexpr int64_t kPieceBytes = 512 << 20;
 // tokens, hidden 4096: x in one group of 64 MB 5.68 ms, in two of 32 MB 5.44 ms, in four 5.84 ms, forward).
 constexpr int64_t kGroupBytes = 32 << 20;
 constexpr int kJobStages = 4;                // what a tile's start and end cost, in stages of K = 64
-// A tile of dw takes its stages, or as long as its 128 KB (bf16) take to leave: 2.2 us in all, eight stages' time.
-int64_t dw_job(int64_t T) { return std::max<int64_t>(ceil_div(T, 64), 4) + kJobStages; }
+// A tile of dw takes its stages and those of the tokens that have their target in it, or as long as its 128 KB (bf16)
+// take to leave: 2.2 us in all, eight stages' time.
+int64_t dw_job(int64_t T, int64_t num_v) {
+    return std::max<int64_t>(ceil_div(T, 64) + ceil_div(T, 64 * num_v), 4) + kJobStages;
+}
 
 struct XentPlan {
     int64_t num_m, num_v, num_k;   // 256-wide tiles of T, V and K
@@ -288,7 +291,7 @@ XentPlan xent_plan(int64_t T, int64_t K, int64_t V) {
     // take it, and what comes after them is levelled by estimate (16 tokens, hidden 4096, vocabulary 64000: two cuts
     // 338 us, four 299, nine 301).
     const int64_t nks = p.piece / 64, dx = p.num_m * p.num_k;
-    const int64_t dw = p.piece / 256 * p.num_k * dw_job(T);
+    const int64_t dw = p.piece / 256 * p.num_k * dw_job(T, p.num_v);
     double best = 0;
     for (int s = 1; s <= 16 && s * 16 <= std::max<int64_t>(16, nks); ++s) {
         const int64_t job = ceil_div(nks, s) + kJobStages;
@@ -317,7 +320,11 @@ XentFwdWs xent_fwd_ws(const XentPlan &p, int64_t T, void *ws) {
     return w;
 }
 struct XentBwdWs {
-    __nv_bfloat16 *P, *xs;
+    __nv_bfloat16 *P, *xs, *low;
+    __nv_bfloat16 *H;
+    int64_t h_rows;
+    int *count, *pos;
+    XentTile *tile;
     XentRow *rows;
     float *acc;
     size_t bytes;
@@ -327,6 +334,12 @@ XentBwdWs xent_bwd_ws(const XentPlan &p, int64_t T, int64_t K, void *ws) {
     XentBwdWs w;
     w.P = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * p.piece * 2));
     w.xs = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * ceil_div(K, 64) * 128));
+    w.low = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)T * ceil_div(K, 64) * 128));
+    w.h_rows = T + (kTileRows - 1) * std::min<int64_t>(p.num_v, T);   // no more tiles have targets
+    w.H = reinterpret_cast<__nv_bfloat16 *>(c.take((size_t)w.h_rows * 512));
+    w.count = reinterpret_cast<int *>(c.take((size_t)(p.num_v + 1) * ceil_div(T, kSortTokens) * sizeof(int)));
+    w.pos = reinterpret_cast<int *>(c.take((size_t)T * sizeof(int)));
+    w.tile = reinterpret_cast<XentTile *>(c.take((size_t)p.num_v * sizeof(XentTile)));
     w.rows = reinterpret_cast<XentRow *>(c.take((size_t)T * sizeof(XentRow)));
     w.acc = reinterpret_cast<float *>(c.take((size_t)p.splits * p.num_m * p.num_k * 65536 * sizeof(float)));
     w.bytes = c.used;
@@ -360,6 +373,17 @@ cudaError_t launch_xent_loss(const MmArgs &a, float *loss, float *lse, cudaStrea
 cudaError_t launch_xent_rows(const MmArgs &a, const float *lse, const float *dloss, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     return launch(xent_rows_kernel, (unsigned)ceil_div(a.T, 8), 256, 0, s, a, lse, dloss);
+}
+
+cudaError_t launch_xent_sort(const MmArgs &a, int blocks, int phases, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    return launch(xent_sort_kernel, (unsigned)blocks, 1024, 0, s, a, phases);
+}
+cudaError_t xent_sort(const MmArgs &a, cudaStream_t s) {
+    if (a.words == 1) return launch_xent_sort(a, 1, kCount | kScan | kRank, s);
+    cudaError_t e = launch_xent_sort(a, a.words, kCount, s);
+    if (e == cudaSuccess) e = launch_xent_sort(a, 1, kScan, s);
+    return e == cudaSuccess ? launch_xent_sort(a, a.words, kRank, s) : e;
 }
 
 cudaError_t launch_xent_dx(const MmArgs &a, void *dx, int64_t lddx, cudaStream_t s) {
@@ -660,6 +684,8 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     MmMaps maps{};
     if (!encode_bf16(&maps.x_k, x, K, T, ldx, p.swap ? kSwapN / 2 : 128) ||
         !encode_bf16(&maps.w_k, w, K, V, ldw, 128) || !encode_bf16(&maps.x_mn, ws.xs, K, T, ceil_div(K, 64) * 64, 64) ||
+        !encode_bf16(&maps.low_mn, ws.low, K, T, ceil_div(K, 64) * 64, 64) ||
+        !encode_bf16(&maps.h_mn, ws.H, 256, ws.h_rows, 256, 64) ||
         !encode_bf16(&maps.w_mn, w, K, V, ldw, 64))
         return QT2_ERR_CUDA;
     MmArgs a{};
@@ -677,6 +703,13 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.acc = ws.acc;
     a.rows = ws.rows;
     a.xs = dw ? ws.xs : nullptr;
+    a.low = ws.low;
+    a.H = ws.H;
+    a.h_rows = ws.h_rows;
+    a.count = ws.count;
+    a.words = (int)ceil_div(T, kSortTokens);
+    a.pos = ws.pos;
+    a.tile = ws.tile;
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.ldx = ldx;
     a.ldxs = ceil_div(K, 64) * 64;
@@ -687,7 +720,9 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     a.dw_f32 = dw_dtype == QT2_DTYPE_F32;
     a.dw_wide = aligned(dw, 32) && lddw * (a.dw_f32 ? 4 : 2) % 32 == 0;
     const cudaStream_t s = as_stream(stream);
-    if (const cudaError_t e = launch_xent_rows(a, lse, dloss, s)) return from_cuda(e);
+    cudaError_t e = dw ? xent_sort(a, s) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_xent_rows(a, lse, dloss, s);
+    if (e != cudaSuccess) return from_cuda(e);
     for (int i = 0; i < p.pieces; ++i) {
         a.v0 = (int)(i * p.piece);
         a.vw = (int)std::min<int64_t>(p.piece, p.num_v * 256 - a.v0);
@@ -696,11 +731,11 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
         a.splits = (int)std::min<int64_t>(p.splits, a.vw / 64);
         a.dx_jobs = dx ? a.splits * a.dx_m * a.dx_n : 0;
         a.dw_jobs = dw ? a.num_n * (int)p.num_k : 0;
-        a.lead = (int)((a.vw / 64 / a.splits + kJobStages) / dw_job(T));
+        a.lead = (int)((a.vw / 64 / a.splits + kJobStages) / dw_job(T, p.num_v));
         if (!encode_bf16(&maps.p_k, ws.P, a.vw, T, a.vw, 128) || !encode_bf16(&maps.p_mn, ws.P, a.vw, T, a.vw, 64))
             return QT2_ERR_CUDA;
-        cudaError_t e = p.swap ? launch_mm<kProbs, true>(maps, a, a.num_n, s)
-                                 : launch_mm<kProbs, false>(maps, a, (int64_t)a.num_m * a.num_n, s);
+        e = p.swap ? launch_mm<kProbs, true>(maps, a, a.num_n, s)
+                   : launch_mm<kProbs, false>(maps, a, (int64_t)a.num_m * a.num_n, s);
         if (e == cudaSuccess) e = launch_mm<kGrads, false>(maps, a, (int64_t)a.dx_jobs + a.dw_jobs, s);
         if (e != cudaSuccess) return from_cuda(e);
     }

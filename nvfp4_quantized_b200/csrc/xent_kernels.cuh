@@ -6,8 +6,17 @@
 // The tensor cores take G as c_t P_tv: with q_t = 1 - exp(l_t,y(t) - lse_t), the rest of the row's
 // probability, c_t = dloss_t q_t and P_tv = exp(l_tv - lse_t) / q_t, -1 at the target.  P's largest entry
 // is then exact in bf16 and the others' roundings independent; c_t multiplies dx's rows in fp32, and
-// x's for dw (c x in bf16, rounded an element at a time).  Rounded as it stands, G's entry at the
-// target is off by up to 2^-8 in all of dx's row, and equal dloss in all rows alike.
+// x's for dw.  Rounded as it stands, G's entry at the target is off by up to 2^-8 in all of dx's row, and
+// equal dloss in all rows alike.
+//
+// c x is the sum of two bf16 numbers (2^-16 off at most).  P is multiplied by the first.  The second
+// takes part where an entry of P shows c x in full, at the targets: the tokens are sorted by the tile of
+// dw that holds their target (stable: the sums' order is fixed), and a tile multiplies its tokens' second
+// numbers by a matrix H of one entry a row, P's at the target: a stage or so more a tile.  Products with
+// P's other entries have that entry's rounding anyway.  With the first number alone an fp32 dw was off by
+// 1.6e-3 to 2.2e-3 (2-norm; 300 x 1000 x 8000 with equal dloss), and a bf16 one by 2.2e-3, of which 1.65e-3
+// are its own rounding.  (P times both numbers wherever a tile and a stage of 64 tokens hold a target, which
+// needs no sorting: 2048 x 2048 x 32000 697 us for 539, 8192 x 1024 x 1000 143 for 92.)
 //
 // All three products are bf16 with fp32 sums on the tensor cores, in one persistent kernel shape
 // (mm_pair_kernel): a pair of SMs forms 256x256 tiles with tcgen05.mma.cta_group::2, each SM
@@ -81,13 +90,20 @@ enum MmMode { kLoss = 0, kProbs = 1, kGrads = 2 };
 
 // Tensor maps: k = K-major reads (box 64 x 128 rows), mn = MN-major reads (box 64 x 64).
 struct MmMaps {
-    CUtensorMap x_k, w_k, p_k, x_mn, w_mn, p_mn;
+    CUtensorMap x_k, w_k, p_k, x_mn, low_mn, h_mn, w_mn, p_mn;
 };
 
 // What the backward pass needs of a row: lse, 1 / q (0: no target), P's entry at the target, c.
 struct __align__(16) XentRow {
     float lse, inv, at, c;
 };
+
+// Of a 256-wide tile of the vocabulary: where the tokens that have their target in it begin in sorted order, how
+// many they are, and their first row of H (a multiple of kTileRows).
+struct __align__(16) XentTile {
+    int start, count, h, none;
+};
+constexpr int kTileRows = 16;   // K of one MMA: a tile's rows of H are filled up with zeros to a multiple of it
 
 struct MmArgs {
     int T, K, V;
@@ -100,6 +116,13 @@ struct MmArgs {
     int64_t ldx, ldw;
     __nv_bfloat16 *xs;     // backward, where dw is wanted: c x, zeros in rows without a target
     int64_t ldxs;
+    __nv_bfloat16 *low;    // what c x's rounding to xs left over, rows in sorted order
+    __nv_bfloat16 *H;      // [h_rows][256]: P's entry at the target, in column target % 256
+    int64_t h_rows;
+    int *count;            // [num_v + 1][words]: tokens of a tile in each 2048; then what comes before them in sorted order
+    int words;
+    int *pos;              // [T]: the token's place in sorted order, behind the tiles' those without a target
+    XentTile *tile;        // [num_v]
     XentRow *rows;         // backward: [T]
     float *hit, *exact;    // kLoss: the target's logit as the tile has it, and formed in fp32
     __nv_bfloat16 *P;      // [T][vw]
@@ -168,6 +191,13 @@ __device__ __forceinline__ bool mm_job(const MmArgs &a, int c, int pairs, int i,
     return true;
 }
 
+// What a dw job's tile has behind its stages: the products with H (count 0: no dw job).
+template <int MODE>
+__device__ __forceinline__ XentTile mm_tile(const MmArgs &a, const MmJob &b) {
+    if (MODE != kGrads || !b.dw) return {};
+    return a.tile[(a.v0 >> 8) + b.m];
+}
+
 // The row's target within the vocabulary, or -1.
 __device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
     const int64_t y = a.targets[t];
@@ -196,9 +226,122 @@ __device__ __forceinline__ float xent_exact(const MmArgs &a, int64_t t, int y, i
     return h;
 }
 
-// Backward, before the pieces: what each row needs (XentRow), and c x for dw.  A warp a row.  What
-// a row without a target holds, inf and NaN among it, must not reach dw through a product with a zero of
-// P: its copy is zero.
+// Backward, where dw is wanted: the tokens' stable order by the tile of their target (tile num_v: none), in three
+// phases: a block counts 2048 tokens a tile (kCount); one block adds up the counts before each (kScan); a
+// block gives its 2048 tokens their places (kRank): every warp ranks 32 tokens among themselves, then one warp
+// goes over these groups in their order (2048 tokens: 13 us in all; one warp for both 20 us).  Up to 2048
+// tokens: one launch.
+constexpr int kSortTokens = 2048, kSortTiles = 4096;   // of a block; tiles at a time in shared memory
+enum SortPhase { kCount = 1, kScan = 2, kRank = 4 };
+
+// Exclusive sum over the block's 1024 threads of v; `sum` becomes the carry plus all of them.
+__device__ __forceinline__ int sort_scan(int v, int &carry, int (&sh)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += u;
+    }
+    __syncthreads();   // the last call's sums are read
+    if (lane == 31) sh[warp] = s;
+    __syncthreads();
+    int before = lane < warp ? sh[lane] : 0, all = sh[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    }
+    const int r = carry + before + s - v;
+    carry += all;
+    return r;
+}
+
+__global__ void __launch_bounds__(1024) xent_sort_kernel(const MmArgs a, int phases) {
+    grid_dependency();
+    __shared__ int n_of[kSortTiles], tile_of[kSortTokens], sh[32];
+    __shared__ uint8_t rank_of[kSortTokens];   // within its 32 tokens; 128: the last of its tile there
+    const int tiles = (a.V + 255) >> 8, word = blockIdx.x, tid = threadIdx.x;
+    const int64_t first = (int64_t)word * kSortTokens, all = (int64_t)(tiles + 1) * a.words;
+    const int tokens = (int)min((int64_t)kSortTokens, a.T - first);
+    if (phases & (kCount | kRank)) {
+        for (int i = tid; i < tokens; i += 1024) {
+            const int y = xent_target(a, first + i);
+            tile_of[i] = y < 0 ? tiles : y >> 8;
+        }
+    }
+    if (phases & kCount) {
+        for (int lo = 0; lo <= tiles; lo += kSortTiles) {
+            const int n = min(kSortTiles, tiles + 1 - lo);
+            for (int i = tid; i < n; i += 1024) n_of[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < tokens; i += 1024) {
+                const int k = tile_of[i] - lo;
+                if (k >= 0 && k < n) atomicAdd(n_of + k, 1);   // a count: the same in any order
+            }
+            __syncthreads();
+            for (int i = tid; i < n; i += 1024) put(a.count, (int64_t)(lo + i) * a.words + word, all, n_of[i]);
+            __syncthreads();
+        }
+    }
+    if (phases & kScan) {
+        int carry = 0;
+        for (int64_t i = 0; i < all; i += 1024) {
+            const int64_t k = i + tid;
+            const int before = sort_scan(k < all ? a.count[k] : 0, carry, sh);
+            if (k < all) put(a.count, k, all, before);
+        }
+        __syncthreads();
+        carry = 0;
+        for (int i = 0; i < tiles; i += 1024) {
+            const int64_t k = i + tid;
+            XentTile t{};
+            if (k < tiles) {
+                t.start = a.count[k * a.words];
+                t.count = a.count[(k + 1) * a.words] - t.start;
+            }
+            t.h = sort_scan((t.count + kTileRows - 1) / kTileRows * kTileRows, carry, sh);
+            if (k < tiles) put(a.tile, k, (int64_t)tiles, t);
+        }
+        __syncthreads();
+    }
+    if (phases & kRank) {
+        __syncthreads();
+        for (int i = tid; i < kSortTokens; i += 1024) {
+            const int lane = tid & 31;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, i < tokens ? tile_of[i] : -1);
+            rank_of[i] = (uint8_t)(__popc(same & ((1u << lane) - 1)) | ((same >> lane) == 1 ? 128 : 0));
+        }
+        for (int lo = 0; lo <= tiles; lo += kSortTiles) {
+            const int n = min(kSortTiles, tiles + 1 - lo);
+            for (int i = tid; i < n; i += 1024) n_of[i] = a.count[(int64_t)(lo + i) * a.words + word];
+            __syncthreads();
+            if (tid < 32) {
+                int k = -1, r = 0;
+                auto fetch = [&](int i) {
+                    k = i < tokens ? tile_of[i] - lo : -1;
+                    r = i < tokens ? rank_of[i] : 0;
+                };
+                fetch(tid);
+                for (int i = tid; i - tid < tokens; i += 32) {
+                    const int tile = k, rank = r & 127;
+                    const bool in = tile >= 0 && tile < n, last = r & 128;
+                    fetch(i + 32);
+                    const int at = in ? n_of[tile] + rank : 0;
+                    __syncwarp();
+                    if (in && last) n_of[tile] = at + 1;
+                    __syncwarp();
+                    if (in) put(a.pos, first + i, (int64_t)a.T, at);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Backward, before the pieces: what each row needs (XentRow), and for dw c x, what its rounding left over,
+// and H's row.  A warp a row.  What a row without a target holds, inf and NaN among it, must not reach
+// dw through a product with a zero of P: its copies are zero.
 __global__ void __launch_bounds__(256) xent_rows_kernel(const MmArgs a, const float *lse, const float *dloss) {
     grid_dependency();
     const int lane = threadIdx.x & 31;
@@ -216,18 +359,42 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const MmArgs a, const fl
     }
     if (lane == 0) put(a.rows, t, (int64_t)a.T, r);
     if (!a.xs) return;
+    const int64_t pos = a.pos[t];
+    if (y >= 0) {
+        // the tile's last token fills up its rows of H
+        const XentTile tile = a.tile[y >> 8];
+        const int i = (int)pos - tile.start;
+        const int last = i == tile.count - 1 ? (i | (kTileRows - 1)) : i;
+        const __nv_bfloat16 e = __float2bfloat16_rn(r.at);
+        for (int k = i; k <= last; ++k) {
+            uint32_t v[4] = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k == i && lane * 4 + j == (y & 255) >> 1)
+                    v[j] = (uint32_t)*reinterpret_cast<const uint16_t *>(&e) << (16 * (y & 1));
+            __nv_bfloat16 *dst = a.H + ((int64_t)tile.h + k) * 256 + lane * 8;
+            if (QT2_STORE_OK(dst, 16, a.H, a.h_rows * 512))
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
 #pragma unroll 4
     for (int k = lane * 8; k < a.K; k += 256) {
-        uint4 v = make_uint4(0, 0, 0, 0);
+        uint4 v = make_uint4(0, 0, 0, 0), left = v;
         if (y >= 0) {
-            float f[8];
+            float f[8], h[8];
             unpack(*reinterpret_cast<const uint4 *>(a.x + t * a.ldx + k), f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= r.c;
-            v = pack(f);
+            for (int e = 0; e < 8; ++e) h[e] = f[e] * r.c;
+            v = pack(h);
+            unpack(v, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fabsf(h[e]) < INFINITY ? fmaf(f[e], r.c, -h[e]) : 0.0f;
+            left = pack(f);
         }
-        __nv_bfloat16 *dst = a.xs + t * a.ldxs + k;
-        if (QT2_STORE_OK(dst, 16, a.xs, (int64_t)a.T * a.ldxs * 2)) *reinterpret_cast<uint4 *>(dst) = v;
+        const int64_t extent = (int64_t)a.T * a.ldxs * 2;
+        __nv_bfloat16 *dst = a.xs + t * a.ldxs + k, *low = a.low + pos * a.ldxs + k;
+        if (QT2_STORE_OK(dst, 16, a.xs, extent)) *reinterpret_cast<uint4 *>(dst) = v;
+        if (QT2_STORE_OK(low, 16, a.low, extent)) *reinterpret_cast<uint4 *>(low) = left;
     }
 }
 
@@ -590,7 +757,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
         MmJob b;
         for (int j = 0; ok && mm_job<MODE>(a, cluster_id, num_clusters, j, b); ++j) {
             const int am = b.m * 256 + (int)rank * 128, bn = b.n * 256 + (int)rank * 128;
-            for (int ks = b.ks; ks < b.ks + b.nk; ++ks) {
+            const XentTile tile = mm_tile<MODE>(a, b);
+            const int end = b.ks + b.nk;
+            for (int ks = b.ks; ks < end + (tile.count + 63) / 64; ++ks) {
                 const int it = issued, s = it % S;
                 if (it >= S && !mbar_wait_warp(empty0 + 8 * s, ((it / S) & 1) ^ 1)) {
                     ok = false;
@@ -611,6 +780,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
                         tma_load_2d_pair(st, &maps.p_k, k, am, fb);
                         tma_load_2d_pair(st + Cfg::kA, &maps.w_mn, bn, a.v0 + k, fb);
                         tma_load_2d_pair(st + Cfg::kA + 8192, &maps.w_mn, bn + 64, a.v0 + k, fb);
+                    } else if (ks >= end) {
+                        const int i = (ks - end) * 64, col = (int)rank * 128;
+                        tma_load_2d_pair(st, &maps.h_mn, col, tile.h + i, fb);
+                        tma_load_2d_pair(st + 8192, &maps.h_mn, col + 64, tile.h + i, fb);
+                        tma_load_2d_pair(st + Cfg::kA, &maps.low_mn, bn, tile.start + i, fb);
+                        tma_load_2d_pair(st + Cfg::kA + 8192, &maps.low_mn, bn + 64, tile.start + i, fb);
                     } else {
                         tma_load_2d_pair(st, &maps.p_mn, am, k, fb);
                         tma_load_2d_pair(st + 8192, &maps.p_mn, am + 64, k, fb);
@@ -631,13 +806,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
         MmJob b;
         for (int t_iter = 0; ok && mm_job<MODE>(a, cluster_id, num_clusters, t_iter, b); ++t_iter) {
             const int buf = t_iter & 1;
+            const XentTile tile = mm_tile<MODE>(a, b);
             if (t_iter >= 2 && !mbar_wait_warp(acc_empty0 + 8 * buf, ((t_iter >> 1) & 1) ^ 1)) break;
             tc_fence_after();
             const bool mn_a = MODE == kGrads && b.dw, mn_b = MODE == kGrads;
             const uint32_t idesc = Cfg::kIdesc | (mn_a ? Cfg::kIdescMnA : 0) | (mn_b ? Cfg::kIdescMnB : 0);
             const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
             const uint32_t lbo_a = mn_a ? 8192 : 16, lbo_b = mn_b ? 8192 : 16;
-            for (int ks = 0; ks < b.nk; ++ks) {
+            for (int ks = 0; ks < b.nk + (tile.count + 63) / 64; ++ks) {
+                // rows of H behind the tile's, another tile's or none, take no part
+                const int steps = ks < b.nk ? 4 : min(4, (tile.count - (ks - b.nk) * 64 + kTileRows - 1) / kTileRows);
                 const int it = mma_done, s = it % S;
                 if (!mbar_wait_warp(full0 + 8 * s, (it / S) & 1)) {
                     ok = false;
@@ -647,10 +825,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MmCfg<SWAP>::kThread
                 const uint32_t st = smem_u32(base + s * Cfg::kStageBytes);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (MODE == kGrads && kk >= steps) break;
                         tc_mma_pair_f16(tmem + 256 * buf, make_smem_desc(st + step_a * kk, lbo_a, 1024, 2),
                                         make_smem_desc(st + Cfg::kA + step_b * kk, lbo_b, 1024, 2), idesc,
                                         (ks | kk) != 0);
+                    }
                     tc_commit_pair_both(empty0 + 8 * s);
                 }
                 __syncwarp();
