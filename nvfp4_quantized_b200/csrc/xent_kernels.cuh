@@ -205,7 +205,8 @@ __device__ __forceinline__ int xent_target(const MmArgs &a, int64_t t) {
 }
 
 // The target's logit again, in fp32 with short sums, by one warp: the tensor cores' long ones lose up
-// to 1e-5 of it (K = 4096), which the loss of a row that expects its target otherwise shows in full.
+// to 1.7e-5 of it (K = 4096, products of one sign), which the loss of a row that expects its target
+// otherwise shows in full.
 __device__ __forceinline__ float xent_exact(const MmArgs &a, int64_t t, int y, int lane) {
     const __nv_bfloat16 *x = a.x + t * a.ldx, *w = a.w + (int64_t)y * a.ldw;
     float h = 0.0f;

@@ -94,6 +94,26 @@ def test_tokens_that_share_a_target(T):
             check_norm(g, v, s, b, name)
 
 
+@pytest.mark.parametrize("K", [256, 1024, 4096, 16384])
+@pytest.mark.parametrize("T", [8, 64])
+def test_rows_that_one_entry_dominates(T, K):
+    """Logits of about 40 whose products are all of one sign, as far from zero as sums of the tensor cores get.  Of the
+    target: formed again in fp32, 2^-20 of it allowed.  Of another entry: what the sums lose, a step of 2^-23 for each of
+    K / 16 additions and 16 more."""
+    V = 3000
+    g = torch.Generator(device="cuda").manual_seed(K + T)
+    w = (torch.randn((V, K), generator=g, device="cuda") * 0.1).to(BF)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    for top, most in ((y, 2.0 ** -20), ((y + 1) % V, 2 * ref.U * (K / 16 + 16) + 2.0 ** -20)):
+        x = (w[top].float() * (40 / (0.01 * K))).to(BF)
+        l = x.double() @ w.double().T
+        assert (l.amax(1) > 20 + l.topk(2, 1).values[:, 1]).all()   # nothing else counts
+        loss, lse = forward(x, w, y)
+        want = torch.logsumexp(l, 1)
+        assert ((lse - want).abs() <= most * l.amax(1)).all()
+        assert ((loss - (want - l.gather(1, y[:, None])[:, 0])).abs() <= most * l.amax(1)).all()
+
+
 @pytest.mark.parametrize("T", [70, 2500])
 def test_vocabulary_of_more_tiles_than_the_sort_takes_at_a_time(T):
     """dw's rows around tile 4096 and at both ends of 1.1 million entries, targets among them."""
