@@ -68,6 +68,10 @@ __device__ __forceinline__ float ex2(float x) {
 // logits (at 1e7 to halves).
 __device__ __forceinline__ float exp_of(float d) { return ex2(d * 1.4426950408889634f); }
 
+// What logits of maximum m are reduced by before exp: where m is infinite nothing (m - m is no number), so that
+// exponentials of -inf add up to 0 and one of +inf to inf.
+__device__ __forceinline__ float exp_ref(float m) { return fabsf(m) == INFINITY ? 0.0f : m; }
+
 constexpr int kSwapN = 32;   // SWAP: its tiles' columns, the least that a pair's MMA takes
 template <bool SWAP>
 struct MmCfg {
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const MmArgs a, const fl
 
 // Two (max, sum of exp) pairs as one.
 __device__ __forceinline__ float2 xent_join(const float2 &p, const float2 &q) {
-    const float m = fmaxf(p.x, q.x), ref = m == -INFINITY ? 0.0f : m;
+    const float m = fmaxf(p.x, q.x), ref = exp_ref(m);
     return make_float2(m, p.y * __expf(p.x - ref) + q.y * __expf(q.x - ref));
 }
 
@@ -505,7 +509,7 @@ __device__ __forceinline__ void mm_epilogue(const MmArgs &a, const MmJob &b, uin
         float m = __uint_as_float(v[0]);
 #pragma unroll
         for (int i = 1; i < 128; ++i) m = fmaxf(m, __uint_as_float(v[i]));
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = exp_ref(m);
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 128; i += 4) {
@@ -683,7 +687,7 @@ __device__ __forceinline__ void swap_epilogue(const MmArgs &a, int v, int first,
             float m = l;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const float ref = m == -INFINITY ? 0.0f : m;
+            const float ref = exp_ref(m);
             float s = exp_of(l - ref);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, float *
                 p[k] = i + 32 * k < parts ? a.part[(int64_t)(i + 32 * k) * a.T + t] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) n = fmaxf(n, p[k].x);
-            const float ref = n == -INFINITY ? 0.0f : n;
+            const float ref = exp_ref(n);
             s *= __expf(m - ref);
 #pragma unroll
             for (int k = 0; k < 8; ++k) s += p[k].y * __expf(p[k].x - ref);
@@ -949,7 +953,7 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const MmArgs a, float *
     float top = p.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float ref = top == -INFINITY ? 0.0f : top;
+    const float ref = exp_ref(top);
     float sum = p.y * __expf(p.x - ref);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
