@@ -596,8 +596,9 @@ __device__ __forceinline__ void norm_put_weight(const NormArgs &a, bool bias, in
 // row, V vectors a thread, B rows at a time; the next rows are on their way while these are reduced and
 // written.  A thread keeps its columns (and their weights) for all of the block's rows and sums their
 // dw and db in registers; a block leaves one partial sum a column, which layernorm_dw_kernel adds up.
-// With d = x - mean the row's sums are sum(a) and sum(a d), and dx = rstd a - (rstd^3 sum(a d) / C) d -
-// rstd sum(a) / C.
+// With d = x - mean the row's sums are sum(a) and sum(a d), and dx = rstd (a - (rstd^2 sum(a d) / C) d -
+// sum(a) / C): sum(a d) times rstd once is of a's size, and no power of rstd stands alone, so that rows of
+// any deviation that fp32 has stay within it.
 // ---------------------------------------------------------------------------------------------
 template <class T, int G, int V, int B>
 __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a) {
@@ -670,14 +671,13 @@ __global__ void __launch_bounds__(256, 2) layernorm_bwd_kernel(const NormArgs a)
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 if (r0 + k >= a.rows) continue;
-                const float m1 = -s[2 * k] * inv * scale[k];
-                const float m2 = -s[2 * k + 1] * inv * scale[k] * scale[k] * scale[k];
+                const float m1 = -s[2 * k] * inv, m2 = -s[2 * k + 1] * inv * scale[k] * scale[k];
                 const uint64_t m1p = f2(m1, m1), m2p = f2(m2, m2), r2 = f2(scale[k], scale[k]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
 #pragma unroll
                     for (int e = 0; e < P; ++e)
-                        p[k][i][e] = f2_fma(p[k][i][e], r2, f2_fma(d[k][i][e], m2p, m1p));
+                        p[k][i][e] = f2_mul(f2_add(p[k][i][e], f2_fma(d[k][i][e], m2p, m1p)), r2);
                     float o[E];
                     floats_of<E>(p[k][i], o);
                     store_row(static_cast<T *>(a.y) + (r0 + k) * a.ldy, (lane + i * G) * E, a.cols, o, a.y,
@@ -882,8 +882,7 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 if (row + k >= rows) continue;
-                const float m1 = -s[2 * k] * inv * rstd[k];
-                const float m2 = -s[2 * k + 1] * inv * rstd[k] * rstd[k] * rstd[k];
+                const float m1 = -s[2 * k] * inv, m2 = -s[2 * k + 1] * inv * rstd[k] * rstd[k];
                 const uint64_t m1p = f2(m1, m1), m2p = f2(m2, m2), r2 = f2(rstd[k], rstd[k]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -894,7 +893,7 @@ __global__ void __launch_bounds__(NormRing<T, G, C>::kGroups *G, 1) layernorm_bw
                     weight(v, w);
 #pragma unroll
                     for (int e = 0; e < P; ++e)
-                        g[e] = f2_fma(f2_mul(g[e], w[e]), r2, f2_fma(d[e], m2p, m1p));
+                        g[e] = f2_mul(f2_fma(g[e], w[e], f2_fma(d[e], m2p, m1p)), r2);
                     float o[E];
                     floats_of<E>(g, o);
                     store_row<T, WHOLE>(static_cast<T *>(a.y) + (row + k) * a.ldy, c, cols, o, a.y,
