@@ -3,9 +3,12 @@ head's softmax cross entropy and the global gradient norm with clipping, in ``li
 
 Argument marshalling only, in the manner of ``qt2``: every function forwards to the entry point of
 the same name with the tensors' device pointers and the current CUDA stream (or ``stream``), and
-raises ``QT2Error`` on a non-OK status.  Element types are the tensors' own (bf16 or fp32);
-a tensor that is not on the current CUDA device, or of a type that the call does not take, raises
-``QT2Error`` with QT2_ERR_DEVICE or QT2_ERR_INVALID_ARG before the call.  There is no fallback.
+raises ``QT2Error`` on a non-OK status.  Element types are the tensors' own (bf16 or fp32); before
+the call a tensor that is not on the current CUDA device raises ``QT2Error`` with QT2_ERR_DEVICE, one
+of a type that the call does not take with QT2_ERR_INVALID_ARG, as does a vector (weights, statistics,
+targets, losses and their gradients, workspaces) that is not contiguous: an expanded or strided one
+holds other elements, or fewer, than the call reads.  Matrices are given by their leading dimension.
+There is no fallback.
 """
 from __future__ import annotations
 
@@ -114,6 +117,12 @@ def _only(fn: str, dtype: torch.dtype, *tensors):
             raise QT2Error(fn, QT2_ERR_INVALID_ARG)
 
 
+def _vectors(fn: str, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+
+
 # The current stream's handle; torch.cuda.current_stream() makes a Stream object for it, which takes
 # longer than a small kernel (3.4 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -145,6 +154,7 @@ def qt2_layernorm_fwd(x: torch.Tensor, rows: int, cols: int, ldx: int, weight: t
     fn = "qt2_layernorm_fwd"
     xd, wd = _dtype(fn, x, y), _dtype(fn, weight, bias)
     _only(fn, torch.float32, mean, rstd)
+    _vectors(fn, weight, bias, mean, rstd)
     px, pw, pb, py, pm, pr = _ptrs(fn, x, weight, bias, y, mean, rstd)
     _check(fn, lib().qt2_layernorm_fwd(px, xd, rows, cols, ldx, pw, pb, wd, eps, py, ldy, pm, pr, _stream(stream)))
 
@@ -164,6 +174,7 @@ def qt2_layernorm_bwd(dy: torch.Tensor, lddy: int, x: torch.Tensor, rows: int, c
     fn = "qt2_layernorm_bwd"
     xd, wd = _dtype(fn, dy, x, dx), _dtype(fn, weight, dweight, dbias)
     _only(fn, torch.float32, mean, rstd)
+    _vectors(fn, weight, mean, rstd, dweight, dbias, workspace)
     pdy, px, pw, pm, pr, pdx, pdw, pdb, pws = _ptrs(fn, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
     _check(fn, lib().qt2_layernorm_bwd(pdy, lddy, px, xd, rows, cols, ldx, pw, wd, pm, pr, pdx, lddx, pdw, pdb, pws,
                                        ws_bytes, _stream(stream)))
@@ -184,6 +195,7 @@ def qt2_linear_xent_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     _only(fn, torch.bfloat16, x, w)
     _only(fn, torch.int64, targets)
     _only(fn, torch.float32, loss, lse)
+    _vectors(fn, targets, loss, lse, workspace)
     px, pw, pt, pl, ps, pws = _ptrs(fn, x, w, targets, loss, lse, workspace)
     _check(fn, lib().qt2_linear_xent_fwd(px, pw, pt, T, K, V, ldx, ldw, ignore_index, pl, ps, pws, ws_bytes,
                                          _stream(stream)))
@@ -204,6 +216,7 @@ def qt2_linear_xent_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     _only(fn, torch.bfloat16, x, w, dx)
     _only(fn, torch.int64, targets)
     _only(fn, torch.float32, lse, dloss)
+    _vectors(fn, targets, lse, dloss, workspace)
     if dw is not None and _dtype(fn, dw) != dw_dtype:
         raise QT2Error(fn, QT2_ERR_INVALID_ARG)
     px, pw, pt, ps, pg, pdx, pdw, pws = _ptrs(fn, x, w, targets, lse, dloss, dx, dw, workspace)
@@ -262,6 +275,7 @@ def qt2_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, 
     """norm (one fp32 element) = the 2-norm of all the list's gradients together."""
     fn = "qt2_grad_norm"
     _only(fn, torch.float32, norm)
+    _vectors(fn, workspace)
     pn, pws = _ptrs(fn, norm, workspace)
     if grads.count and grads.device != norm.get_device():
         raise QT2Error(fn, QT2_ERR_DEVICE)
