@@ -403,6 +403,7 @@ qt2_status xent_check(const void *x, const void *w, const int64_t *targets, int6
                       int64_t ldx, int64_t ldw) {
     if (!x || !w || !targets) return QT2_ERR_INVALID_ARG;
     if (!xent_dims_ok(T, K, V) || !ld_shape_ok(ldx, K) || !ld_shape_ok(ldw, K)) return QT2_ERR_SHAPE;
+    if (std::max(ldx, ldw) >= (int64_t(1) << 39)) return QT2_ERR_SHAPE;   // a tensor map's rows: below 2^40 bytes
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(targets, 8) || ldx % 8 || ldw % 8) return QT2_ERR_ALIGN;
     return QT2_OK;
 }

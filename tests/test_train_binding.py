@@ -52,3 +52,14 @@ def test_workspace_of_the_gradient_norm(monkeypatch):
         with pytest.raises(qt2.QT2Error) as e:
             tr.qt2_grad_norm(grads, torch.zeros(1), bad, 1 << 20)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("arg", ["ldx", "ldw"])
+def test_leading_dimensions_that_no_tensor_map_holds(arg):
+    """A row stride of 2^40 bytes is refused as a shape, with the device and the library's CUDA calls left out."""
+    from tests.test_train_abi import _xent_bwd, _xent_fwd
+    L = tr.lib()
+    for call in (_xent_fwd, _xent_bwd):
+        for ld, status in (((1 << 39) - 8, qt2.QT2_OK), (1 << 39, qt2.QT2_ERR_SHAPE), (1 << 42, qt2.QT2_ERR_SHAPE)):
+            with tr.fault_hook(lambda site: qt2.FAULT_SKIP):
+                assert call(L, **{arg: ld}) == status, ld
