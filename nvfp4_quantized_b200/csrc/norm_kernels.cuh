@@ -5,9 +5,12 @@
 //   dw = sum_r dy h, db = sum_r dy
 //
 // HBM bounds all of it from some MB on, launches below.  Measured (B200, inputs larger than L2, a copy
-// of as many bytes at 6.0-6.4 TB/s): forward 16384 x 4096 bf16 50 us (5.4 TB/s), 32768 x 2048 bf16 46 us (5.9),
-// 16384 x 4096 fp32 85 us (6.3); backward 32768 x 2048 bf16 62 us for dx (6.4), 69 us with dw and db,
-// 16384 x 4096 fp32 121 and 127 us (6.7), 4096 x 16384 bf16 83 and 99 us (4.9).
+// of as many bytes at 6.0-6.3 TB/s; calls back to back, 1 to 6 us more where inputs change from call to call):
+// forward 16384 x 4096 bf16 51 us (5.3 TB/s), 32768 x 2048 bf16 46 us (5.9), 16384 x 4096 fp32 92 us (5.9);
+// backward 32768 x 2048 bf16 64 us for dx (6.3), 70 us with dw and db, 16384 x 4096 fp32 121 and 127 us (6.7),
+// 4096 x 16384 bf16 84 and 102 us (4.8).  Rows of more than 16384 columns are read again for each pass: 2048 x
+// 20000 bf16 forward 58 us (2.8), backward 58 us for dx (4.2), 128 us with dw and db, which read x and dy from
+// HBM once more, a column a thread.
 #pragma once
 
 #include <cuda_bf16.h>

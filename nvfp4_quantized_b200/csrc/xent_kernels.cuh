@@ -16,7 +16,8 @@
 // P's other entries have that entry's rounding anyway.  With the first number alone an fp32 dw was off by
 // 1.6e-3 to 2.2e-3 (2-norm; 300 x 1000 x 8000 with equal dloss), and a bf16 one by 2.2e-3, of which 1.65e-3
 // are its own rounding.  (P times both numbers wherever a tile and a stage of 64 tokens hold a target, which
-// needs no sorting: 2048 x 2048 x 32000 697 us for 539, 8192 x 1024 x 1000 143 for 92.)
+// needs no sorting: backward 2048 x 2048 x 32000 697 us, with sorting 570, with one number 530; 8192 x 1024 x
+// 1000, 5100 targets in one tile of four, 143, 130 and 92.)
 //
 // All three products are bf16 with fp32 sums on the tensor cores, in one persistent kernel shape
 // (mm_pair_kernel): a pair of SMs forms 256x256 tiles with tcgen05.mma.cta_group::2, each SM
