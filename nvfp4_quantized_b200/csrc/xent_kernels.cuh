@@ -240,7 +240,7 @@ __device__ __forceinline__ float xent_exact(const MmArgs &a, int64_t t, int y, i
 constexpr int kSortTokens = 2048, kSortTiles = 4096;   // of a block; tiles at a time in shared memory
 enum SortPhase { kCount = 1, kScan = 2, kRank = 4 };
 
-// Exclusive sum over the block's 1024 threads of v; `sum` becomes the carry plus all of them.
+// Exclusive sum over the block's 1024 threads of v, on top of `carry`, which gains their sum.
 __device__ __forceinline__ int sort_scan(int v, int &carry, int (&sh)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int s = v;

@@ -60,9 +60,9 @@ def check_norm(got, want, var, bound, what):
 
 
 # tokens, hidden size, vocabulary: one stage of tokens and several, ends inside a stage; vocabularies of few
-# tiles (every stage of every tile has a target) and of many (few have one); more stages than a word has bits
+# tiles (with many targets each) and of many (few have one); more tokens than a block sorts; two pieces
 SHAPES = [(16, 512, 3000), (31, 130, 700), (64, 256, 5000), (65, 264, 20001), (300, 1000, 8000), (777, 500, 20000),
-          (1024, 512, 257), (2048, 512, 8000), (2049, 72, 3001), (4500, 64, 2500)]
+          (1024, 512, 257), (2048, 512, 8000), (2049, 72, 3001), (4500, 64, 2500), (8200, 72, 40000)]
 
 
 @pytest.mark.parametrize("equal", [False, True])
