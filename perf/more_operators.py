@@ -116,7 +116,7 @@ def _view(g, R, C, std):
     s = (top / (6 * scale)).to(torch.float8_e4m3fn)
     mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
     code = torch.bucketize(x.abs() / (s.float() * scale)[:, :, None].clamp(min=1e-30), mid, out_int32=True).to(torch.uint8)
-    code = (code + 8 * (x < 0)).view(R, C // 2, 2)
+    code = (code + (x < 0).to(torch.uint8) * 8).view(R, C // 2, 2)
     order = s.view(torch.uint8).view(R // 128, 4, 32, C // 64, 4).permute(0, 3, 2, 1, 4)
     return code[:, :, 0] + 16 * code[:, :, 1], order.reshape(-1).contiguous(), scale.reshape(1)
 
