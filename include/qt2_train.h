@@ -1,14 +1,14 @@
 /*
  * qt2_train.h -- C ABI of the training operators beside the quantized linears (qt2.h) for NVIDIA
  * B200 (sm_100a), in the library libqt2_train.so: layer norm, the head's softmax cross entropy
- * over a large vocabulary, and the global gradient norm with clipping, each with what a training
- * step needs of it.
+ * over a large vocabulary, the gated feed-forward product on NVFP4 operands, and the global gradient
+ * norm with clipping, each with what a training step needs of it.
  *
  * Conventions are those of qt2.h (device pointers owned by the caller, work enqueued on `stream`,
  * arguments validated on the host before any launch, negative qt2_status on error, no allocation,
  * no abort, one NVTX range per call), with these differences:
- *   - Dimensions are any positive ints below 2^30, not multiples of 128 (a matrix of the head loss
- *     has fewer than 2^44 elements).  Matrices are row-major with a leading dimension that is a
+ *   - Dimensions are any positive ints below 2^30, not multiples of 128 unless a call says so (a matrix
+ *     of the head loss or of a gated product has fewer than 2^44 elements).  Matrices are row-major with a leading dimension that is a
  *     multiple of 8 elements, at least the row's length and below 2^40 (x and w of the head loss:
  *     2^39), and 16-byte aligned bases.  Elements between a row's length and its leading dimension
  *     are neither used nor written.  All other arrays are contiguous.
@@ -106,6 +106,39 @@ QT2_API qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64
                                        const float *dloss, int64_t T, int64_t K, int64_t V, int64_t ldx, int64_t ldw,
                                        int64_t ignore_index, void *dx, int64_t lddx, void *dw, int dw_dtype,
                                        int64_t lddw, void *workspace, size_t ws_bytes, qt2_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Gated feed-forward product: both projections, the activation and the product in one kernel.
+ *   g = alpha ga gg sum_k val(a)*sa * val(b_gate)*sg,  u the same of b_up,  h = act(g) * u.
+ * a is an [M][K] view (the quantized x), b_gate and b_up are [F][K] views (the two weights, each with a
+ * tensor scale of its own), as qt2_gemm_nvfp4 takes them; M, F and K are multiples of 128.  act(x) = x s(x):
+ *   QT2_ACT_SILU       s = 1 / (1 + exp(-x)),
+ *   QT2_ACT_GELU_TANH  s = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (x + 0.044715 x^3).
+ * Sums, activation and product are fp32, each output rounded once.  h [M][F] is bf16; gate and up [M][F]
+ * (bf16, both with leading dimension ldgu) are what the backward pass needs: both, or both NULL.  They may
+ * be the two halves of one [M][2F] matrix.
+ * --------------------------------------------------------------------------------------- */
+enum { QT2_ACT_SILU = 0, QT2_ACT_GELU_TANH = 1 };
+QT2_API qt2_status qt2_gemm_nvfp4_gated(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b_gate,
+                                        const qt2_nvfp4_view *b_up, int64_t M, int64_t F, int64_t K, float alpha,
+                                        int act, void *gate, void *up, int64_t ldgu, void *h, int64_t ldh,
+                                        qt2_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Backward of the gated product, in the epilogue of the down projection's dgrad:
+ *   dh = alpha ga gb sum_k val(a)*sa * val(b)*sb              (fp32, never stored),
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate),  h = act(gate) * up.
+ * a is an [M][K] view (the output's gradient), b an [F][K] view (the down projection's weight with its
+ * output dimension contracted): the row view of dy and the column view of the weight that qt2_quant_msedEN
+ * gives, with alpha = 2^-7.  gate and up are what the forward pass kept.  dgate and dup [M][F] bf16 (leading
+ * dimension lddgu) are the output gradients of the two projections, for qt2_linear_bwd and
+ * qt2_linear_bwd_views; h [M][F] bf16, what the down projection's wgrad contracts, may be NULL.
+ * M, F and K are multiples of 128.  dgate may be gate and dup may be up (with lddgu = ldgu).
+ * --------------------------------------------------------------------------------------- */
+QT2_API qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b, int64_t M, int64_t F,
+                                            int64_t K, float alpha, int act, const void *gate, const void *up,
+                                            int64_t ldgu, void *dgate, void *dup, int64_t lddgu, void *h, int64_t ldh,
+                                            qt2_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Global norm of many gradients, and clipping by it.  A gradient is a contiguous array of numel

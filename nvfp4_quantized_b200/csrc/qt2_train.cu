@@ -1,5 +1,6 @@
 // qt2_train.cu -- the training operators' library: kernel launchers and the C ABI declared in
-// include/qt2_train.h (layer norm, the head's softmax cross entropy, gradient norm and clipping).
+// include/qt2_train.h (layer norm, the head's softmax cross entropy, the gated feed-forward product,
+// gradient norm and clipping).
 //
 // One translation unit, with a device status word, fault hook and caches of its own.  Built for
 // sm_100a only into libqt2_train.so.
@@ -12,6 +13,7 @@
 #include "norm_kernels.cuh"
 #include "grad_kernels.cuh"
 #include "xent_kernels.cuh"
+#include "gated_kernels.cuh"
 
 using namespace qt2;
 
@@ -408,6 +410,50 @@ qt2_status xent_check(const void *x, const void *w, const int64_t *targets, int6
     return QT2_OK;
 }
 
+// ------------------------------------------------------------------------------- gated product
+bool views_given(const qt2_nvfp4_view *v) { return v && v->codes && v->scales && v->tensor_scale; }
+bool view_aligned(const qt2_nvfp4_view *v) {
+    return aligned(v->codes, 16) && aligned(v->scales, 16) && aligned(v->tensor_scale, 4);
+}
+
+// Multiples of 128, and no more than 2^31 steps of a tile in all.
+bool gated_dims_ok(int64_t M, int64_t F, int64_t K) {
+    const int64_t most = int64_t(1) << 44;
+    if (!dim_ok(M) || !dim_ok(F) || !dim_ok(K) || M % 128 || F % 128 || K % 128) return false;
+    if (M * F >= most || M * K >= most || F * K >= most) return false;
+    return ceil_div(M, 256) * (F / 128) <= INT32_MAX / ceil_div(K, 256);
+}
+
+// Codes in boxes of 128 rows, scale atoms as rows of K/64 512-byte atoms, `atoms` rows a box.
+bool encode_view(CUtensorMap *codes, CUtensorMap *scales, const qt2_nvfp4_view *v, int64_t R, int64_t K, int atoms) {
+    return encode_tmap_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, v->codes, (uint64_t)K / 2, (uint64_t)R,
+                          (uint64_t)K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_tmap_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, v->scales, (uint64_t)K, (uint64_t)R / 128,
+                          (uint64_t)K * 8, 256, (uint32_t)atoms, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool rows_of_32_bytes(const void *p, int64_t ld) { return !p || (aligned(p, 32) && ld % 16 == 0); }
+
+template <bool BWD, int ACT>
+cudaError_t launch_gated(const GatedMaps &maps, const GatedArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(gated_pair_kernel<BWD, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    GatedCfg::kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.F, BWD ? 256 : 128);
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
+    return launch(gated_pair_kernel<BWD, ACT>, (unsigned)(2 * clusters), GatedCfg::kThreads, GatedCfg::kSmemBytes, s,
+                  maps, a);
+}
+template <bool BWD>
+cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream_t s) {
+    return act == QT2_ACT_SILU ? launch_gated<BWD, QT2_ACT_SILU>(maps, a, s)
+                               : launch_gated<BWD, QT2_ACT_GELU_TANH>(maps, a, s);
+}
+
 // ------------------------------------------------------------------------------- gradients
 qt2_status grad_check(const qt2_grad *g, int64_t count, bool with_out) {
     if (!g) return QT2_ERR_INVALID_ARG;
@@ -743,6 +789,76 @@ qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64_t *targ
     if (!dx) return QT2_OK;
     a.splits = p.splits;
     return from_cuda(launch_xent_dx(a, dx, lddx, s));
+}
+
+qt2_status qt2_gemm_nvfp4_gated(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b_gate, const qt2_nvfp4_view *b_up,
+                                int64_t M, int64_t F, int64_t K, float alpha, int act, void *gate, void *up,
+                                int64_t ldgu, void *h, int64_t ldh, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!views_given(a) || !views_given(b_gate) || !views_given(b_up) || !h || !gate != !up ||
+        (act != QT2_ACT_SILU && act != QT2_ACT_GELU_TANH))
+        return QT2_ERR_INVALID_ARG;
+    if (!gated_dims_ok(M, F, K) || !ld_shape_ok(ldh, F) || (gate && !ld_shape_ok(ldgu, F))) return QT2_ERR_SHAPE;
+    if (!view_aligned(a) || !view_aligned(b_gate) || !view_aligned(b_up) || !aligned(h, 16) || ldh % 8 ||
+        (gate && (!aligned(gate, 16) || !aligned(up, 16) || ldgu % 8)))
+        return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    GatedMaps maps{};
+    if (!encode_view(&maps.a, &maps.sfa, a, M, K, 1) || !encode_view(&maps.b[0], &maps.sfb[0], b_gate, F, K, 1) ||
+        !encode_view(&maps.b[1], &maps.sfb[1], b_up, F, K, 1))
+        return QT2_ERR_CUDA;
+    GatedArgs g{};
+    g.ga = a->tensor_scale;
+    g.gb[0] = b_gate->tensor_scale;
+    g.gb[1] = b_up->tensor_scale;
+    g.alpha = alpha;
+    g.M = (int)M;
+    g.F = (int)F;
+    g.K = (int)K;
+    g.m_fast = M < 2 * F;
+    g.gate = static_cast<__nv_bfloat16 *>(gate);
+    g.up = static_cast<__nv_bfloat16 *>(up);
+    g.ldgu = ldgu;
+    g.h = static_cast<__nv_bfloat16 *>(h);
+    g.ldh = ldh;
+    g.wide = rows_of_32_bytes(h, ldh) && rows_of_32_bytes(gate, ldgu) && rows_of_32_bytes(up, ldgu);
+    return from_cuda(gated<false>(maps, g, act, as_stream(stream)));
+}
+
+qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b, int64_t M, int64_t F, int64_t K,
+                                    float alpha, int act, const void *gate, const void *up, int64_t ldgu, void *dgate,
+                                    void *dup, int64_t lddgu, void *h, int64_t ldh, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!views_given(a) || !views_given(b) || !gate || !up || !dgate || !dup ||
+        (act != QT2_ACT_SILU && act != QT2_ACT_GELU_TANH))
+        return QT2_ERR_INVALID_ARG;
+    if (!gated_dims_ok(M, F, K) || !ld_shape_ok(ldgu, F) || !ld_shape_ok(lddgu, F) || (h && !ld_shape_ok(ldh, F)))
+        return QT2_ERR_SHAPE;
+    if (!view_aligned(a) || !view_aligned(b) || !aligned(gate, 16) || !aligned(up, 16) || ldgu % 8 ||
+        !aligned(dgate, 16) || !aligned(dup, 16) || lddgu % 8 || (h && (!aligned(h, 16) || ldh % 8)))
+        return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    GatedMaps maps{};
+    if (!encode_view(&maps.a, &maps.sfa, a, M, K, 1) || !encode_view(&maps.b[0], &maps.sfb[0], b, F, K, 2))
+        return QT2_ERR_CUDA;
+    GatedArgs g{};
+    g.ga = a->tensor_scale;
+    g.gb[0] = b->tensor_scale;
+    g.alpha = alpha;
+    g.M = (int)M;
+    g.F = (int)F;
+    g.K = (int)K;
+    g.m_fast = M < F;
+    g.gate = static_cast<__nv_bfloat16 *>(const_cast<void *>(gate));
+    g.up = static_cast<__nv_bfloat16 *>(const_cast<void *>(up));
+    g.ldgu = ldgu;
+    g.dgate = static_cast<__nv_bfloat16 *>(dgate);
+    g.dup = static_cast<__nv_bfloat16 *>(dup);
+    g.lddgu = lddgu;
+    g.h = static_cast<__nv_bfloat16 *>(h);
+    g.ldh = ldh;
+    g.wide = rows_of_32_bytes(dgate, lddgu) && rows_of_32_bytes(dup, lddgu) && rows_of_32_bytes(h, ldh);
+    return from_cuda(gated<true>(maps, g, act, as_stream(stream)));
 }
 
 qt2_status qt2_grad_norm_workspace_size(const qt2_grad *grads, int64_t count, size_t *bytes) {

@@ -1,5 +1,6 @@
 """Thin ctypes binding of the training operators' C ABI (include/qt2_train.h): layer norm, the
-head's softmax cross entropy and the global gradient norm with clipping, in ``libqt2_train.so``.
+head's softmax cross entropy, the gated feed-forward product on NVFP4 operands and the global gradient
+norm with clipping, in ``libqt2_train.so``.
 
 Argument marshalling only, in the manner of ``qt2``: every function forwards to the entry point of
 the same name with the tensors' device pointers and the current CUDA stream (or ``stream``), and
@@ -21,13 +22,16 @@ import threading
 import torch
 
 from . import qt2
-from .qt2 import QT2_DTYPE_BF16, QT2_DTYPE_F32, QT2_ERR_DEVICE, QT2_ERR_INVALID_ARG, FaultHookC, QT2Error
+from .qt2 import (QT2_DTYPE_BF16, QT2_DTYPE_F32, QT2_ERR_DEVICE, QT2_ERR_INVALID_ARG, QT2_ERR_SHAPE, FaultHookC,
+                  QT2Error)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # QT2_LIBRARY=checked loads the checked build, as in qt2
 LIB_PATH = os.path.join(_PKG, "libqt2_train_checked.so" if os.environ.get("QT2_LIBRARY") == "checked"
                         else "libqt2_train.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qt2_train.h")
+
+QT2_ACT_SILU, QT2_ACT_GELU_TANH = 0, 1
 
 _DTYPE = {torch.bfloat16: QT2_DTYPE_BF16, torch.float32: QT2_DTYPE_F32}
 
@@ -53,7 +57,7 @@ def lib() -> ctypes.CDLL:
                                    "(there is no fallback path)")
             L = ctypes.CDLL(LIB_PATH)
             i32, i64, sz, vp, f32 = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-            psz = ctypes.POINTER(ctypes.c_size_t)
+            psz, pv = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(qt2.NVFP4ViewC)
             sigs = {
                 "qt2_train_device_status": (i32, [vp, ctypes.POINTER(ctypes.c_int)]),
                 "qt2_train_set_fault_hook": (None, [FaultHookC, vp]),
@@ -67,6 +71,9 @@ def lib() -> ctypes.CDLL:
                 "qt2_linear_xent_bwd_workspace_size": (i32, [i64, i64, i64, psz]),
                 "qt2_linear_xent_bwd": (i32, [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp, i64, vp, i32, i64,
                                               vp, sz, vp]),
+                "qt2_gemm_nvfp4_gated": (i32, [pv, pv, pv, i64, i64, i64, f32, i32, vp, vp, i64, vp, i64, vp]),
+                "qt2_gemm_nvfp4_gated_bwd": (i32, [pv, pv, i64, i64, i64, f32, i32, vp, vp, i64, vp, vp, i64, vp, i64,
+                                                   vp]),
                 "qt2_grad_norm_workspace_size": (i32, [vp, i64, psz]),
                 "qt2_grad_norm": (i32, [vp, i64, vp, vp, sz, vp]),
                 "qt2_grad_clip": (i32, [vp, i64, vp, f32, vp]),
@@ -222,6 +229,43 @@ def qt2_linear_xent_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     px, pw, pt, ps, pg, pdx, pdw, pws = _ptrs(fn, x, w, targets, lse, dloss, dx, dw, workspace)
     _check(fn, lib().qt2_linear_xent_bwd(px, pw, pt, ps, pg, T, K, V, ldx, ldw, ignore_index, pdx, lddx, pdw, dw_dtype,
                                          lddw, pws, ws_bytes, _stream(stream)))
+
+
+def _view(fn: str, v: qt2.View, R: int, C: int):
+    """The C form of an [R, C] view whose arrays are on the current device."""
+    if v.codes.dtype is not torch.uint8 or v.scales.dtype is not torch.uint8:
+        raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+    _only(fn, torch.float32, v.tensor_scale)
+    _vectors(fn, v.codes, v.scales)
+    # a view of other sizes holds fewer elements than the call reads, or others (sizes that no call takes are its to refuse)
+    if R > 0 and C > 0 and (v.codes.numel() != R * C // 2 or v.scales.numel() != R * C // 16):
+        raise QT2Error(fn, QT2_ERR_SHAPE)
+    return ctypes.byref(qt2.NVFP4ViewC(*_ptrs(fn, v.codes, v.scales, v.tensor_scale)))
+
+
+def qt2_gemm_nvfp4_gated(a: qt2.View, b_gate: qt2.View, b_up: qt2.View, M: int, F: int, K: int, alpha: float, act: int,
+                         gate: torch.Tensor | None, up: torch.Tensor | None, ldgu: int, h: torch.Tensor, ldh: int,
+                         stream=None) -> None:
+    """h = act(g) * u of the two products g = alpha a b_gate^T and u = alpha a b_up^T (views [M, K], [F, K],
+    [F, K]); g and u go to gate and up (for the backward pass; None: not kept).  bf16 outputs."""
+    fn = "qt2_gemm_nvfp4_gated"
+    _only(fn, torch.bfloat16, gate, up, h)
+    pa, pg, pu = _view(fn, a, M, K), _view(fn, b_gate, F, K), _view(fn, b_up, F, K)
+    qg, qu, qh = _ptrs(fn, gate, up, h)
+    _check(fn, lib().qt2_gemm_nvfp4_gated(pa, pg, pu, M, F, K, alpha, act, qg, qu, ldgu, qh, ldh, _stream(stream)))
+
+
+def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, alpha: float, act: int,
+                             gate: torch.Tensor, up: torch.Tensor, ldgu: int, dgate: torch.Tensor, dup: torch.Tensor,
+                             lddgu: int, h: torch.Tensor | None, ldh: int, stream=None) -> None:
+    """dgate = dh up act'(gate), dup = dh act(gate) and h = act(gate) up (None: not wanted) of
+    dh = alpha a b^T (views [M, K], [F, K]), which is not stored.  bf16 outputs."""
+    fn = "qt2_gemm_nvfp4_gated_bwd"
+    _only(fn, torch.bfloat16, gate, up, dgate, dup, h)
+    pa, pb = _view(fn, a, M, K), _view(fn, b, F, K)
+    qg, qu, qdg, qdu, qh = _ptrs(fn, gate, up, dgate, dup, h)
+    _check(fn, lib().qt2_gemm_nvfp4_gated_bwd(pa, pb, M, F, K, alpha, act, qg, qu, ldgu, qdg, qdu, lddgu, qh, ldh,
+                                              _stream(stream)))
 
 
 class GradList:

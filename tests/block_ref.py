@@ -1,0 +1,88 @@
+"""Plain 64-bit implementations of a transformer block's operators (gated product, norm of queries and keys
+with rotation, AdamW) and the error bounds that the kernels' arithmetic allows (u = 2^-24, the half step
+of fp32; an output type adds half a step of its own: train_ref.check)."""
+import math
+
+import torch
+
+U = 2.0 ** -24
+SILU, GELU = 0, 1
+
+
+# ------------------------------------------------------------------------------------------ views
+def random_view(R, C, seed, scale=1.0, device="cuda"):
+    """(codes, scales, tensor_scale) of an [R, C] view: every code, E4M3 scales from 2^-4 to 8 and some zeros."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    codes = torch.randint(0, 256, (R, C // 2), generator=g, device=device, dtype=torch.uint8)
+    scales = torch.randint(0x18, 0x51, (R * C // 16,), generator=g, device=device, dtype=torch.uint8)
+    scales[torch.rand(scales.shape, generator=g, device=device) < 0.02] = 0
+    return codes, scales, torch.full((1,), scale, device=device)
+
+
+def view_values(codes, scales, tensor_scale):
+    """The elements' values in 64 bits."""
+    R, C = codes.shape[0], 2 * codes.shape[1]
+    dev = codes.device
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=dev)
+    nib = torch.stack([codes & 15, codes >> 4], 2).view(R, C).long()
+    x = grid[nib & 7] * (1 - 2 * (nib >> 3)).double()
+    r, j = torch.arange(R, device=dev)[:, None], torch.arange(C // 16, device=dev)
+    at = ((r // 128) * (C // 64) + j // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + j % 4
+    s = scales[at].view(torch.float8_e4m3fn).double()
+    return x * s.repeat_interleave(16, 1) * tensor_scale.double()
+
+
+# ------------------------------------------------------------------------------------------ gated product
+def act(kind, x):
+    """(act(x), act'(x), exponent) in 64 bits."""
+    if kind == SILU:
+        t, dt = x, torch.ones_like(x)
+    else:
+        c = 2 * math.sqrt(2 / math.pi)
+        t, dt = c * (x + 0.044715 * x ** 3), c * (1 + 3 * 0.044715 * x ** 2)
+    s = torch.sigmoid(t)
+    return x * s, s + x * s * torch.sigmoid(-t) * dt, t
+
+
+def act_bounds(kind, x):
+    """Errors of act and act' computed in fp32 from x.
+
+    exp(-t): the argument's roundings (at most six) and log2(e)'s, and 2 units of ex2: relative (8 |t| + 4) u;
+    s = 1 / (1 + e): e / (1 + e) of it, the sum's rounding and 2 units of the division: at most d below.
+    1 - s is off by s d' where d' is that error and its own rounding u, and in act' it meets x and dt."""
+    f, df, t = act(kind, x)
+    s, dt = torch.sigmoid(t), (torch.ones_like(t) if kind == SILU else 2 * math.sqrt(2 / math.pi) * (1 + 0.134145 * x ** 2))
+    t = t.clamp(-90, 90)
+    d = (torch.sigmoid(-t) * (8 * t.abs() + 4) + 6) * U
+    tiny = x.abs() * 1e-37   # exp(-t) past fp32: s = 0 (SiLU below -88, GELU from the clamp at -10 on)
+    e_f = f.abs() * (d + 2 * U) + tiny
+    far = torch.where(x.abs() > 10, torch.zeros_like(x), dt)
+    e_df = s * d + x.abs() * s * (torch.sigmoid(-t) * (d + 6 * U) + s * d + U) * (dt if kind == SILU else far) + 2 * U * df.abs() + tiny
+    return e_f, e_df
+
+
+def _product(a, b, alpha, K):
+    """a b^T, and what fp32 sums of the tensor cores (at most a whole step lost each time 16 products join) are off by."""
+    z = alpha * (a @ b.T)
+    return z, alpha * (2 * U * (K / 16 + 16) * (a.abs() @ b.abs().T)) + 4 * U * z.abs()
+
+
+def gated_fwd(a, bg, bu, alpha, kind):
+    """(h, g, u) and bounds, from the operands' values."""
+    K = a.shape[1]
+    g, e_g = _product(a, bg, alpha, K)
+    u, e_u = _product(a, bu, alpha, K)
+    f, df, _ = act(kind, g)
+    e_f = act_bounds(kind, g)[0] + e_g * (df.abs() + 0.1) + e_g ** 2   # |act''| is below 1.6
+    return (f * u, g, u), (e_f * u.abs() + (f.abs() + e_f) * e_u + 3 * U * (f * u).abs(), e_g, e_u)
+
+
+def gated_bwd(a, b, alpha, kind, gate, up):
+    """(dgate, dup, h) and bounds."""
+    dh, e_dh = _product(a, b, alpha, a.shape[1])
+    g, u = gate.double(), up.double()
+    f, df, _ = act(kind, g)
+    e_f, e_df = act_bounds(kind, g)
+    dg, du, h = dh * u * df, dh * f, f * u
+    e_dg = e_dh * (u * df).abs() + (dh.abs() + e_dh) * u.abs() * e_df + 3 * U * dg.abs()
+    return (dg, du, h), (e_dg, e_dh * f.abs() + (dh.abs() + e_dh) * e_f + 2 * U * du.abs(), e_f * u.abs() + 2 * U * h.abs())

@@ -1,0 +1,119 @@
+"""A transformer block's operators (include/qt2_train.h): host-side refusals and injected failures, without a
+GPU (fake, never-dereferenced device addresses)."""
+import ctypes
+
+import pytest
+import torch
+
+from nvfp4_quantized_b200 import build as qbuild
+from nvfp4_quantized_b200 import qt2
+from nvfp4_quantized_b200 import qt2_train as tr
+
+OK, ARG, SHAPE, ALIGN, WS = 0, qt2.QT2_ERR_INVALID_ARG, qt2.QT2_ERR_SHAPE, qt2.QT2_ERR_ALIGN, qt2.QT2_ERR_WORKSPACE
+DEV, CUDA = qt2.QT2_ERR_DEVICE, qt2.QT2_ERR_CUDA
+
+
+@pytest.fixture(scope="module")
+def L():
+    qbuild.build_train()
+    return tr.lib()
+
+
+def injected(call):
+    """Skipping every CUDA call completes; failing the k-th returns that site's error and enqueues nothing further."""
+    with tr.fault_hook(lambda site: qt2.FAULT_SKIP) as h:
+        assert call() == OK
+    sites = list(h.sites)
+    assert sites[0] == "device" and "launch" in sites
+    for k in range(len(sites)):
+        seen = []
+
+        def decide(site, k=k, seen=seen):
+            seen.append(site)
+            return qt2.FAULT_FAIL if len(seen) == k + 1 else qt2.FAULT_SKIP
+        with tr.fault_hook(decide):
+            st = call()
+        assert len(seen) == k + 1 and st == (DEV if sites[k] == "device" else CUDA), (k, sites[k], st)
+    return sites
+
+
+# ------------------------------------------------------------------------------------------ gated product
+def view(codes=0x1000, scales=0x2000, scale=0x3000):
+    return ctypes.byref(qt2.NVFP4ViewC(codes, scales, scale))
+
+
+def gated(L, a=view(), bg=view(), bu=view(), M=128, F=256, K=384, act=0, gate=0x4000, up=0x5000, ldgu=256, h=0x6000, ldh=256):
+    return L.qt2_gemm_nvfp4_gated(a, bg, bu, M, F, K, 1.0, act, gate, up, ldgu, h, ldh, None)
+
+
+def gated_bwd(L, a=view(), b=view(), M=128, F=256, K=384, act=0, gate=0x4000, up=0x5000, ldgu=256, dgate=0x6000, dup=0x7000,
+              lddgu=256, h=0x8000, ldh=256):
+    return L.qt2_gemm_nvfp4_gated_bwd(a, b, M, F, K, 1.0, act, gate, up, ldgu, dgate, dup, lddgu, h, ldh, None)
+
+
+SIZES = [(dict(M=0), SHAPE), (dict(F=0), SHAPE), (dict(K=-128), SHAPE), (dict(M=100), SHAPE), (dict(F=130), SHAPE), (dict(K=64), SHAPE),
+         (dict(M=1 << 30), SHAPE), (dict(ldgu=248), SHAPE), (dict(ldh=8), SHAPE), (dict(ldgu=1 << 40), SHAPE),
+         (dict(M=1 << 22, F=1 << 22, ldgu=1 << 22, ldh=1 << 22, lddgu=1 << 22), SHAPE),
+         (dict(M=1 << 21, F=1 << 22, K=1 << 21, ldgu=1 << 22, ldh=1 << 22, lddgu=1 << 22), SHAPE),
+         (dict(act=2), ARG), (dict(act=-1), ARG), (dict(a=None), ARG), (dict(a=view(codes=None)), ARG), (dict(a=view(scale=None)), ARG),
+         (dict(a=view(codes=0x1008)), ALIGN), (dict(a=view(scales=0x2004)), ALIGN), (dict(a=view(scale=0x3002)), ALIGN),
+         (dict(gate=0x4008), ALIGN), (dict(up=0x5002), ALIGN), (dict(h=0x6004), ALIGN), (dict(ldgu=260), ALIGN), (dict(ldh=257), ALIGN)]
+
+
+@pytest.mark.parametrize("bad,status", SIZES + [
+    (dict(bg=None), ARG), (dict(bu=view(scales=None)), ARG), (dict(gate=None), ARG), (dict(up=None), ARG), (dict(h=None), ARG),
+    (dict(bg=view(codes=0x1004)), ALIGN), (dict(bu=view(codes=0x1004)), ALIGN)])
+def test_gated_refusals(L, bad, status):
+    bad.pop("lddgu", None)
+    assert gated(L, **bad) == status
+
+
+@pytest.mark.parametrize("bad,status", SIZES + [
+    (dict(b=None), ARG), (dict(b=view(scale=None)), ARG), (dict(gate=None), ARG), (dict(up=None), ARG), (dict(dgate=None), ARG),
+    (dict(dup=None), ARG), (dict(lddgu=128), SHAPE), (dict(lddgu=260), ALIGN), (dict(dgate=0x6002), ALIGN), (dict(dup=0x7008), ALIGN),
+    (dict(b=view(scales=0x2008)), ALIGN)])
+def test_gated_bwd_refusals(L, bad, status):
+    if "lddgu" not in bad and bad.get("F", 0) > 1 << 20:
+        bad = dict(bad, lddgu=bad["F"])
+    assert gated_bwd(L, **bad) == status
+
+
+@pytest.mark.parametrize("call", [gated, lambda L: gated(L, gate=None, up=None, ldgu=0), lambda L: gated(L, act=1, M=384, F=128, ldgu=128, ldh=128),
+                                  gated_bwd, lambda L: gated_bwd(L, h=None, ldh=0, act=1)])
+def test_gated_failures_at_every_site(L, call):
+    sites = injected(lambda: call(L))
+    assert sites.count("launch") == 1
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU behaviour")
+def test_valid_calls_without_gpu_fail_loudly(L):
+    for st in (gated(L), gated_bwd(L)):
+        assert st == DEV
+
+
+def test_gated_binding_refuses_before_the_call(monkeypatch):
+    b, f = torch.zeros(128, 128, dtype=torch.bfloat16), torch.zeros(128, 128)
+
+    def v(R=128, C=128, codes=None, scales=None, scale=None):
+        return qt2.View(torch.zeros(R, C // 2, dtype=torch.uint8) if codes is None else codes,
+                        torch.zeros(R * C // 16, dtype=torch.uint8) if scales is None else scales, torch.zeros(1) if scale is None else scale)
+
+    def fwd(a=None, bg=None, bu=None, g=b, u=b, h=b):
+        tr.qt2_gemm_nvfp4_gated(a or v(), bg or v(), bu or v(), 128, 128, 128, 1.0, 0, g, u, 128, h, 128)
+
+    def bwd(a=None, w=None, g=b, u=b, dg=b, du=b, h=b):
+        tr.qt2_gemm_nvfp4_gated_bwd(a or v(), w or v(), 128, 128, 128, 1.0, 0, g, u, 128, dg, du, 128, h, 128)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # where a CPU tensor's "device" is: types and sizes come first
+    cases = [(lambda: fwd(g=f), ARG), (lambda: fwd(h=f), ARG), (lambda: bwd(dg=f), ARG), (lambda: bwd(u=f), ARG),
+             (lambda: fwd(a=v(scale=torch.zeros(1).double())), ARG), (lambda: fwd(bg=v(codes=torch.zeros(128, 64, dtype=torch.int8))), ARG),
+             (lambda: fwd(bu=v(codes=torch.zeros(64, 128, dtype=torch.uint8).t())), ARG), (lambda: bwd(w=v(scales=torch.zeros(2048, dtype=torch.uint8)[::2])), ARG),
+             (lambda: fwd(a=v(256)), SHAPE), (lambda: fwd(bu=v(128, 256)), SHAPE), (lambda: bwd(w=v(scales=torch.zeros(512, dtype=torch.uint8))), SHAPE)]
+    for k, (case, status) in enumerate(cases):
+        with pytest.raises(qt2.QT2Error) as e:
+            case()
+        assert e.value.status == status, k
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for case in (fwd, bwd):
+        with pytest.raises(qt2.QT2Error) as e:
+            case()
+        assert e.value.status == DEV
