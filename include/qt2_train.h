@@ -1,8 +1,9 @@
 /*
  * qt2_train.h -- C ABI of the training operators beside the quantized linears (qt2.h) for NVIDIA
  * B200 (sm_100a), in the library libqt2_train.so: layer norm, the head's softmax cross entropy
- * over a large vocabulary, the gated feed-forward product on NVFP4 operands, and the global gradient
- * norm with clipping, each with what a training step needs of it.
+ * over a large vocabulary, the gated feed-forward product on NVFP4 operands, the norm of queries and
+ * keys with the position rotation, and the global gradient norm with clipping, each with what a training
+ * step needs of it.
  *
  * Conventions are those of qt2.h (device pointers owned by the caller, work enqueued on `stream`,
  * arguments validated on the host before any launch, negative qt2_status on error, no allocation,
@@ -139,6 +140,46 @@ QT2_API qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_n
                                             int64_t K, float alpha, int act, const void *gate, const void *up,
                                             int64_t ldgu, void *dgate, void *dup, int64_t lddgu, void *h, int64_t ldh,
                                             qt2_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Norm of queries and keys for each head, with the position rotation, in one pass over the QKV linear's
+ * output.  x holds Hq + Hk heads of D elements for each of T tokens: head h of token t starts at element
+ * t * ldx + h * hsx, the Hq query heads first (with ldx = (Hq + 2 Hk) D and hsx = D they are part of rows
+ * that hold the values too, which are not touched; with hsx = T D and ldx = D the heads are outermost).
+ * Heads of queries alone or keys alone: Hk = 0 or Hq = 0.  For each head of each token:
+ *   r = 1 / sqrt(sum_d x_d^2 / D + eps),  a_d = x_d r w_d  (w = wq or wk, [D]; NULL stands for ones),
+ *   y = a with the pairs of its first R elements turned: (p, q) -> (p cos - q sin, q cos + p sin),
+ * pair i < R/2 being (i, i + R/2) with QT2_ROPE_HALVES, (2i, 2i + 1) with QT2_ROPE_PAIRS, and cos and sin
+ * rows positions[t] of the two fp32 tables [P][R/2].  positions (int64 [T]) NULL: token t is at t (T <= P).
+ * A position outside [0, P) leaves its token unturned and is reported as QT2_ERR_INVALID_ARG through
+ * qt2_train_device_status.  R = 0: nothing is turned; positions and tables may be NULL.
+ * x and y have type x_dtype, wq and wk w_dtype; all of it 16-byte aligned (positions 8), strides multiples of
+ * 8 elements, so that no two heads overlap.  D and R are multiples of 8, D <= 1024, R <= D.  Statistics and
+ * products are fp32, rounded once on writing (squares too: elements from 2^63 on overflow them).  y may be x
+ * with its strides.  eps >= 0 and finite.  T, Hq and Hk are below 2^30, 2^20 and 2^20.
+ * --------------------------------------------------------------------------------------- */
+enum { QT2_ROPE_HALVES = 0, QT2_ROPE_PAIRS = 1 };
+QT2_API qt2_status qt2_qk_norm_rope_fwd(const void *x, int x_dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                        int64_t ldx, int64_t hsx, const void *wq, const void *wk, int w_dtype,
+                                        float eps, const int64_t *positions, const float *cos, const float *sin,
+                                        int64_t P, int64_t R, int pairing, void *y, int64_t ldy, int64_t hsy,
+                                        qt2_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Backward of qt2_qk_norm_rope_fwd from its input x, with n = x r and b = dy turned the other way:
+ *   dx_d = r (b_d w_d - n_d sum_e (b_e w_e n_e) / D),  dwq_d = sum over tokens and query heads of b_d n_d,
+ * dwk the same over the key heads (zeros where there are none).  dy and dx have type x_dtype and strides of
+ * their own, dwq and dwk w_dtype.  dx, dwq and dwk may each be NULL (not wanted), not all of them.  dx may be
+ * dy or x, with its strides.  Positions outside the tables are not reported again.  Sums are fp32.
+ * Workspace: qt2_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned.
+ * --------------------------------------------------------------------------------------- */
+QT2_API qt2_status qt2_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t Hq, int64_t Hk, int64_t D, size_t *bytes);
+QT2_API qt2_status qt2_qk_norm_rope_bwd(const void *dy, int64_t lddy, int64_t hsdy, const void *x, int x_dtype,
+                                        int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t ldx, int64_t hsx,
+                                        const void *wq, const void *wk, int w_dtype, float eps,
+                                        const int64_t *positions, const float *cos, const float *sin, int64_t P,
+                                        int64_t R, int pairing, void *dx, int64_t lddx, int64_t hsdx, void *dwq,
+                                        void *dwk, void *workspace, size_t ws_bytes, qt2_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Global norm of many gradients, and clipping by it.  A gradient is a contiguous array of numel

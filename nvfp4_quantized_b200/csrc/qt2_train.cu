@@ -1,6 +1,6 @@
 // qt2_train.cu -- the training operators' library: kernel launchers and the C ABI declared in
 // include/qt2_train.h (layer norm, the head's softmax cross entropy, the gated feed-forward product,
-// gradient norm and clipping).
+// the norm of queries and keys with the rotation, gradient norm and clipping).
 //
 // One translation unit, with a device status word, fault hook and caches of its own.  Built for
 // sm_100a only into libqt2_train.so.
@@ -14,6 +14,7 @@
 #include "grad_kernels.cuh"
 #include "xent_kernels.cuh"
 #include "gated_kernels.cuh"
+#include "rope_kernels.cuh"
 
 using namespace qt2;
 
@@ -454,6 +455,98 @@ cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream
                                : launch_gated<BWD, QT2_ACT_GELU_TANH>(maps, a, s);
 }
 
+// ------------------------------------------------------------------------------- queries and keys
+// Rows a group of lanes has in flight, by the registers that they take.
+template <class T, int N>
+constexpr int kQkUnroll = std::max(1, (sizeof(T) == 2 ? 4 : 2) / N);
+
+// Blocks of the backward pass: each leaves a share of dw.
+int64_t qk_bwd_blocks(int64_t T, int64_t Hq, int64_t Hk) {
+    return std::min<int64_t>(148 * 3, ceil_div(T * (Hq + Hk), kQkThreads / 32));
+}
+
+template <class T, int G, int N>
+cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    constexpr int U = kQkUnroll<T, N>, kRows = 32 / G * U;
+    const int64_t items = ceil_div(a.T * a.heads[0], kRows) + ceil_div(a.T * a.heads[1], kRows);
+    return launch(qk_norm_rope_fwd_kernel<T, G, N, U>, (unsigned)ceil_div(items, kQkThreads / 32), kQkThreads, 0, s, a);
+}
+template <class T, int G, int N>
+cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    return launch(qk_norm_rope_bwd_kernel<T, G, N, kQkUnroll<T, N>>, (unsigned)a.parts, kQkThreads,
+                  a.D * (kQkThreads / 32) * sizeof(float), s, a);
+}
+template <bool BWD, class T, int G, int N>
+cudaError_t qk_launch(const QkArgs &a, cudaStream_t s) {
+    return BWD ? launch_qk_bwd<T, G, N>(a, s) : launch_qk_fwd<T, G, N>(a, s);
+}
+template <bool BWD, class T>
+cudaError_t qk_norm_rope(const QkArgs &a, cudaStream_t s) {
+    const int slots = a.D / 8;
+    if (slots <= 4) return qk_launch<BWD, T, 4, 1>(a, s);
+    if (slots <= 8) return qk_launch<BWD, T, 8, 1>(a, s);
+    if (slots <= 16) return qk_launch<BWD, T, 16, 1>(a, s);
+    if (slots <= 32) return qk_launch<BWD, T, 32, 1>(a, s);
+    if (slots <= 64) return qk_launch<BWD, T, 32, 2>(a, s);
+    return qk_launch<BWD, T, 32, 4>(a, s);
+}
+cudaError_t launch_qk_dw(const QkArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    return launch(qk_dw_kernel, dim3((unsigned)ceil_div(a.D, 32), 2), 1024, 0, s, a);
+}
+
+bool qk_dims_ok(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
+    const int64_t heads = int64_t(1) << 20;
+    return dim_ok(T) && Hq >= 0 && Hk >= 0 && Hq < heads && Hk < heads && Hq + Hk > 0 &&
+           T * (Hq + Hk) < (int64_t(1) << 32) && D > 0 && D <= 1024 && D % 8 == 0;
+}
+// T tokens of H heads of D elements, one inside the other either way, none over another.
+bool qk_strides_ok(int64_t T, int64_t H, int64_t D, int64_t ld, int64_t hs) {
+    const int64_t most = int64_t(1) << 40;
+    if (ld < 0 || hs < 0 || ld >= most || hs >= most) return false;
+    const __int128 heads = (__int128)(H - 1) * hs + D, tokens = (__int128)(T - 1) * ld + D;   // of a token, of a head
+    return ((H == 1 || hs >= D) && (T == 1 || ld >= heads)) || ((T == 1 || ld >= D) && (H == 1 || hs >= tokens));
+}
+qt2_status qk_check(const void *x, int x_dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t ldx, int64_t hsx,
+                    const void *wq, const void *wk, int w_dtype, float eps, const int64_t *positions, const float *cos,
+                    const float *sin, int64_t P, int64_t R, int pairing) {
+    if (!x || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !(eps >= 0.0f) || std::isinf(eps) ||
+        (pairing != QT2_ROPE_HALVES && pairing != QT2_ROPE_PAIRS) || (R != 0 && (!cos || !sin)))
+        return QT2_ERR_INVALID_ARG;
+    if (!qk_dims_ok(T, Hq, Hk, D) || R < 0 || R > D || R % 8 || !qk_strides_ok(T, Hq + Hk, D, ldx, hsx))
+        return QT2_ERR_SHAPE;
+    if (R != 0 && (!dim_ok(P) || (!positions && T > P))) return QT2_ERR_SHAPE;
+    if (!aligned(x, 16) || ldx % 8 || hsx % 8 || !aligned(wq, 16) || !aligned(wk, 16) || !aligned(positions, 8) ||
+        !aligned(cos, 16) || !aligned(sin, 16))
+        return QT2_ERR_ALIGN;
+    return QT2_OK;
+}
+QkArgs qk_args(const void *x, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t ldx, int64_t hsx, const void *wq,
+               const void *wk, int w_dtype, float eps, const int64_t *positions, const float *cos, const float *sin,
+               int64_t P, int64_t R, int pairing) {
+    QkArgs a{};
+    a.x = x;
+    a.w[0] = wq;
+    a.w[1] = wk;
+    a.pos = positions;
+    a.cos = cos;
+    a.sin = sin;
+    a.P = P;
+    a.T = T;
+    a.heads[0] = (int)Hq;
+    a.heads[1] = (int)Hk;
+    a.D = (int)D;
+    a.R = (int)R;
+    a.ldx = ldx;
+    a.hsx = hsx;
+    a.pairs = pairing == QT2_ROPE_PAIRS;
+    a.w_f32 = w_dtype == QT2_DTYPE_F32;
+    a.eps = eps;
+    return a;
+}
+
 // ------------------------------------------------------------------------------- gradients
 qt2_status grad_check(const qt2_grad *g, int64_t count, bool with_out) {
     if (!g) return QT2_ERR_INVALID_ARG;
@@ -859,6 +952,71 @@ qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_vie
     g.ldh = ldh;
     g.wide = rows_of_32_bytes(dgate, lddgu) && rows_of_32_bytes(dup, lddgu) && rows_of_32_bytes(h, ldh);
     return from_cuda(gated<true>(maps, g, act, as_stream(stream)));
+}
+
+qt2_status qt2_qk_norm_rope_fwd(const void *x, int x_dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t ldx,
+                                int64_t hsx, const void *wq, const void *wk, int w_dtype, float eps,
+                                const int64_t *positions, const float *cos, const float *sin, int64_t P, int64_t R,
+                                int pairing, void *y, int64_t ldy, int64_t hsy, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!y) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = qk_check(x, x_dtype, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P,
+                                       R, pairing))
+        return st;
+    if (!qk_strides_ok(T, Hq + Hk, D, ldy, hsy)) return QT2_ERR_SHAPE;
+    if (!aligned(y, 16) || ldy % 8 || hsy % 8) return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R, pairing);
+    a.y = y;
+    a.ldy = ldy;
+    a.hsy = hsy;
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<false, float>(a, s)
+                                              : qk_norm_rope<false, __nv_bfloat16>(a, s));
+}
+
+qt2_status qt2_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t Hq, int64_t Hk, int64_t D, size_t *bytes) {
+    if (!bytes) return QT2_ERR_INVALID_ARG;
+    if (!qk_dims_ok(T, Hq, Hk, D)) return QT2_ERR_SHAPE;
+    *bytes = align_up((size_t)qk_bwd_blocks(T, Hq, Hk) * 2 * D * sizeof(float), kWsAlign);
+    return QT2_OK;
+}
+
+qt2_status qt2_qk_norm_rope_bwd(const void *dy, int64_t lddy, int64_t hsdy, const void *x, int x_dtype, int64_t T,
+                                int64_t Hq, int64_t Hk, int64_t D, int64_t ldx, int64_t hsx, const void *wq,
+                                const void *wk, int w_dtype, float eps, const int64_t *positions, const float *cos,
+                                const float *sin, int64_t P, int64_t R, int pairing, void *dx, int64_t lddx,
+                                int64_t hsdx, void *dwq, void *dwk, void *workspace, size_t ws_bytes,
+                                qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!dy || (!dx && !dwq && !dwk)) return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = qk_check(x, x_dtype, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P,
+                                       R, pairing))
+        return st;
+    if (!qk_strides_ok(T, Hq + Hk, D, lddy, hsdy) || (dx && !qk_strides_ok(T, Hq + Hk, D, lddx, hsdx)))
+        return QT2_ERR_SHAPE;
+    if (!aligned(dy, 16) || lddy % 8 || hsdy % 8 || (dx && (!aligned(dx, 16) || lddx % 8 || hsdx % 8)) ||
+        !aligned(dwq, 16) || !aligned(dwk, 16))
+        return QT2_ERR_ALIGN;
+    size_t need = 0;
+    if (const qt2_status st = qt2_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D, &need)) return st;
+    if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    if (const qt2_status st = check_device()) return st;
+    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R, pairing);
+    a.dy = dy;
+    a.lddy = lddy;
+    a.hsdy = hsdy;
+    a.y = dx;
+    a.ldy = lddx;
+    a.hsy = hsdx;
+    a.dw[0] = dwq;
+    a.dw[1] = dwk;
+    a.part = dwq || dwk ? static_cast<float *>(workspace) : nullptr;
+    a.parts = (int)qk_bwd_blocks(T, Hq, Hk);
+    const cudaStream_t s = as_stream(stream);
+    cudaError_t e = x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<true, float>(a, s) : qk_norm_rope<true, __nv_bfloat16>(a, s);
+    if (e == cudaSuccess && a.part) e = launch_qk_dw(a, s);
+    return from_cuda(e);
 }
 
 qt2_status qt2_grad_norm_workspace_size(const qt2_grad *grads, int64_t count, size_t *bytes) {

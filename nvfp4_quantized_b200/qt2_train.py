@@ -1,6 +1,6 @@
 """Thin ctypes binding of the training operators' C ABI (include/qt2_train.h): layer norm, the
-head's softmax cross entropy, the gated feed-forward product on NVFP4 operands and the global gradient
-norm with clipping, in ``libqt2_train.so``.
+head's softmax cross entropy, the gated feed-forward product on NVFP4 operands, the norm of queries and
+keys with the position rotation and the global gradient norm with clipping, in ``libqt2_train.so``.
 
 Argument marshalling only, in the manner of ``qt2``: every function forwards to the entry point of
 the same name with the tensors' device pointers and the current CUDA stream (or ``stream``), and
@@ -32,6 +32,7 @@ LIB_PATH = os.path.join(_PKG, "libqt2_train_checked.so" if os.environ.get("QT2_L
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qt2_train.h")
 
 QT2_ACT_SILU, QT2_ACT_GELU_TANH = 0, 1
+QT2_ROPE_HALVES, QT2_ROPE_PAIRS = 0, 1
 
 _DTYPE = {torch.bfloat16: QT2_DTYPE_BF16, torch.float32: QT2_DTYPE_F32}
 
@@ -74,6 +75,11 @@ def lib() -> ctypes.CDLL:
                 "qt2_gemm_nvfp4_gated": (i32, [pv, pv, pv, i64, i64, i64, f32, i32, vp, vp, i64, vp, i64, vp]),
                 "qt2_gemm_nvfp4_gated_bwd": (i32, [pv, pv, i64, i64, i64, f32, i32, vp, vp, i64, vp, vp, i64, vp, i64,
                                                    vp]),
+                "qt2_qk_norm_rope_fwd": (i32, [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64,
+                                               i64, i32, vp, i64, i64, vp]),
+                "qt2_qk_norm_rope_bwd_workspace_size": (i32, [i64, i64, i64, i64, psz]),
+                "qt2_qk_norm_rope_bwd": (i32, [vp, i64, i64, vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, i32, f32, vp,
+                                               vp, vp, i64, i64, i32, vp, i64, i64, vp, vp, vp, sz, vp]),
                 "qt2_grad_norm_workspace_size": (i32, [vp, i64, psz]),
                 "qt2_grad_norm": (i32, [vp, i64, vp, vp, sz, vp]),
                 "qt2_grad_clip": (i32, [vp, i64, vp, f32, vp]),
@@ -266,6 +272,48 @@ def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, a
     qg, qu, qdg, qdu, qh = _ptrs(fn, gate, up, dgate, dup, h)
     _check(fn, lib().qt2_gemm_nvfp4_gated_bwd(pa, pb, M, F, K, alpha, act, qg, qu, ldgu, qdg, qdu, lddgu, qh, ldh,
                                               _stream(stream)))
+
+
+def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx: int, hsx: int,
+                         wq: torch.Tensor | None, wk: torch.Tensor | None, eps: float, positions: torch.Tensor | None,
+                         cos: torch.Tensor | None, sin: torch.Tensor | None, P: int, R: int, pairing: int,
+                         y: torch.Tensor, ldy: int, hsy: int, stream=None) -> None:
+    """y = the Hq + Hk heads of x, each divided by its root mean square, times wq or wk, its first R elements
+    turned by row positions[t] of the tables cos and sin [P, R/2].  x and y of one type, wq and wk of one type."""
+    fn = "qt2_qk_norm_rope_fwd"
+    xd, wd = _dtype(fn, x, y), _dtype(fn, wq, wk)
+    _only(fn, torch.int64, positions)
+    _only(fn, torch.float32, cos, sin)
+    _vectors(fn, wq, wk, positions, cos, sin)
+    px, pq, pk, pp, pc, ps, py = _ptrs(fn, x, wq, wk, positions, cos, sin, y)
+    _check(fn, lib().qt2_qk_norm_rope_fwd(px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P, R, pairing, py,
+                                          ldy, hsy, _stream(stream)))
+
+
+def qt2_qk_norm_rope_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("qt2_qk_norm_rope_bwd_workspace_size",
+           lib().qt2_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D, ctypes.byref(n)))
+    return n.value
+
+
+def qt2_qk_norm_rope_bwd(dy: torch.Tensor, lddy: int, hsdy: int, x: torch.Tensor, T: int, Hq: int, Hk: int, D: int,
+                         ldx: int, hsx: int, wq: torch.Tensor | None, wk: torch.Tensor | None, eps: float,
+                         positions: torch.Tensor | None, cos: torch.Tensor | None, sin: torch.Tensor | None, P: int,
+                         R: int, pairing: int, dx: torch.Tensor | None, lddx: int, hsdx: int,
+                         dwq: torch.Tensor | None, dwk: torch.Tensor | None, workspace: torch.Tensor, ws_bytes: int,
+                         stream=None) -> None:
+    """dx, dwq and dwk (each may be None, not all) of qt2_qk_norm_rope_fwd; dy, x and dx of one type, wq, wk,
+    dwq and dwk of one type."""
+    fn = "qt2_qk_norm_rope_bwd"
+    xd, wd = _dtype(fn, dy, x, dx), _dtype(fn, wq, wk, dwq, dwk)
+    _only(fn, torch.int64, positions)
+    _only(fn, torch.float32, cos, sin)
+    _vectors(fn, wq, wk, positions, cos, sin, dwq, dwk, workspace)
+    pdy, px, pq, pk, pp, pc, ps, pdx, pdq, pdk, pws = _ptrs(fn, dy, x, wq, wk, positions, cos, sin, dx, dwq, dwk,
+                                                            workspace)
+    _check(fn, lib().qt2_qk_norm_rope_bwd(pdy, lddy, hsdy, px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P,
+                                          R, pairing, pdx, lddx, hsdx, pdq, pdk, pws, ws_bytes, _stream(stream)))
 
 
 class GradList:

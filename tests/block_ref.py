@@ -86,3 +86,63 @@ def gated_bwd(a, b, alpha, kind, gate, up):
     dg, du, h = dh * u * df, dh * f, f * u
     e_dg = e_dh * (u * df).abs() + (dh.abs() + e_dh) * u.abs() * e_df + 3 * U * dg.abs()
     return (dg, du, h), (e_dg, e_dh * f.abs() + (dh.abs() + e_dh) * e_f + 2 * U * du.abs(), e_f * u.abs() + 2 * U * h.abs())
+
+
+# ------------------------------------------------------------------------------------------ queries and keys
+def tables(P, R, base=1e4, device="cuda"):
+    """cos and sin [P, R/2] of p / base^(2 i / R), rounded to fp32 from 64 bits."""
+    i = torch.arange(R // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(P, dtype=torch.float64, device=device)[:, None] / base ** (2 * i / max(1, R))
+    return angle.cos().float(), angle.sin().float()
+
+
+def _pairs(R, pairs, device):
+    i = torch.arange(R // 2, device=device)
+    return (2 * i, 2 * i + 1) if pairs else (i, i + R // 2)
+
+
+def _turn(x, cos, sin, R, pairs, sign):
+    """x [T, H, D] with its pairs turned by cos, sin [T, R/2]; and |x|'s sum in each element."""
+    p, q = _pairs(R, pairs, x.device)
+    y, size = x.clone(), x.abs()
+    c, s = cos[:, None], sign * sin[:, None]
+    y[..., p], y[..., q] = x[..., p] * c - x[..., q] * s, x[..., q] * c + x[..., p] * s
+    size[..., p], size[..., q] = (x[..., p] * c).abs() + (x[..., q] * s).abs(), (x[..., q] * c).abs() + (x[..., p] * s).abs()
+    return y, size
+
+
+def _weights(wq, wk, Hq, Hk, D, device):
+    one = torch.ones(D, dtype=torch.float64, device=device)
+    return torch.cat([(one if w is None else w.double()).expand(n, D) for w, n in ((wq, Hq), (wk, Hk))])
+
+
+def qk_fwd(x, Hq, wq, wk, eps, cos, sin, R, pairs):
+    """y [T, H, D] in 64 bits and its bound, x [T, H, D] and cos, sin [T, R/2] of the tokens' positions.
+
+    Sum of squares: no term passes more than D/32 + 16 additions; rsqrt 4 u; two products and the turn's three
+    roundings."""
+    x = x.double()
+    T, H, D = x.shape
+    w = _weights(wq, wk, Hq, H - Hq, D, x.device)
+    r = 1 / torch.sqrt(x.square().mean(2, keepdim=True) + eps)
+    y, size = _turn(x * r * w, cos.double(), sin.double(), R, pairs, 1)
+    return y, size * (D / 64 + 8 + 4 + 2 + 3 + 1) * U
+
+
+def qk_bwd(dy, x, Hq, wq, wk, eps, cos, sin, R, pairs, row_depth):
+    """(dx, dwq, dwk) and bounds; row_depth: additions that any term of a sum over tokens and heads passes."""
+    x, dy = x.double(), dy.double()
+    T, H, D = x.shape
+    w = _weights(wq, wk, Hq, H - Hq, D, x.device)
+    r = 1 / torch.sqrt(x.square().mean(2, keepdim=True) + eps)
+    b, size = _turn(dy, cos.double(), sin.double(), R, pairs, -1)
+    n = x * r
+    mean = (b * w * n).mean(2, keepdim=True)
+    dx = r * (b * w - n * mean)
+    depth, e_r = D / 32 + 16, (D / 64 + 13) * U
+    e_mean = (size * w.abs() * n.abs()).mean(2, keepdim=True) * ((depth + 9) * U + e_r)
+    big = size * w.abs() + n.abs() * mean.abs()
+    e_dx = r * (size * w.abs() * 5 * U + n.abs() * e_mean + big * (e_r + 4 * U)) + dx.abs() * e_r
+    dw = b * n
+    e_dw = size * n.abs() * ((row_depth + 6) * U + e_r)
+    return ((dx, dw[:, :Hq].sum((0, 1)), dw[:, Hq:].sum((0, 1))), (e_dx, e_dw[:, :Hq].sum((0, 1)), e_dw[:, Hq:].sum((0, 1))))

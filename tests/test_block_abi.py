@@ -117,3 +117,84 @@ def test_gated_binding_refuses_before_the_call(monkeypatch):
         with pytest.raises(qt2.QT2Error) as e:
             case()
         assert e.value.status == DEV
+
+
+# ------------------------------------------------------------------------------------------ queries and keys
+QK = dict(x=0x1000, xd=0, T=5, Hq=3, Hk=1, D=16, ldx=80, hsx=16, wq=0x2000, wk=0x3000, wd=1, eps=1e-6, pos=0x4000, cos=0x5000, sin=0x6000, P=9,
+          R=16, pairing=0)
+
+
+def qk_fwd(L, y=0x7000, ldy=64, hsy=16, **kw):
+    return L.qt2_qk_norm_rope_fwd(*dict(QK, **kw).values(), y, ldy, hsy, None)
+
+
+def qk_bwd(L, dy=0x8000, lddy=64, hsdy=16, dx=0x9000, lddx=80, hsdx=16, dwq=0xa000, dwk=0xb000, ws=0x10000, n=1 << 20, **kw):
+    return L.qt2_qk_norm_rope_bwd(dy, lddy, hsdy, *dict(QK, **kw).values(), dx, lddx, hsdx, dwq, dwk, ws, n, None)
+
+
+QK_BAD = [(dict(x=None), ARG), (dict(xd=2), ARG), (dict(wd=9), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG),
+          (dict(pairing=2), ARG), (dict(cos=None), ARG), (dict(sin=None), ARG), (dict(T=0), SHAPE), (dict(T=1 << 30), SHAPE), (dict(Hq=-1), SHAPE),
+          (dict(Hq=0, Hk=0), SHAPE), (dict(Hk=1 << 20), SHAPE), (dict(T=1 << 20, Hq=1 << 13), SHAPE), (dict(D=0), SHAPE), (dict(D=12), SHAPE),
+          (dict(D=1032), SHAPE), (dict(R=24), SHAPE), (dict(R=4), SHAPE), (dict(R=-8), SHAPE), (dict(P=0), SHAPE), (dict(P=1 << 30), SHAPE),
+          (dict(pos=None, P=4), SHAPE), (dict(ldx=56), SHAPE), (dict(hsx=8), SHAPE), (dict(ldx=-80), SHAPE), (dict(ldx=1 << 40), SHAPE),
+          (dict(ldx=16, hsx=72), SHAPE), (dict(x=0x1008), ALIGN), (dict(ldx=84), ALIGN), (dict(hsx=17), ALIGN), (dict(wq=0x2008), ALIGN),
+          (dict(wk=0x3004), ALIGN), (dict(pos=0x4004), ALIGN), (dict(cos=0x5008), ALIGN), (dict(sin=0x6004), ALIGN)]
+
+
+@pytest.mark.parametrize("bad,status", QK_BAD + [(dict(y=None), ARG), (dict(ldy=48), SHAPE), (dict(hsy=0), SHAPE), (dict(ldy=68), ALIGN), (dict(y=0x7008), ALIGN)])
+def test_qk_fwd_refusals(L, bad, status):
+    assert qk_fwd(L, **bad) == status
+
+
+@pytest.mark.parametrize("bad,status", QK_BAD + [
+    (dict(dy=None), ARG), (dict(dx=None, dwq=None, dwk=None), ARG), (dict(lddy=48), SHAPE), (dict(hsdx=8), SHAPE), (dict(lddx=84), ALIGN),
+    (dict(dy=0x8004), ALIGN), (dict(dx=0x9008), ALIGN), (dict(dwq=0xa008), ALIGN), (dict(dwk=0xb002), ALIGN), (dict(ws=None), WS), (dict(n=64), WS),
+    (dict(ws=0x10080), ALIGN)])
+def test_qk_bwd_refusals(L, bad, status):
+    assert qk_bwd(L, **bad) == status
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(R=0, pos=None, cos=None, sin=None, P=0), dict(pos=None), dict(Hq=0), dict(Hk=0), dict(T=1, ldx=0),
+                                dict(ldx=16, hsx=80), dict(wq=None, wk=None, xd=1, wd=0), dict(D=512, R=8, ldx=2048, hsx=512)])
+def test_qk_calls_that_are_right(L, kw):
+    """Either layout, nothing turned, heads of one kind; a call may give no leading dimension where there is one row."""
+    wide = dict(ldy=4096, hsy=1024) if kw.get("D") else {}
+    assert injected(lambda: qk_fwd(L, **wide, **kw)).count("launch") == 1
+    wide = dict(lddy=4096, hsdy=1024, lddx=4096, hsdx=1024) if kw.get("D") else {}
+    assert injected(lambda: qk_bwd(L, **wide, **kw)).count("launch") == 2
+    assert injected(lambda: qk_bwd(L, dwq=None, dwk=None, **wide, **kw)).count("launch") == 1
+
+
+def test_qk_workspace(L):
+    n = ctypes.c_size_t(0)
+    assert L.qt2_qk_norm_rope_bwd_workspace_size(4, 2, 1, 64, None) == ARG
+    for dims in ((0, 1, 1, 64), (4, 0, 0, 64), (4, 1, 1, 60), (4, 1, 1, 2048), (4, -1, 3, 64)):
+        assert L.qt2_qk_norm_rope_bwd_workspace_size(*dims, ctypes.byref(n)) == SHAPE
+    assert tr.qt2_qk_norm_rope_bwd_workspace_size(1 << 20, 32, 8, 128) < 1 << 20
+
+
+def test_qk_binding_refuses_before_the_call(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x, w, t, pos, ws = torch.zeros(4, 64), torch.zeros(16), torch.zeros(9, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(1 << 16, dtype=torch.uint8)
+    vectors = dict(wq=w, wk=w, pos=pos, cos=t, sin=t)
+
+    def fwd(x=x, y=x, **kw):
+        v = dict(vectors, **kw)
+        tr.qt2_qk_norm_rope_fwd(x, 4, 3, 1, 16, 64, 16, v["wq"], v["wk"], 1e-6, v["pos"], v["cos"], v["sin"], 9, 16, 0, y, 64, 16)
+
+    def bwd(x=x, dy=x, dx=x, dwq=w, dwk=w, ws=ws, **kw):
+        v = dict(vectors, **kw)
+        tr.qt2_qk_norm_rope_bwd(dy, 64, 16, x, 4, 3, 1, 16, 64, 16, v["wq"], v["wk"], 1e-6, v["pos"], v["cos"], v["sin"], 9, 16, 0, dx, 64, 16, dwq,
+                                dwk, ws, 1 << 16)
+    half = torch.zeros(4, 64, dtype=torch.float16)
+    bad = [lambda f: f(x=half), lambda f: f(x=x.bfloat16()), lambda f: f(wq=w.bfloat16()), lambda f: f(pos=pos.int()), lambda f: f(cos=t.double()),
+           lambda f: f(pos=torch.zeros(8, dtype=torch.int64)[::2]), lambda f: f(sin=torch.zeros(8, 9).t()), lambda f: f(wk=w[:1].expand(16))]
+    extra = [lambda f: f(dx=half), lambda f: f(dwq=w.bfloat16()), lambda f: f(dwk=torch.zeros(32)[::2]), lambda f: f(ws=ws[::2])]
+    for f, cases in ((fwd, bad + [lambda f: f(y=half)]), (bwd, bad + extra)):
+        for k, case in enumerate(cases):
+            with pytest.raises(qt2.QT2Error) as e:
+                case(f)
+            assert e.value.status == ARG, k
+        with pytest.raises(qt2.QT2Error) as e:
+            f()
+        assert e.value.status == DEV
