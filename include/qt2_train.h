@@ -2,8 +2,8 @@
  * qt2_train.h -- C ABI of the training operators beside the quantized linears (qt2.h) for NVIDIA
  * B200 (sm_100a), in the library libqt2_train.so: layer norm, the head's softmax cross entropy
  * over a large vocabulary, the gated feed-forward product on NVFP4 operands, the norm of queries and
- * keys with the position rotation, and the global gradient norm with clipping, each with what a training
- * step needs of it.
+ * keys with the position rotation, the global gradient norm with clipping, and the AdamW step of many
+ * tensors, each with what a training step needs of it.
  *
  * Conventions are those of qt2.h (device pointers owned by the caller, work enqueued on `stream`,
  * arguments validated on the host before any launch, negative qt2_status on error, no allocation,
@@ -32,8 +32,8 @@ extern "C" {
 #endif
 
 /* qt2_device_status, qt2_set_fault_hook and qt2_build_checked of this library.  Its kernels
- * report QT2_ERR_TIMEOUT, QT2_ERR_INVALID_ARG (a target outside the vocabulary), and in the
- * checked build QT2_ERR_BOUNDS. */
+ * report QT2_ERR_TIMEOUT, QT2_ERR_INVALID_ARG (a target outside the vocabulary, a position outside the
+ * tables, a step below 1), and in the checked build QT2_ERR_BOUNDS. */
 QT2_API qt2_status qt2_train_device_status(qt2_stream_t stream, int *code);
 QT2_API void qt2_train_set_fault_hook(qt2_fault_hook hook, void *user);
 QT2_API int qt2_train_build_checked(void);
@@ -208,6 +208,49 @@ QT2_API qt2_status qt2_grad_norm(const qt2_grad *grads, int64_t count, float *no
                                  qt2_stream_t stream);
 QT2_API qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm, float max_norm,
                                  qt2_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * One AdamW step (decoupled weight decay) of many tensors, in place, the clipping by the global norm taken
+ * along.  With f = min(1, max_norm / (*norm + 1e-6)), or 1 where norm is NULL, and t = *step:
+ *   g' = g f,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * A tensor is numel (>= 0, below 2^40) contiguous elements.  param is bf16 or fp32.  With a master (fp32, for a bf16 param
+ * alone; else NULL) p is read from and kept in the master, and param receives it rounded; without one a bf16
+ * param is read, and written rounded to nearest.  grad is bf16 or fp32.  States:
+ *   QT2_STATE_F32   m and v are fp32; the scales are not used.
+ *   QT2_STATE_E4M3  m and v are E4M3 codes, with an fp32 scale for every 256 elements in m_scale and v_scale
+ *     [ceil(numel / 256)]: m = code * scale, and sqrt(v) = code * scale (the codes hold the root).  The new
+ *     scale is the largest magnitude / 448 (in the step's own update m and v are not rounded); a code is
+ *     one of the two neighbours of its value, picked by 16 random bits r so that the mean stays: the fp32
+ *     encoding of |value| * (448 / largest) plus r * 2^4, cut to 3 bits of mantissa (below 2^-6 with 2^-6 added
+ *     before and taken off after).  Element i draws from word i % 4 of the Philox4x32-10 block of counter
+ *     (lo32(i / 4), hi32(i / 4), the tensor's place in the list, lo32(*step)) under the key seed: its low 16 bits
+ *     for m, the others for v.  Blocks whose largest magnitude is below 2^-100 become zeros with scale 0; an inf
+ *     or NaN makes its block of 256 NaN.  Zeros with scales of zero are a fresh state.
+ * Codes, scales and v are rounded operation by operation in the order above (fp32, no contraction).
+ * lr (fp32), step (int64, 1 for the first step) and norm (fp32, what qt2_grad_norm gives) are one element each
+ * in device memory, so that a captured graph can be replayed as they change.  A step below 1 is reported as
+ * QT2_ERR_INVALID_ARG through qt2_train_device_status; then, and where the norm is inf or NaN, nothing changes.
+ * 0 <= beta1, beta2 < 1, eps >= 0, max_norm >= 0, weight_decay finite.  The list is read on the host during
+ * the call.  Arrays are aligned to their elements only; those of a tensor go fastest when they start on 16
+ * bytes, or equally far (in elements) behind.  Nothing that the step writes may overlap another tensor's
+ * arrays or the gradients.
+ * --------------------------------------------------------------------------------------- */
+enum { QT2_STATE_F32 = 0, QT2_STATE_E4M3 = 1 };
+typedef struct {
+    void *param;       /* device */
+    float *master;     /* device, or NULL */
+    const void *grad;  /* device */
+    void *m, *v;       /* device */
+    float *m_scale, *v_scale; /* device; QT2_STATE_E4M3 */
+    int64_t numel;
+    int32_t param_dtype, grad_dtype; /* QT2_DTYPE_* */
+    int32_t state;                   /* QT2_STATE_* */
+    float weight_decay;
+} qt2_adamw_tensor;
+QT2_API qt2_status qt2_adamw(const qt2_adamw_tensor *tensors, int64_t count, const float *lr, const int64_t *step,
+                             double beta1, double beta2, float eps, const float *norm, float max_norm, uint64_t seed,
+                             qt2_stream_t stream);
 
 #ifdef __cplusplus
 }

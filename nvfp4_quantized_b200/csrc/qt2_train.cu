@@ -1,6 +1,6 @@
 // qt2_train.cu -- the training operators' library: kernel launchers and the C ABI declared in
 // include/qt2_train.h (layer norm, the head's softmax cross entropy, the gated feed-forward product,
-// the norm of queries and keys with the rotation, gradient norm and clipping).
+// the norm of queries and keys with the rotation, gradient norm and clipping, AdamW).
 //
 // One translation unit, with a device status word, fault hook and caches of its own.  Built for
 // sm_100a only into libqt2_train.so.
@@ -15,6 +15,7 @@
 #include "xent_kernels.cuh"
 #include "gated_kernels.cuh"
 #include "rope_kernels.cuh"
+#include "adamw_kernels.cuh"
 
 using namespace qt2;
 
@@ -644,6 +645,92 @@ cudaError_t grad_clip(const qt2_grad *grads, int64_t count, const float *norm, f
     return cudaSuccess;
 }
 
+// ------------------------------------------------------------------------------- AdamW
+qt2_status adamw_check(const qt2_adamw_tensor *t, int64_t count) {
+    if (!t) return QT2_ERR_INVALID_ARG;
+    if (count <= 0 || count > (int64_t(1) << 30)) return QT2_ERR_SHAPE;
+    for (int64_t i = 0; i < count; ++i) {
+        const qt2_adamw_tensor &a = t[i];
+        const bool e4m3 = a.state == QT2_STATE_E4M3;
+        if (!dtype_ok(a.param_dtype) || !dtype_ok(a.grad_dtype) || (a.state != QT2_STATE_F32 && !e4m3) ||
+            !std::isfinite(a.weight_decay) || (a.master && a.param_dtype == QT2_DTYPE_F32))
+            return QT2_ERR_INVALID_ARG;
+        if (a.numel < 0 || a.numel >= (int64_t(1) << 40)) return QT2_ERR_SHAPE;
+        if (a.numel == 0) continue;
+        if (!a.param || !a.grad || !a.m || !a.v || (e4m3 && (!a.m_scale || !a.v_scale))) return QT2_ERR_INVALID_ARG;
+        const uintptr_t p = a.param_dtype == QT2_DTYPE_F32 ? 4 : 2, g = a.grad_dtype == QT2_DTYPE_F32 ? 4 : 2;
+        const uintptr_t s = e4m3 ? 1 : 4;
+        if (!aligned(a.param, p) || !aligned(a.grad, g) || !aligned(a.m, s) || !aligned(a.v, s) || !aligned(a.master, 4) ||
+            (e4m3 && (!aligned(a.m_scale, 4) || !aligned(a.v_scale, 4))))
+            return QT2_ERR_ALIGN;
+    }
+    return QT2_OK;
+}
+
+// Elements by which a tensor's arrays all start behind a multiple of four; -1 where they differ, or where
+// blocks of 256, which count from the first element, would not be made of whole vectors.
+int adamw_head(const qt2_adamw_tensor &a) {
+    auto behind = [](const void *p, int size) { return (int)(reinterpret_cast<uintptr_t>(p) / size & 3); };
+    const bool e4m3 = a.state == QT2_STATE_E4M3;
+    const int s = e4m3 ? 1 : 4, head = behind(a.grad, a.grad_dtype == QT2_DTYPE_F32 ? 4 : 2);
+    const bool same = behind(a.param, a.param_dtype == QT2_DTYPE_F32 ? 4 : 2) == head && behind(a.m, s) == head &&
+                      behind(a.v, s) == head && (!a.master || behind(a.master, 4) == head);
+    return same && (!e4m3 || head == 0) ? head : -1;
+}
+
+// The next launch's tensors, from tensors[at] on; returns the next `at`.
+template <int N>
+int64_t adamw_table(AdamTable<N> &t, const qt2_adamw_tensor *tensors, int64_t at, int64_t count) {
+    t.count = 0;
+    t.first[0] = 0;
+    for (; at < count && t.count < N; ++at) {
+        const qt2_adamw_tensor &a = tensors[at];
+        if (a.numel == 0) continue;
+        const int k = t.count, head = adamw_head(a);
+        const int64_t next = t.first[k] + ceil_div(std::max(0, head) + a.numel, kAdamChunk);
+        if (next > INT32_MAX / 2) break;   // a launch's chunks, and the blocks' next ones
+        ++t.count;
+        t.param[k] = a.param;
+        t.master[k] = a.master;
+        t.grad[k] = a.grad;
+        t.m[k] = a.m;
+        t.v[k] = a.v;
+        t.m_scale[k] = a.m_scale;
+        t.v_scale[k] = a.v_scale;
+        t.numel[k] = a.numel;
+        t.first[k + 1] = (int32_t)next;
+        t.id[k] = (int32_t)at;
+        t.decay[k] = a.weight_decay;
+        t.flags[k] = (uint8_t)((a.param_dtype == QT2_DTYPE_F32 ? kAdamParamF32 : 0) |
+                               (a.grad_dtype == QT2_DTYPE_F32 ? kAdamGradF32 : 0) |
+                               (a.state == QT2_STATE_E4M3 ? kAdamE4m3 : 0) | (head >= 0 ? kAdamVectors : 0) |
+                               std::max(0, head) * kAdamHead);
+    }
+    return at;
+}
+
+template <int N>
+cudaError_t launch_adamw(const AdamTable<N> &t, const AdamArgs &a, cudaStream_t s) {
+    QT2_LAUNCH_SITE();
+    static PerDeviceOnce once;
+    static std::atomic<int> blocks[kMaxDevices];
+    int64_t n = 0;
+    const cudaError_t e = resident_blocks(once, blocks, adamw_kernel<N>, kAdamThreads, 0, &n);
+    if (e != cudaSuccess) return e;
+    return launch(adamw_kernel<N>, (unsigned)std::min<int64_t>(n, t.first[t.count]), kAdamThreads, 0, s, t, a);
+}
+template <int N>
+cudaError_t adamw(const qt2_adamw_tensor *tensors, int64_t count, const AdamArgs &a, cudaStream_t s) {
+    AdamTable<N> t;
+    for (int64_t at = 0; at < count;) {
+        at = adamw_table(t, tensors, at, count);
+        if (t.count == 0) break;
+        const cudaError_t e = launch_adamw(t, a, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1054,6 +1141,33 @@ qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const float *norm
     return from_cuda(count <= kGradSmall    ? grad_clip<kGradSmall>(grads, count, norm, max_norm, s)
                      : count <= kGradMiddle ? grad_clip<kGradMiddle>(grads, count, norm, max_norm, s)
                                             : grad_clip<kGradLarge>(grads, count, norm, max_norm, s));
+}
+
+qt2_status qt2_adamw(const qt2_adamw_tensor *tensors, int64_t count, const float *lr, const int64_t *step, double beta1,
+                     double beta2, float eps, const float *norm, float max_norm, uint64_t seed, qt2_stream_t stream) {
+    QT2_TRACE();
+    if (!lr || !step || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0f) ||
+        std::isinf(eps) || (norm && !(max_norm >= 0.0f)))
+        return QT2_ERR_INVALID_ARG;
+    if (const qt2_status st = adamw_check(tensors, count)) return st;
+    if (!aligned(lr, 4) || !aligned(step, 8) || !aligned(norm, 4)) return QT2_ERR_ALIGN;
+    if (const qt2_status st = check_device()) return st;
+    AdamArgs a{};
+    a.lr = lr;
+    a.norm = norm;
+    a.step = step;
+    a.log_b1 = std::log(beta1);
+    a.log_b2 = std::log(beta2);
+    a.b1 = (float)beta1;
+    a.b2 = (float)beta2;
+    a.one_b1 = (float)(1.0 - beta1);
+    a.one_b2 = (float)(1.0 - beta2);
+    a.eps = eps;
+    a.max_norm = max_norm;
+    a.seed = seed;
+    const cudaStream_t s = as_stream(stream);
+    return from_cuda(count <= kAdamSmall ? adamw<kAdamSmall>(tensors, count, a, s)
+                                         : adamw<kAdamLarge>(tensors, count, a, s));
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 """Thin ctypes binding of the training operators' C ABI (include/qt2_train.h): layer norm, the
 head's softmax cross entropy, the gated feed-forward product on NVFP4 operands, the norm of queries and
-keys with the position rotation and the global gradient norm with clipping, in ``libqt2_train.so``.
+keys with the position rotation, the global gradient norm with clipping and the AdamW step of many
+tensors, in ``libqt2_train.so``.
 
 Argument marshalling only, in the manner of ``qt2``: every function forwards to the entry point of
 the same name with the tensors' device pointers and the current CUDA stream (or ``stream``), and
@@ -33,6 +34,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qt2_train.h")
 
 QT2_ACT_SILU, QT2_ACT_GELU_TANH = 0, 1
 QT2_ROPE_HALVES, QT2_ROPE_PAIRS = 0, 1
+QT2_STATE_F32, QT2_STATE_E4M3 = 0, 1
 
 _DTYPE = {torch.bfloat16: QT2_DTYPE_BF16, torch.float32: QT2_DTYPE_F32}
 
@@ -40,6 +42,12 @@ _DTYPE = {torch.bfloat16: QT2_DTYPE_BF16, torch.float32: QT2_DTYPE_F32}
 class GradC(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWTensorC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -83,6 +91,7 @@ def lib() -> ctypes.CDLL:
                 "qt2_grad_norm_workspace_size": (i32, [vp, i64, psz]),
                 "qt2_grad_norm": (i32, [vp, i64, vp, vp, sz, vp]),
                 "qt2_grad_clip": (i32, [vp, i64, vp, f32, vp]),
+                "qt2_adamw": (i32, [vp, i64, vp, vp, ctypes.c_double, ctypes.c_double, f32, vp, f32, ctypes.c_uint64, vp]),
             }
             for name, (res, args) in sigs.items():
                 fn = getattr(L, name)
@@ -382,6 +391,76 @@ def qt2_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, stream=N
     if grads.count and grads.device != norm.get_device():
         raise QT2Error(fn, QT2_ERR_DEVICE)
     _check(fn, lib().qt2_grad_clip(grads.address, grads.count, pn, max_norm, _stream(stream)))
+
+
+class AdamWList:
+    """The list that qt2_adamw takes: parameters (bf16 or fp32), their gradients (bf16 or fp32) and states m and v,
+    contiguous tensors on one device.  States are fp32, or torch.float8_e4m3fn with fp32 scales of one element for
+    256 in m_scales and v_scales.  masters: an fp32 tensor for each bf16 parameter, or None (no masters), in the
+    whole list's place or an entry's.  weight_decay: one number, or one for each.  Made once for buffers that stay
+    where they are; it keeps the tensors alive."""
+
+    def __init__(self, params, grads, m, v, masters=None, m_scales=None, v_scales=None, weight_decay=0.0):
+        fn = "AdamWList"
+        self.params, self.grads, self.m, self.v = (list(t) for t in (params, grads, m, v))
+        self.count = n = len(self.params)
+        self.masters, self.m_scales, self.v_scales = ([None] * n if t is None else list(t)
+                                                      for t in (masters, m_scales, v_scales))
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(w) for w in weight_decay]
+        columns = (self.params, self.masters, self.grads, self.m, self.v, self.m_scales, self.v_scales)
+        if any(len(c) != n for c in columns) or len(decay) != n:
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        self.c = (AdamWTensorC * max(1, n))()
+        devices, written, read = set(), [], []
+        for row, w, *tensors in zip(self.c, decay, *columns):
+            p, master, g, m1, v1, ms, vs = tensors
+            eight = m1.dtype is torch.float8_e4m3fn
+            if (p.dtype not in _DTYPE or g.dtype not in _DTYPE or not (eight or m1.dtype is torch.float32)
+                    or v1.dtype is not m1.dtype or (master is not None and p.dtype is torch.float32)):
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            if eight == (ms is None) or eight == (vs is None):
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            _only(fn, torch.float32, master, ms, vs)
+            _vectors(fn, *tensors)
+            size = p.numel()
+            if any(t is not None and t.numel() != size for t in (master, g, m1, v1)) or any(
+                    t is not None and t.numel() != (size + 255) // 256 for t in (ms, vs)):
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            devices.update(t.get_device() for t in tensors if t is not None)
+            at = [None if t is None else t.data_ptr() for t in tensors]
+            row.param, row.master, row.grad, row.m, row.v, row.m_scale, row.v_scale = at
+            row.numel, row.param_dtype, row.grad_dtype, row.state, row.weight_decay = size, _DTYPE[p.dtype], _DTYPE[g.dtype], eight, w
+            for k, t in enumerate(tensors):
+                if t is not None and size:
+                    (read if k == 2 else written).append((at[k], at[k] + t.numel() * t.element_size(), k != 2))
+        if len(devices) > 1:
+            raise QT2Error(fn, QT2_ERR_DEVICE)
+        self.device = devices.pop() if devices else -1
+        # what is written overlaps nothing else
+        end, end_written = 0, 0
+        for lo, hi, writes in sorted(written + read):
+            if lo < end_written or (writes and lo < end):
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            end = max(end, hi)
+            end_written = hi if writes else end_written
+        self.address = ctypes.addressof(self.c)
+
+
+def qt2_adamw(tensors: AdamWList, lr: torch.Tensor, step: torch.Tensor, beta1: float, beta2: float, eps: float,
+              norm: torch.Tensor | None, max_norm: float, seed: int, stream=None) -> None:
+    """One AdamW step of the list's tensors in place, gradients times min(1, max_norm / (norm + 1e-6)) (norm None:
+    as they are).  lr (fp32), step (int64, from 1) and norm (fp32) are one element each on the device; seed draws
+    the roundings of 8-bit states."""
+    fn = "qt2_adamw"
+    _only(fn, torch.float32, lr, norm)
+    _only(fn, torch.int64, step)
+    if any(t is not None and t.numel() != 1 for t in (lr, step, norm)):
+        raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+    pl, ps, pn = _ptrs(fn, lr, step, norm)
+    if tensors.count and tensors.device != lr.get_device():
+        raise QT2Error(fn, QT2_ERR_DEVICE)
+    _check(fn, lib().qt2_adamw(tensors.address, tensors.count, pl, ps, beta1, beta2, eps, pn, max_norm, seed,
+                               _stream(stream)))
 
 
 class fault_hook(qt2.fault_hook):

@@ -146,3 +146,47 @@ def qk_bwd(dy, x, Hq, wq, wk, eps, cos, sin, R, pairs, row_depth):
     dw = b * n
     e_dw = size * n.abs() * ((row_depth + 6) * U + e_r)
     return ((dx, dw[:, :Hq].sum((0, 1)), dw[:, Hq:].sum((0, 1))), (e_dx, e_dw[:, :Hq].sum((0, 1)), e_dw[:, Hq:].sum((0, 1))))
+
+
+# ------------------------------------------------------------------------------------------ AdamW
+def adamw(p, g, m, v, lr, step, b1, b2, eps, decay, clip):
+    """(p, m, v) after a step in 64 bits, and bounds.  m, v: what the states stand for; clip: the factor (64 bits).
+
+    The factor is off by 3 u; m and v have a product's rounding on either side and the sum's; the update's
+    quotient: root, correction, sum, rate, product and a division of 2 units."""
+    p, g, m, v = (t.double() for t in (p, g, m, v))
+    h = g * clip
+    e_h = 4 * U * h.abs()
+    m1, v1 = b1 * m + (1 - b1) * h, b2 * v + (1 - b2) * h * h
+    # b and 1 - b rounded to fp32, the products, the sum
+    e_m = 3 * U * (b1 * m).abs() + (1 - b1) * (e_h + 2 * U * h.abs()) + U * m1.abs()
+    e_v = 3 * U * b2 * v + (1 - b2) * (2 * e_h * h.abs() + 3 * U * h * h) + U * v1 + 2.0 ** -148
+    c1, c2 = 1 / (1 - b1 ** step), math.sqrt(1 / (1 - b2 ** step))
+    root = v1.sqrt()
+    # the root's own relative error: half of v's, or where v is nearly nothing what it may be at most
+    e_root = torch.minimum(e_v / root.clamp(min=1e-300), e_v.sqrt()) + U * root
+    den = root * c2 + eps
+    up = lr * c1 * m1 / den
+    e_up = lr * c1 * e_m / den + up.abs() * (c2 * e_root / den * 1.5 + 8 * U)
+    p1 = p - lr * decay * p - up
+    return (p1, m1, v1), (3 * U * (lr * decay * p).abs() + U * p.abs() + U * p1.abs() + e_up * 1.001, e_m, e_v)
+
+
+def philox(counter, seed):
+    """Words [n, 4] of Philox4x32-10 at counters [n, 4] (numpy, as published)."""
+    import numpy as np
+    c = [np.asarray(counter[:, i], dtype=np.uint64) for i in range(4)]
+    k = [np.uint64(seed & 0xFFFFFFFF), np.uint64(seed >> 32 & 0xFFFFFFFF)]
+    low = np.uint64(0xFFFFFFFF)
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> np.uint64(32)) ^ c[1] ^ k[0], b & low, (a >> np.uint64(32)) ^ c[3] ^ k[1], a & low]
+        k = [(k[0] + np.uint64(0x9E3779B9)) & low, (k[1] + np.uint64(0xBB67AE85)) & low]
+    return np.stack(c, 1)
+
+
+def e4m3_neighbours(x):
+    """The E4M3 numbers at or next below and next above |x| <= 448 (64 bits)."""
+    grid = torch.arange(127, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn).double()
+    i = torch.searchsorted(grid, x.abs().contiguous(), right=True) - 1
+    return grid[i], grid[(i + 1).clamp(max=126)]

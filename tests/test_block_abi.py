@@ -198,3 +198,89 @@ def test_qk_binding_refuses_before_the_call(monkeypatch):
         with pytest.raises(qt2.QT2Error) as e:
             f()
         assert e.value.status == DEV
+
+
+# ------------------------------------------------------------------------------------------ AdamW
+ROW = dict(param=0x1000, master=None, grad=0x2000, m=0x3000, v=0x4000, m_scale=None, v_scale=None, numel=5, param_dtype=1, grad_dtype=1, state=0,
+           weight_decay=0.0)
+EIGHT = dict(m_scale=0x5000, v_scale=0x6000, state=1)
+
+
+def rows(*changes):
+    a = (tr.AdamWTensorC * max(1, len(changes)))()
+    for c, change in zip(a, changes):
+        for k, v in dict(ROW, **change).items():
+            setattr(c, k, v)
+    return a
+
+
+def adamw(L, *changes, count=None, lr=0x7000, step=0x8000, b1=0.9, b2=0.99, eps=1e-8, norm=0x9000, max_norm=1.0):
+    a = rows(*(changes or ({},)))
+    return L.qt2_adamw(ctypes.addressof(a), len(changes or (1,)) if count is None else count, lr, step, b1, b2, eps, norm, max_norm, 7, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(param=None), ARG), (dict(grad=None), ARG), (dict(m=None), ARG), (dict(v=None), ARG), (dict(param_dtype=2), ARG), (dict(grad_dtype=-1), ARG),
+    (dict(state=2), ARG), (dict(state=1), ARG), (dict(EIGHT, v_scale=None), ARG), (dict(weight_decay=float("nan")), ARG), (dict(weight_decay=float("inf")), ARG),
+    (dict(master=0x5000), ARG), (dict(numel=-1), SHAPE), (dict(numel=1 << 40), SHAPE), (dict(param=0x1002), ALIGN), (dict(grad=0x2002), ALIGN),
+    (dict(m=0x3002), ALIGN), (dict(v=0x4001), ALIGN), (dict(param_dtype=0, param=0x1001), ALIGN), (dict(param_dtype=0, master=0x5002), ALIGN),
+    (dict(EIGHT, m_scale=0x5002), ALIGN), (dict(EIGHT, v_scale=0x6001), ALIGN)])
+def test_adamw_tensor_refusals(L, bad, status):
+    assert adamw(L, {}, bad) == status
+    if status != SHAPE and bad.get("state", 0) != 2 and "dtype" not in str(bad) and "decay" not in str(bad) and "master" not in bad:
+        with tr.fault_hook(lambda site: qt2.FAULT_SKIP):   # of an empty tensor nothing is read
+            assert adamw(L, {}, dict(bad, numel=0)) == OK
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(lr=None), ARG), (dict(step=None), ARG), (dict(b1=1.0), ARG), (dict(b1=-0.1), ARG), (dict(b2=1.0), ARG), (dict(b2=float("nan")), ARG),
+    (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG), (dict(max_norm=-1.0), ARG), (dict(max_norm=float("nan")), ARG),
+    (dict(count=0), SHAPE), (dict(count=-3), SHAPE), (dict(lr=0x7002), ALIGN), (dict(step=0x8004), ALIGN), (dict(norm=0x9001), ALIGN)])
+def test_adamw_refusals(L, bad, status):
+    assert adamw(L, **bad) == status
+
+
+def test_adamw_calls_that_are_right(L):
+    assert L.qt2_adamw(None, 1, 0x7000, 0x8000, 0.9, 0.99, 1e-8, None, 1.0, 7, None) == ARG
+    for changes, kw, launches in (([{}], {}, 1), ([dict(EIGHT, m=0x3001, v=0x4003)], {}, 1), ([{}], dict(norm=None, max_norm=-1.0), 1),
+                                  ([dict(numel=0, param=None, grad=None, m=None, v=None)], {}, 0), ([dict(param_dtype=0, master=0xa000)] * 33, {}, 1),
+                                  ([{}, dict(numel=0)] * 400, {}, 2), ([dict(numel=(1 << 40) - 1)] * 3, {}, 3), ([{}], dict(b1=0.0, b2=0.0), 1)):
+        if launches:
+            assert injected(lambda: adamw(L, *changes, **kw)).count("launch") == launches
+        else:
+            with tr.fault_hook(lambda site: qt2.FAULT_SKIP) as h:
+                assert adamw(L, *changes, **kw) == OK
+            assert "launch" not in h.sites
+
+
+def test_adamw_list_refuses(monkeypatch):
+    f, g, m, v = (torch.zeros(300) for _ in range(4))
+    b, half = torch.zeros(300, dtype=torch.bfloat16), torch.zeros(300, dtype=torch.float16)
+    e, e2, s, s2 = torch.zeros(300, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros(300, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros(2), torch.zeros(2)
+    long = torch.zeros(1200)
+    cases = [
+        lambda: tr.AdamWList([half], [g], [m], [v]), lambda: tr.AdamWList([f], [half], [m], [v]), lambda: tr.AdamWList([f], [g], [b], [v]),
+        lambda: tr.AdamWList([f], [g], [m], [e]), lambda: tr.AdamWList([f], [g], [e], [e2]), lambda: tr.AdamWList([f], [g], [e], [e2], None, [s], None),
+        lambda: tr.AdamWList([f], [g], [m], [v], None, [s], [s2]), lambda: tr.AdamWList([f], [g], [m], [v], [long[:300]]),
+        lambda: tr.AdamWList([b], [g], [m], [v], [b]), lambda: tr.AdamWList([f], [g[:299]], [m], [v]), lambda: tr.AdamWList([f], [g], [e], [e2], None, [s[:1]], [s2]),
+        lambda: tr.AdamWList([f], [g], [m], [v, v]), lambda: tr.AdamWList([f], [g], [m], [v], weight_decay=[0.1, 0.1]),
+        lambda: tr.AdamWList([torch.zeros(20, 15).t()], [g], [m], [v]), lambda: tr.AdamWList([f], [g[:1].expand(300)], [m], [v]),
+        # what the step writes, and another array
+        lambda: tr.AdamWList([f], [f], [m], [v]), lambda: tr.AdamWList([f], [g], [m], [m]), lambda: tr.AdamWList([f], [g], [f], [v]),
+        lambda: tr.AdamWList([long[:300]], [long[299:599]], [m], [v]), lambda: tr.AdamWList([f, long[:300]], [g, g], [m, long[200:500]], [v, torch.zeros(300)]),
+        lambda: tr.AdamWList([f], [g], [e], [e2], None, [s], [s])]
+    for k, case in enumerate(cases):
+        with pytest.raises(qt2.QT2Error) as err:
+            case()
+        assert err.value.status == ARG, k
+    tr.AdamWList([f, torch.zeros(300)], [g, g], [m, torch.zeros(300)], [v, torch.zeros(300)], weight_decay=[0.0, 0.1])   # a gradient of two
+    ok = tr.AdamWList([b, f], [g, g], [e, m], [e2, v], [long[:300], None], [s, None], [s2, None], 0.1)
+    tr.AdamWList([long[:300]], [long[300:600]], [long[600:900]], [long[900:]])
+    assert tr.AdamWList([], [], [], []).count == 0
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    one, step = torch.zeros(1), torch.ones(1, dtype=torch.int64)
+    for args, status in (((one, step, None), DEV), ((one.double(), step, None), ARG), ((one, step.int(), None), ARG), ((one, step, one.bfloat16()), ARG),
+                         ((f, step, None), ARG), ((one, step, s), ARG)):
+        with pytest.raises(qt2.QT2Error) as err:
+            tr.qt2_adamw(ok, args[0], args[1], 0.9, 0.99, 1e-8, args[2], 1.0, 7)
+        assert err.value.status == status
