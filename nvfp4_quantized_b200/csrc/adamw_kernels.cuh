@@ -13,7 +13,8 @@
 //
 // A stream over HBM: everything is read and written once, and the clipping takes no pass of its own.  A
 // warp takes 256 elements, its lanes 4 neighbours twice, and loads all arrays before it uses any.  The
-// list travels in the kernel's parameters.
+// list travels in the kernel's parameters; tensors of different types take launches of their own, each
+// compiled for its types.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,8 +29,10 @@ constexpr int kAdamBlock = 256;                              // elements that sh
 constexpr int kAdamChunk = kAdamThreads / 32 * kAdamBlock;   // elements a block takes at a time
 constexpr int kAdamSmall = 32, kAdamLarge = 384;             // tensors a launch's parameters hold
 
-// Bits of AdamTable::flags.
-enum { kAdamParamF32 = 1, kAdamGradF32 = 2, kAdamE4m3 = 4, kAdamVectors = 8, kAdamHead = 16 };   // head: bits 4 and 5
+// AdamTable::flags: whether the arrays are aligned alike, and how many elements behind a vector they start.
+enum { kAdamVectors = 1, kAdamHead = 2 };
+// What a tensor's parameter is; with its gradient's type and its states, what a kernel is compiled for.
+enum AdamParam { kAdamBf16 = 0, kAdamF32 = 1, kAdamMaster = 2 };
 
 template <int N>
 struct AdamTable {
@@ -51,7 +54,8 @@ struct AdamArgs {
     const int64_t *step;
     double log_b1, log_b2;
     float b1, b2, one_b1, one_b2, eps, max_norm;
-    uint64_t seed;
+    float minus_zero;
+    uint32_t key0[10], key1[10];   // Philox's keys of each round
 };
 
 // Four neighbours as they lie in memory: 4 words (fp32), 2 (bf16) or 1 (E4M3).
@@ -84,20 +88,24 @@ __device__ __forceinline__ void adam_load(AdamRaw &r, const void *base, int64_t 
             r.w[0] |= (uint32_t)p[e] << (8 * e);
     }
 }
-__device__ __forceinline__ void adam_get_f32(const AdamRaw &r, float (&v)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(r.w[e]);
+// The four as pairs.
+__device__ __forceinline__ void adam_get_f32(const AdamRaw &r, uint64_t (&v)[2]) {
+    v[0] = f2(__uint_as_float(r.w[0]), __uint_as_float(r.w[1]));
+    v[1] = f2(__uint_as_float(r.w[2]), __uint_as_float(r.w[3]));
 }
-__device__ __forceinline__ void adam_get_bf16(const AdamRaw &r, float (&v)[4]) {
-    v[0] = bf16_lo(r.w[0]); v[1] = bf16_hi(r.w[0]); v[2] = bf16_lo(r.w[1]); v[3] = bf16_hi(r.w[1]);
+__device__ __forceinline__ void adam_get_bf16(const AdamRaw &r, uint64_t (&v)[2]) {
+    v[0] = f2(bf16_lo(r.w[0]), bf16_hi(r.w[0]));
+    v[1] = f2(bf16_lo(r.w[1]), bf16_hi(r.w[1]));
 }
-__device__ __forceinline__ void adam_get_e4m3(const AdamRaw &r, float (&v)[4]) {
+__device__ __forceinline__ void adam_get_e4m3(const AdamRaw &r, uint64_t (&v)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        float x, y;
         asm("{\n\t.reg .b32 h;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 h, %2;\n\tmov.b32 {a, b}, h;\n\t"
             "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+            : "=f"(x), "=f"(y)
             : "h"((uint16_t)(r.w[0] >> (16 * i))));
+        v[i] = f2(x, y);
     }
 }
 template <int BYTES>
@@ -124,17 +132,13 @@ __device__ __forceinline__ void adam_store(void *base, int64_t at, bool whole, i
             p[e] = (uint8_t)(r.w[0] >> (8 * e));
     }
 }
-__device__ __forceinline__ void adam_put_f32(void *base, int64_t at, bool whole, int64_t n, const float (&v)[4]) {
-    AdamRaw r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r.w[e] = __float_as_uint(v[e]);
-    adam_store<4>(base, at, whole, n, r);
+__device__ __forceinline__ void adam_put_f32(void *base, int64_t at, bool whole, int64_t n, const uint64_t (&v)[2]) {
+    const float2 x = f2_get(v[0]), y = f2_get(v[1]);
+    adam_store<4>(base, at, whole, n, AdamRaw{{__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y)}});
 }
-__device__ __forceinline__ void adam_put_bf16(void *base, int64_t at, bool whole, int64_t n, const float (&v)[4]) {
-    AdamRaw r;
-    r.w[0] = bf16_pair(v[0], v[1]);
-    r.w[1] = bf16_pair(v[2], v[3]);
-    adam_store<2>(base, at, whole, n, r);
+__device__ __forceinline__ void adam_put_bf16(void *base, int64_t at, bool whole, int64_t n, const uint64_t (&v)[2]) {
+    const float2 x = f2_get(v[0]), y = f2_get(v[1]);
+    adam_store<2>(base, at, whole, n, AdamRaw{{bf16_pair(x.x, x.y), bf16_pair(y.x, y.y), 0, 0}});
 }
 
 // What the 256 elements of a warp are divided by to reach E4M3's largest number, and that scale.  Elements
@@ -151,34 +155,207 @@ __device__ __forceinline__ void adam_scale(uint32_t top, float &inv, float &scal
         scale = __fdiv_rn(t, 448.0f);
     }
 }
-// |x| * inv, rounded to E4M3 up or down by a 16-bit draw: the fp32 encoding keeps 3 bits of its mantissa, and
-// adding the draw to the 20 behind them carries with the right probability.  Below the normal numbers the
-// spacing is that of the smallest normal, which is added meanwhile.  Returns an fp32 number that E4M3 holds.
-__device__ __forceinline__ float adam_round(float x, float inv, uint32_t draw) {
-    const float a = __fmul_rn(fabsf(x), inv);
-    const float lift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
-    const uint32_t bits = (__float_as_uint(__fadd_rn(a, lift)) + (draw << 4)) & ~0xFFFFFu;
-    return copysignf(fminf(__fsub_rn(__uint_as_float(bits), lift), 448.0f), x);
-}
+// a * b, rounded, where the product goes on into a sum: as a fused multiply-add with -0, which changes nothing.  A
+// packed product and a packed sum would be contracted into one operation; nz is -0 at run time only, so that
+// this one is not taken for a plain product.
+__device__ __forceinline__ uint64_t adam_product(uint64_t a, uint64_t b, float nz) { return f2_fma(a, b, f2(nz, nz)); }
+
 __device__ __forceinline__ uint32_t adam_codes(const float (&v)[4]) {
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
     return lo | (uint32_t)hi << 16;
 }
+// b * 2^s + c and (b >> (32 - s)) + c as one instruction each.
+__device__ __forceinline__ uint32_t adam_up(uint32_t b, uint32_t s, uint32_t c) {
+    uint32_t r;
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(1u << s), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t adam_down(uint32_t b, uint32_t s, uint32_t c) {
+    uint32_t r;
+    asm("mad.hi.u32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(1u << s), "r"(c));
+    return r;
+}
 
-template <int N>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<N> t,
-                                                             const __grid_constant__ AdamArgs a) {
+// Four elements as E4M3 codes.  Each is x * inv, rounded up or down by a 16-bit draw d from the low (V: high) half
+// of its word: the fp32 encoding (sign and magnitude) keeps 3 bits of its mantissa, and adding 2^4 d to the 20
+// behind them carries with the right probability; the largest is off 448 by two units at most, which no draw
+// carries any further.  Below the normal numbers the spacing is that of the smallest normal, 2^-6, which is
+// added meanwhile: a warp without such elements (and zeros count as such) takes the shorter way.
+template <bool V>
+__device__ __forceinline__ float adam_cut(float x, uint32_t word) {
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float((V ? adam_down(word & 0xFFFF0000u, 20, b) : adam_up(word & 0xFFFFu, 4, b)) & ~0xFFFFFu);
+}
+__device__ __forceinline__ float adam_lift(float x) { return fabsf(x) < 0x1p-6f ? copysignf(0x1p-6f, x) : 0.0f; }
+template <bool V>
+__device__ __forceinline__ uint32_t adam_round(const float (&x)[4], bool small, const uint4 &w) {
+    float y[4];
+    if (small) {
+        const float l[4] = {adam_lift(x[0]), adam_lift(x[1]), adam_lift(x[2]), adam_lift(x[3])};
+        y[0] = __fsub_rn(adam_cut<V>(__fadd_rn(x[0], l[0]), w.x), l[0]);
+        y[1] = __fsub_rn(adam_cut<V>(__fadd_rn(x[1], l[1]), w.y), l[1]);
+        y[2] = __fsub_rn(adam_cut<V>(__fadd_rn(x[2], l[2]), w.z), l[2]);
+        y[3] = __fsub_rn(adam_cut<V>(__fadd_rn(x[3], l[3]), w.w), l[3]);
+    } else {
+        y[0] = adam_cut<V>(x[0], w.x);
+        y[1] = adam_cut<V>(x[1], w.y);
+        y[2] = adam_cut<V>(x[2], w.z);
+        y[3] = adam_cut<V>(x[3], w.w);
+    }
+    return adam_codes(y);
+}
+// The larger and the smaller magnitude of the three; NaN where one is.
+__device__ __forceinline__ float adam_max(float a, float b, float c) {
+    float m;
+    asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %2;\n\tabs.f32 y, %3;\n\tmax.NaN.f32 %0, %1, x, y;\n\t}" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float adam_min(float a, float b, float c) {
+    float m;
+    asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %2;\n\tabs.f32 y, %3;\n\tmin.NaN.f32 %0, %1, x, y;\n\t}" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float adam_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Of the step, the same for all tensors.
+struct AdamStep {
+    uint32_t step;
+    float lr, rate, c2, clip;
+};
+
+// 256 elements of tensor k, from the warp's first one on.  WHOLE: all of them are the tensor's, and its arrays
+// aligned alike; else `first` may be up to three before the tensor's first.
+template <int N, bool E4M3, AdamParam P, bool GF32, bool WHOLE>
+__device__ __forceinline__ void adam_step(const AdamTable<N> &t, int k, int64_t first, const AdamArgs &a,
+                                          const AdamStep &j, int lane) {
+    constexpr int kState = E4M3 ? 1 : 4, kGrad = GF32 ? 4 : 2;
+    const int64_t n = t.numel[k];
+    int64_t at[2];
+    bool whole[2];
+    AdamRaw rg[2], rp[2], rm[2], rv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        at[i] = first + 128 * i + 4 * lane;
+        whole[i] = WHOLE || ((t.flags[k] & kAdamVectors) && at[i] >= 0 && at[i] + 4 <= n);
+        if constexpr (!WHOLE) rg[i] = rp[i] = rm[i] = rv[i] = AdamRaw{};
+        adam_load<kGrad>(rg[i], t.grad[k], at[i], whole[i], n);
+        adam_load<kState>(rm[i], t.m[k], at[i], whole[i], n);
+        adam_load<kState>(rv[i], t.v[k], at[i], whole[i], n);
+        if constexpr (P == kAdamBf16)
+            adam_load<2>(rp[i], t.param[k], at[i], whole[i], n);
+        else
+            adam_load<4>(rp[i], P == kAdamMaster ? t.master[k] : t.param[k], at[i], whole[i], n);
+    }
+    const int64_t block = first / kAdamBlock;   // (E4M3: first is a multiple)
+    const float sm = E4M3 ? t.m_scale[k][block] : 0.0f, sv = E4M3 ? t.v_scale[k][block] : 0.0f;
+    const float decay = -j.lr * t.decay[k], nz = a.minus_zero;
+    uint64_t m[2][2], root[2][2];
+    float top_m = 0.0f, top_v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint64_t g[2], v[2], p[2];
+        if constexpr (GF32)
+            adam_get_f32(rg[i], g);
+        else
+            adam_get_bf16(rg[i], g);
+        if constexpr (E4M3) {
+            adam_get_e4m3(rm[i], m[i]);
+            adam_get_e4m3(rv[i], v);
+        } else {
+            adam_get_f32(rm[i], m[i]);
+            adam_get_f32(rv[i], v);
+        }
+        if constexpr (P == kAdamBf16)
+            adam_get_bf16(rp[i], p);
+        else
+            adam_get_f32(rp[i], p);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if constexpr (E4M3) {
+                m[i][e] = f2_mul(m[i][e], f2(sm, sm));
+                v[e] = f2_mul(v[e], f2(sv, sv));
+                v[e] = f2_mul(v[e], v[e]);
+            }
+            const uint64_t h = f2_mul(g[e], f2(j.clip, j.clip));
+            m[i][e] = f2_add(adam_product(m[i][e], f2(a.b1, a.b1), nz), adam_product(h, f2(a.one_b1, a.one_b1), nz));
+            v[e] = f2_add(adam_product(v[e], f2(a.b2, a.b2), nz),
+                          adam_product(f2_mul(h, h), f2(a.one_b2, a.one_b2), nz));
+            const float2 w = f2_get(v[e]);
+            root[i][e] = f2(__fsqrt_rn(w.x), __fsqrt_rn(w.y));
+            const float2 d = f2_get(f2_fma(root[i][e], f2(j.c2, j.c2), f2(a.eps, a.eps)));
+            p[e] = f2_fma(f2_mul(m[i][e], f2(-j.rate, -j.rate)), f2(adam_rcp(d.x), adam_rcp(d.y)),
+                          f2_fma(p[e], f2(decay, decay), p[e]));
+            if constexpr (E4M3) {
+                const float2 x = f2_get(m[i][e]), y = f2_get(root[i][e]);
+                top_m = adam_max(top_m, x.x, x.y);
+                top_v = adam_max(top_v, y.x, y.y);
+            }
+        }
+        if constexpr (P == kAdamMaster) adam_put_f32(t.master[k], at[i], whole[i], n, p);
+        if constexpr (P == kAdamF32)
+            adam_put_f32(t.param[k], at[i], whole[i], n, p);
+        else
+            adam_put_bf16(t.param[k], at[i], whole[i], n, p);
+        if constexpr (!E4M3) {
+            adam_put_f32(t.m[k], at[i], whole[i], n, m[i]);
+            adam_put_f32(t.v[k], at[i], whole[i], n, v);
+        }
+    }
+    if constexpr (E4M3) {
+        // elements behind the tensor's end are zeros here; odd lanes scale v, even ones m
+        const uint32_t um = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_m));
+        const uint32_t uv = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_v));
+        float inv, scale;
+        adam_scale(lane & 1 ? uv : um, inv, scale);
+        const float im = __shfl_sync(0xFFFFFFFFu, inv, 0), iv = __shfl_sync(0xFFFFFFFFu, inv, 1);
+        float xm[2][4], xv[2][4], low_m = 1.0f, low_v = 1.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 x = f2_get(adam_product(m[i][e], f2(im, im), nz)), y = f2_get(adam_product(root[i][e], f2(iv, iv), nz));
+                xm[i][2 * e] = x.x, xm[i][2 * e + 1] = x.y;
+                xv[i][2 * e] = y.x, xv[i][2 * e + 1] = y.y;
+                low_m = adam_min(low_m, x.x, x.y);
+                low_v = adam_min(low_v, y.x, y.y);
+            }
+        }
+        const bool small_m = __any_sync(0xFFFFFFFFu, !(low_m >= 0x1p-6f)), small_v = __any_sync(0xFFFFFFFFu, !(low_v >= 0x1p-6f));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t group = (uint64_t)at[i] >> 2;
+            uint4 w = make_uint4((uint32_t)group, (uint32_t)(group >> 32), (uint32_t)t.id[k], j.step);
+#pragma unroll
+            for (int r = 0; r < 10; ++r) w = philox_round(w, make_uint2(a.key0[r], a.key1[r]));
+            AdamRaw q;
+            q.w[0] = adam_round<false>(xm[i], small_m, w);
+            adam_store<1>(t.m[k], at[i], whole[i], n, q);
+            q.w[0] = adam_round<true>(xv[i], small_v, w);
+            adam_store<1>(t.v[k], at[i], whole[i], n, q);
+        }
+        if (lane < 2) put(lane ? t.v_scale[k] : t.m_scale[k], block, (n + kAdamBlock - 1) / kAdamBlock, scale);
+    }
+}
+
+template <int N, bool E4M3, AdamParam P, bool GF32>
+__global__ void __launch_bounds__(kAdamThreads, E4M3 ? 5 : 2) adamw_kernel(const __grid_constant__ AdamTable<N> t,
+                                                                const __grid_constant__ AdamArgs a) {
     grid_dependency();
     __shared__ float corr[2];
-    const float lr = *a.lr;
+    AdamStep j;
+    j.lr = *a.lr;
+    j.clip = 1.0f;
     const int64_t step = *a.step;
-    float clip = 1.0f;
     if (a.norm) {
         const float n = *a.norm, q = a.max_norm / (n + 1e-6f);
         if (!(fabsf(n) < INFINITY)) return;   // all of the grid: nothing is changed
-        clip = q > 1.0f ? 1.0f : q;
+        j.clip = q > 1.0f ? 1.0f : q;
     }
     if (step < 1) {
         set_device_error(QT2_ERR_INVALID_ARG);
@@ -189,126 +366,31 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         corr[threadIdx.x] = (float)(threadIdx.x ? sqrt(1.0 / left) : 1.0 / left);
     }
     __syncthreads();
-    const float rate = lr * corr[0], c2 = corr[1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    j.rate = j.lr * corr[0];
+    j.c2 = corr[1];
+    j.step = (uint32_t)step;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // the same in all lanes
+    int k = 0, end = 0;   // the current tensor, and the chunk behind its last
     for (int chunk = blockIdx.x; chunk < t.first[t.count]; chunk += gridDim.x) {
-        int k = 0, last = t.count - 1;
-        while (k < last) {
-            const int mid = (k + last + 1) >> 1;
-            if (t.first[mid] <= chunk)
-                k = mid;
-            else
-                last = mid - 1;
-        }
-        const uint32_t flags = t.flags[k];
-        const int64_t n = t.numel[k];
-        const bool e4m3 = flags & kAdamE4m3;
-        // the first element, and (aligned as the vectors are) up to three before the tensor's first
-        const int64_t first = (int64_t)(chunk - t.first[k]) * kAdamChunk + warp * kAdamBlock - (flags / kAdamHead);
-        if (first >= n) continue;
-        const bool p_f32 = flags & kAdamParamF32, g_f32 = flags & kAdamGradF32;
-        const float *const master = t.master[k];
-        int64_t at[2];
-        bool whole[2];
-        AdamRaw rg[2] = {}, rp[2] = {}, rm[2] = {}, rv[2] = {};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            at[i] = first + 128 * i + 4 * lane;
-            whole[i] = (flags & kAdamVectors) && at[i] >= 0 && at[i] + 4 <= n;
-            if (g_f32)
-                adam_load<4>(rg[i], t.grad[k], at[i], whole[i], n);
-            else
-                adam_load<2>(rg[i], t.grad[k], at[i], whole[i], n);
-            if (e4m3) {
-                adam_load<1>(rm[i], t.m[k], at[i], whole[i], n);
-                adam_load<1>(rv[i], t.v[k], at[i], whole[i], n);
-            } else {
-                adam_load<4>(rm[i], t.m[k], at[i], whole[i], n);
-                adam_load<4>(rv[i], t.v[k], at[i], whole[i], n);
+        if (chunk >= end) {
+            k = 0;
+            int last = t.count - 1;
+            while (k < last) {
+                const int mid = (k + last + 1) >> 1;
+                if (t.first[mid] <= chunk)
+                    k = mid;
+                else
+                    last = mid - 1;
             }
-            if (master)
-                adam_load<4>(rp[i], master, at[i], whole[i], n);
-            else if (p_f32)
-                adam_load<4>(rp[i], t.param[k], at[i], whole[i], n);
-            else
-                adam_load<2>(rp[i], t.param[k], at[i], whole[i], n);
+            end = t.first[k + 1];
         }
-        const int64_t block = first / kAdamBlock, blocks = (n + kAdamBlock - 1) / kAdamBlock;
-        const float sm = e4m3 ? t.m_scale[k][block] : 0.0f, sv = e4m3 ? t.v_scale[k][block] : 0.0f;
-        const float decay = lr * t.decay[k];
-        float m[2][4], root[2][4];
-        uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float g[4], v[4], p[4];
-            if (g_f32)
-                adam_get_f32(rg[i], g);
-            else
-                adam_get_bf16(rg[i], g);
-            if (e4m3) {
-                adam_get_e4m3(rm[i], m[i]);
-                adam_get_e4m3(rv[i], v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    m[i][e] = __fmul_rn(m[i][e], sm);
-                    v[e] = __fmul_rn(v[e], sv);
-                    v[e] = __fmul_rn(v[e], v[e]);
-                }
-            } else {
-                adam_get_f32(rm[i], m[i]);
-                adam_get_f32(rv[i], v);
-            }
-            if (master || p_f32)
-                adam_get_f32(rp[i], p);
-            else
-                adam_get_bf16(rp[i], p);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float h = __fmul_rn(g[e], clip);
-                m[i][e] = __fadd_rn(__fmul_rn(m[i][e], a.b1), __fmul_rn(h, a.one_b1));
-                v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(h, h), a.one_b2));
-                root[i][e] = __fsqrt_rn(v[e]);
-                p[e] = fmaf(-decay, p[e], p[e]) - __fdividef(rate * m[i][e], fmaf(root[i][e], c2, a.eps));
-                top_m = max(top_m, __float_as_uint(m[i][e]) & 0x7FFFFFFFu);
-                top_v = max(top_v, __float_as_uint(root[i][e]) & 0x7FFFFFFFu);
-            }
-            if (master) adam_put_f32(t.master[k], at[i], whole[i], n, p);
-            if (p_f32)
-                adam_put_f32(t.param[k], at[i], whole[i], n, p);
-            else
-                adam_put_bf16(t.param[k], at[i], whole[i], n, p);
-            if (!e4m3) {
-                adam_put_f32(t.m[k], at[i], whole[i], n, m[i]);
-                adam_put_f32(t.v[k], at[i], whole[i], n, v);
-            }
-        }
-        if (!e4m3) continue;
-        // elements behind the tensor's end are zeros here
-        float im, iv, nm, nv;
-        adam_scale(__reduce_max_sync(0xFFFFFFFFu, top_m), im, nm);
-        adam_scale(__reduce_max_sync(0xFFFFFFFFu, top_v), iv, nv);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint64_t group = (uint64_t)at[i] >> 2;
-            const uint4 w4 = philox4x32_10(make_uint4((uint32_t)group, (uint32_t)(group >> 32), (uint32_t)t.id[k], (uint32_t)step),
-                                           make_uint2((uint32_t)a.seed, (uint32_t)(a.seed >> 32)));
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            float qm[4], qv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                qm[e] = adam_round(m[i][e], im, w[e] & 0xFFFFu);
-                qv[e] = adam_round(root[i][e], iv, w[e] >> 16);
-            }
-            AdamRaw r;
-            r.w[0] = adam_codes(qm);
-            adam_store<1>(t.m[k], at[i], whole[i], n, r);
-            r.w[0] = adam_codes(qv);
-            adam_store<1>(t.v[k], at[i], whole[i], n, r);
-        }
-        if (lane == 0) {
-            put(t.m_scale[k], block, blocks, nm);
-            put(t.v_scale[k], block, blocks, nv);
-        }
+        const int flags = t.flags[k];
+        const int64_t first = (int64_t)(chunk - t.first[k]) * kAdamChunk + warp * kAdamBlock - flags / kAdamHead;
+        if (first >= t.numel[k]) continue;
+        if ((flags & kAdamVectors) && first >= 0 && first + kAdamBlock <= t.numel[k])
+            adam_step<N, E4M3, P, GF32, true>(t, k, first, a, j, lane);
+        else
+            adam_step<N, E4M3, P, GF32, false>(t, k, first, a, j, lane);
     }
 }
 

@@ -78,37 +78,6 @@ __device__ __forceinline__ void store_row(T *row, int c, int cols, const float (
     }
 }
 
-// Pairs of fp32 values in a 64-bit register, and the packed instructions on them: they halve the
-// instructions an element costs, which is what bounds these kernels next to HBM.
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 f2_get(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ float f2_sum(uint64_t v) {
-    const float2 p = f2_get(v);
-    return p.x + p.y;
-}
 // The pairs of a 16-byte vector, and back (rounded to the row's type).
 __device__ __forceinline__ uint64_t bf16_pair_f2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
 template <class T>

@@ -128,14 +128,18 @@ __device__ __forceinline__ uint32_t e4m3_sr(float v, uint32_t u) {
 // Stream (seed, tensor id): word j is element j&3 of the block at counter
 // (lo32(j>>2), hi32(j>>2), tensor id, 0) under key (lo32(seed), hi32(seed)).
 // ------------------------------------------------------------------------------------------
+constexpr uint32_t kPhiloxKey0 = 0x9E3779B9u, kPhiloxKey1 = 0xBB67AE85u;   // added to the key each round
+__device__ __forceinline__ uint4 philox_round(uint4 c, uint2 k) {
+    uint32_t hi0 = __umulhi(0xD2511F53u, c.x), lo0 = 0xD2511F53u * c.x;
+    uint32_t hi1 = __umulhi(0xCD9E8D57u, c.z), lo1 = 0xCD9E8D57u * c.z;
+    return make_uint4(hi1 ^ c.y ^ k.x, lo1, hi0 ^ c.w ^ k.y, lo0);
+}
 __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
-        uint32_t hi0 = __umulhi(0xD2511F53u, c.x), lo0 = 0xD2511F53u * c.x;
-        uint32_t hi1 = __umulhi(0xCD9E8D57u, c.z), lo1 = 0xCD9E8D57u * c.z;
-        c = make_uint4(hi1 ^ c.y ^ k.x, lo1, hi0 ^ c.w ^ k.y, lo0);
-        k.x += 0x9E3779B9u;
-        k.y += 0xBB67AE85u;
+        c = philox_round(c, k);
+        k.x += kPhiloxKey0;
+        k.y += kPhiloxKey1;
     }
     return c;
 }

@@ -678,14 +678,20 @@ int adamw_head(const qt2_adamw_tensor &a) {
     return same && (!e4m3 || head == 0) ? head : -1;
 }
 
-// The next launch's tensors, from tensors[at] on; returns the next `at`.
+// The types that a kernel is compiled for, as a number below 12.
+int adamw_kind(const qt2_adamw_tensor &a) {
+    const int param = a.master ? kAdamMaster : a.param_dtype == QT2_DTYPE_F32 ? kAdamF32 : kAdamBf16;
+    return param * 4 + (a.grad_dtype == QT2_DTYPE_F32 ? 2 : 0) + (a.state == QT2_STATE_E4M3 ? 1 : 0);
+}
+
+// The next launch's tensors, those of one kind from tensors[at] on; returns the next `at`.
 template <int N>
-int64_t adamw_table(AdamTable<N> &t, const qt2_adamw_tensor *tensors, int64_t at, int64_t count) {
+int64_t adamw_table(AdamTable<N> &t, const qt2_adamw_tensor *tensors, int64_t at, int64_t count, int kind) {
     t.count = 0;
     t.first[0] = 0;
     for (; at < count && t.count < N; ++at) {
         const qt2_adamw_tensor &a = tensors[at];
-        if (a.numel == 0) continue;
+        if (a.numel == 0 || adamw_kind(a) != kind) continue;
         const int k = t.count, head = adamw_head(a);
         const int64_t next = t.first[k] + ceil_div(std::max(0, head) + a.numel, kAdamChunk);
         if (next > INT32_MAX / 2) break;   // a launch's chunks, and the blocks' next ones
@@ -701,32 +707,45 @@ int64_t adamw_table(AdamTable<N> &t, const qt2_adamw_tensor *tensors, int64_t at
         t.first[k + 1] = (int32_t)next;
         t.id[k] = (int32_t)at;
         t.decay[k] = a.weight_decay;
-        t.flags[k] = (uint8_t)((a.param_dtype == QT2_DTYPE_F32 ? kAdamParamF32 : 0) |
-                               (a.grad_dtype == QT2_DTYPE_F32 ? kAdamGradF32 : 0) |
-                               (a.state == QT2_STATE_E4M3 ? kAdamE4m3 : 0) | (head >= 0 ? kAdamVectors : 0) |
-                               std::max(0, head) * kAdamHead);
+        t.flags[k] = (uint8_t)((head >= 0 ? kAdamVectors : 0) + std::max(0, head) * kAdamHead);
     }
     return at;
 }
 
-template <int N>
+template <int N, bool E4M3, AdamParam P, bool GF32>
 cudaError_t launch_adamw(const AdamTable<N> &t, const AdamArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     static PerDeviceOnce once;
     static std::atomic<int> blocks[kMaxDevices];
     int64_t n = 0;
-    const cudaError_t e = resident_blocks(once, blocks, adamw_kernel<N>, kAdamThreads, 0, &n);
+    const auto kernel = adamw_kernel<N, E4M3, P, GF32>;
+    const cudaError_t e = resident_blocks(once, blocks, kernel, kAdamThreads, 0, &n);
     if (e != cudaSuccess) return e;
-    return launch(adamw_kernel<N>, (unsigned)std::min<int64_t>(n, t.first[t.count]), kAdamThreads, 0, s, t, a);
+    return launch(kernel, (unsigned)std::min<int64_t>(n, t.first[t.count]), kAdamThreads, 0, s, t, a);
+}
+template <int N, AdamParam P>
+cudaError_t launch_adamw(const AdamTable<N> &t, int kind, const AdamArgs &a, cudaStream_t s) {
+    return (kind & 3) == 0   ? launch_adamw<N, false, P, false>(t, a, s)
+           : (kind & 3) == 1 ? launch_adamw<N, true, P, false>(t, a, s)
+           : (kind & 3) == 2 ? launch_adamw<N, false, P, true>(t, a, s)
+                             : launch_adamw<N, true, P, true>(t, a, s);
 }
 template <int N>
 cudaError_t adamw(const qt2_adamw_tensor *tensors, int64_t count, const AdamArgs &a, cudaStream_t s) {
+    uint32_t kinds = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (tensors[i].numel) kinds |= 1u << adamw_kind(tensors[i]);
     AdamTable<N> t;
-    for (int64_t at = 0; at < count;) {
-        at = adamw_table(t, tensors, at, count);
-        if (t.count == 0) break;
-        const cudaError_t e = launch_adamw(t, a, s);
-        if (e != cudaSuccess) return e;
+    for (int kind = 0; kind < 12; ++kind) {
+        if (!(kinds >> kind & 1)) continue;
+        for (int64_t at = 0; at < count;) {
+            at = adamw_table(t, tensors, at, count, kind);
+            if (t.count == 0) break;
+            const cudaError_t e = kind / 4 == kAdamBf16  ? launch_adamw<N, kAdamBf16>(t, kind, a, s)
+                                  : kind / 4 == kAdamF32 ? launch_adamw<N, kAdamF32>(t, kind, a, s)
+                                                         : launch_adamw<N, kAdamMaster>(t, kind, a, s);
+            if (e != cudaSuccess) return e;
+        }
     }
     return cudaSuccess;
 }
@@ -1164,7 +1183,11 @@ qt2_status qt2_adamw(const qt2_adamw_tensor *tensors, int64_t count, const float
     a.one_b2 = (float)(1.0 - beta2);
     a.eps = eps;
     a.max_norm = max_norm;
-    a.seed = seed;
+    a.minus_zero = -0.0f;
+    for (uint32_t r = 0; r < 10; ++r) {
+        a.key0[r] = (uint32_t)seed + r * kPhiloxKey0;
+        a.key1[r] = (uint32_t)(seed >> 32) + r * kPhiloxKey1;
+    }
     const cudaStream_t s = as_stream(stream);
     return from_cuda(count <= kAdamSmall ? adamw<kAdamSmall>(tensors, count, a, s)
                                          : adamw<kAdamLarge>(tensors, count, a, s));
