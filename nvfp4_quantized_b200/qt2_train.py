@@ -37,6 +37,7 @@ QT2_ROPE_HALVES, QT2_ROPE_PAIRS = 0, 1
 QT2_STATE_F32, QT2_STATE_E4M3 = 0, 1
 
 _DTYPE = {torch.bfloat16: QT2_DTYPE_BF16, torch.float32: QT2_DTYPE_F32}
+_STATE = {torch.float32: QT2_STATE_F32, torch.float8_e4m3fn: QT2_STATE_E4M3}
 
 
 class GradC(ctypes.Structure):
@@ -410,39 +411,46 @@ class AdamWList:
         columns = (self.params, self.masters, self.grads, self.m, self.v, self.m_scales, self.v_scales)
         if any(len(c) != n for c in columns) or len(decay) != n:
             raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-        self.c = (AdamWTensorC * max(1, n))()
-        devices, written, read = set(), [], []
-        for row, w, *tensors in zip(self.c, decay, *columns):
-            p, master, g, m1, v1, ms, vs = tensors
-            eight = m1.dtype is torch.float8_e4m3fn
-            if (p.dtype not in _DTYPE or g.dtype not in _DTYPE or not (eight or m1.dtype is torch.float32)
-                    or v1.dtype is not m1.dtype or (master is not None and p.dtype is torch.float32)):
-                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-            if eight == (ms is None) or eight == (vs is None):
-                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-            _only(fn, torch.float32, master, ms, vs)
-            _vectors(fn, *tensors)
-            size = p.numel()
-            if any(t is not None and t.numel() != size for t in (master, g, m1, v1)) or any(
-                    t is not None and t.numel() != (size + 255) // 256 for t in (ms, vs)):
-                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-            devices.update(t.get_device() for t in tensors if t is not None)
-            at = [None if t is None else t.data_ptr() for t in tensors]
-            row.param, row.master, row.grad, row.m, row.v, row.m_scale, row.v_scale = at
-            row.numel, row.param_dtype, row.grad_dtype, row.state, row.weight_decay = size, _DTYPE[p.dtype], _DTYPE[g.dtype], eight, w
-            for k, t in enumerate(tensors):
-                if t is not None and size:
-                    (read if k == 2 else written).append((at[k], at[k] + t.numel() * t.element_size(), k != 2))
+        kinds = [_DTYPE.get(t.dtype) for t in self.params], [_DTYPE.get(t.dtype) for t in self.grads]
+        state = [_STATE.get(t.dtype) for t in self.m]
+        if None in kinds[0] or None in kinds[1] or None in state or [_STATE.get(t.dtype) for t in self.v] != state:
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        fp32 = torch.float32
+        if any([t is not None and (k or t.dtype is not fp32) for k, t in zip(kinds[0], self.masters)]) or any(
+                [(t is not None) != e or (e and t.dtype is not fp32) for ts in columns[5:] for e, t in zip(state, ts)]):
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        given = [[t for t in c if t is not None] for c in columns]
+        if not all([t.is_contiguous() for c in given for t in c]):
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        sizes = [t.numel() for t in self.params]
+        four = [4 * m for m in sizes]
+        scales = [4 * ((m + 255) // 256) for m in sizes]
+        states = [m if e else 4 * m for e, m in zip(state, sizes)]
+        # bytes of each array (what is not given is skipped)
+        extent = [[m * (4 if k else 2) for k, m in zip(kinds[0], sizes)], four, [m * (4 if k else 2) for k, m in zip(kinds[1], sizes)],
+                  states, states, scales, scales]
+        if any([t is not None and t.nbytes != m for c, ms in zip(columns, extent) for t, m in zip(c, ms)]):
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        devices = {t.get_device() for c in given for t in c}
         if len(devices) > 1:
             raise QT2Error(fn, QT2_ERR_DEVICE)
         self.device = devices.pop() if devices else -1
+        at = [[0 if t is None else t.data_ptr() for t in c] for c in columns]
         # what is written overlaps nothing else
+        spans = [(p, p + m, k != 2) for k, (ps, ms) in enumerate(zip(at, extent)) for p, m in zip(ps, ms) if p and m]
+        spans.sort()
         end, end_written = 0, 0
-        for lo, hi, writes in sorted(written + read):
+        for lo, hi, writes in spans:
             if lo < end_written or (writes and lo < end):
                 raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-            end = max(end, hi)
-            end_written = hi if writes else end_written
+            if hi > end:
+                end = hi
+            if writes:
+                end_written = hi
+        bits = array.array("I", array.array("f", decay).tobytes())
+        rows = [(*row[:8], row[8] | row[9] << 32, row[10] | row[11] << 32) for row in zip(*at, sizes, *kinds, state, bits)]
+        flat = array.array("Q", [v for row in rows for v in row] or [0] * 10)
+        self.c = (AdamWTensorC * max(1, n)).from_buffer(flat)
         self.address = ctypes.addressof(self.c)
 
 
