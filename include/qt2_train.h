@@ -154,7 +154,7 @@ QT2_API qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_n
  * A position outside [0, P) leaves its token unturned and is reported as QT2_ERR_INVALID_ARG through
  * qt2_train_device_status.  R = 0: nothing is turned; positions and tables may be NULL.
  * x and y have type x_dtype, wq and wk w_dtype; all of it 16-byte aligned (positions 8), strides multiples of
- * 8 elements, so that no two heads overlap.  D and R are multiples of 8, D <= 1024, R <= D.  Statistics and
+ * 8 elements below 2^32, such that no two heads overlap.  D and R are multiples of 8, D <= 1024, R <= D.  Statistics and
  * products are fp32, rounded once on writing (squares too: elements from 2^63 on overflow them).  y may be x
  * with its strides.  eps >= 0 and finite.  T, Hq and Hk are below 2^30, 2^20 and 2^20.
  * --------------------------------------------------------------------------------------- */

@@ -457,41 +457,47 @@ cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream
 }
 
 // ------------------------------------------------------------------------------- queries and keys
-// Rows a group of lanes has in flight, by the registers that they take.
+// Heads that a group of lanes takes at a time.  Forward, 32768 x 16+16 x 128 bf16: 1 head 190 us, 2 heads 143, 4
+// heads 103, 8 heads 100 (but twice the work where a kind has 4); backward 1 head 279, 2 heads 196, 4 heads 158,
+// 8 heads, which spill, 231.
 template <class T, int N>
-constexpr int kQkUnroll = std::max(1, (sizeof(T) == 2 ? 4 : 2) / N);
+constexpr int kQkRows = std::max(1, (sizeof(T) == 2 ? 4 : 2) / N);
 
 // Blocks of the backward pass: each leaves a share of dw.
 int64_t qk_bwd_blocks(int64_t T, int64_t Hq, int64_t Hk) {
-    return std::min<int64_t>(148 * 3, ceil_div(T * (Hq + Hk), kQkThreads / 32));
+    return std::min<int64_t>(148 * 2, ceil_div(T * (Hq + Hk), kQkThreads / 32));
 }
 
-template <class T, int G, int N>
+template <class T, int G, int N, bool PAIRS>
 cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    constexpr int U = kQkUnroll<T, N>, kRows = 32 / G * U;
-    const int64_t items = ceil_div(a.T * a.heads[0], kRows) + ceil_div(a.T * a.heads[1], kRows);
-    return launch(qk_norm_rope_fwd_kernel<T, G, N, U>, (unsigned)ceil_div(items, kQkThreads / 32), kQkThreads, 0, s, a);
+    constexpr int U = kQkRows<T, N>, kGroups = 32 / G;
+    const int64_t warps = ceil_div(a.T * ceil_div(a.heads[0], U), kGroups) + ceil_div(a.T * ceil_div(a.heads[1], U), kGroups);
+    return launch(qk_norm_rope_fwd_kernel<T, G, N, U, PAIRS>, (unsigned)ceil_div(warps, kQkThreads / 32), kQkThreads, 0,
+                  s, a);
 }
-template <class T, int G, int N>
+template <class T, int G, int N, bool PAIRS>
 cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
-    return launch(qk_norm_rope_bwd_kernel<T, G, N, kQkUnroll<T, N>>, (unsigned)a.parts, kQkThreads,
+    return launch(qk_norm_rope_bwd_kernel<T, G, N, kQkRows<T, N>, PAIRS>, (unsigned)a.parts, kQkThreads,
                   a.D * (kQkThreads / 32) * sizeof(float), s, a);
 }
 template <bool BWD, class T, int G, int N>
-cudaError_t qk_launch(const QkArgs &a, cudaStream_t s) {
-    return BWD ? launch_qk_bwd<T, G, N>(a, s) : launch_qk_fwd<T, G, N>(a, s);
+cudaError_t qk_launch(const QkArgs &a, bool pairs, cudaStream_t s) {
+    if constexpr (BWD)
+        return pairs ? launch_qk_bwd<T, G, N, true>(a, s) : launch_qk_bwd<T, G, N, false>(a, s);
+    else
+        return pairs ? launch_qk_fwd<T, G, N, true>(a, s) : launch_qk_fwd<T, G, N, false>(a, s);
 }
 template <bool BWD, class T>
-cudaError_t qk_norm_rope(const QkArgs &a, cudaStream_t s) {
+cudaError_t qk_norm_rope(const QkArgs &a, int pairing, cudaStream_t s) {
     const int slots = a.D / 8;
-    if (slots <= 4) return qk_launch<BWD, T, 4, 1>(a, s);
-    if (slots <= 8) return qk_launch<BWD, T, 8, 1>(a, s);
-    if (slots <= 16) return qk_launch<BWD, T, 16, 1>(a, s);
-    if (slots <= 32) return qk_launch<BWD, T, 32, 1>(a, s);
-    if (slots <= 64) return qk_launch<BWD, T, 32, 2>(a, s);
-    return qk_launch<BWD, T, 32, 4>(a, s);
+    const bool pairs = pairing == QT2_ROPE_PAIRS;
+    if (slots <= 8) return qk_launch<BWD, T, 8, 1>(a, pairs, s);
+    if (slots <= 16) return qk_launch<BWD, T, 16, 1>(a, pairs, s);
+    if (slots <= 32) return qk_launch<BWD, T, 32, 1>(a, pairs, s);
+    if (slots <= 64) return qk_launch<BWD, T, 32, 2>(a, pairs, s);
+    return qk_launch<BWD, T, 32, 4>(a, pairs, s);
 }
 cudaError_t launch_qk_dw(const QkArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
@@ -505,7 +511,7 @@ bool qk_dims_ok(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
 }
 // T tokens of H heads of D elements, one inside the other either way, none over another.
 bool qk_strides_ok(int64_t T, int64_t H, int64_t D, int64_t ld, int64_t hs) {
-    const int64_t most = int64_t(1) << 40;
+    const int64_t most = int64_t(1) << 32;
     if (ld < 0 || hs < 0 || ld >= most || hs >= most) return false;
     const __int128 heads = (__int128)(H - 1) * hs + D, tokens = (__int128)(T - 1) * ld + D;   // of a token, of a head
     return ((H == 1 || hs >= D) && (T == 1 || ld >= heads)) || ((T == 1 || ld >= D) && (H == 1 || hs >= tokens));
@@ -526,7 +532,7 @@ qt2_status qk_check(const void *x, int x_dtype, int64_t T, int64_t Hq, int64_t H
 }
 QkArgs qk_args(const void *x, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t ldx, int64_t hsx, const void *wq,
                const void *wk, int w_dtype, float eps, const int64_t *positions, const float *cos, const float *sin,
-               int64_t P, int64_t R, int pairing) {
+               int64_t P, int64_t R) {
     QkArgs a{};
     a.x = x;
     a.w[0] = wq;
@@ -540,9 +546,8 @@ QkArgs qk_args(const void *x, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int6
     a.heads[1] = (int)Hk;
     a.D = (int)D;
     a.R = (int)R;
-    a.ldx = ldx;
-    a.hsx = hsx;
-    a.pairs = pairing == QT2_ROPE_PAIRS;
+    a.ldx = (uint32_t)ldx;
+    a.hsx = (uint32_t)hsx;
     a.w_f32 = w_dtype == QT2_DTYPE_F32;
     a.eps = eps;
     return a;
@@ -1072,13 +1077,13 @@ qt2_status qt2_qk_norm_rope_fwd(const void *x, int x_dtype, int64_t T, int64_t H
     if (!qk_strides_ok(T, Hq + Hk, D, ldy, hsy)) return QT2_ERR_SHAPE;
     if (!aligned(y, 16) || ldy % 8 || hsy % 8) return QT2_ERR_ALIGN;
     if (const qt2_status st = check_device()) return st;
-    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R, pairing);
+    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R);
     a.y = y;
-    a.ldy = ldy;
-    a.hsy = hsy;
+    a.ldy = (uint32_t)ldy;
+    a.hsy = (uint32_t)hsy;
     const cudaStream_t s = as_stream(stream);
-    return from_cuda(x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<false, float>(a, s)
-                                              : qk_norm_rope<false, __nv_bfloat16>(a, s));
+    return from_cuda(x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<false, float>(a, pairing, s)
+                                              : qk_norm_rope<false, __nv_bfloat16>(a, pairing, s));
 }
 
 qt2_status qt2_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t Hq, int64_t Hk, int64_t D, size_t *bytes) {
@@ -1108,19 +1113,20 @@ qt2_status qt2_qk_norm_rope_bwd(const void *dy, int64_t lddy, int64_t hsdy, cons
     if (const qt2_status st = qt2_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D, &need)) return st;
     if (const qt2_status st = check_workspace(workspace, ws_bytes, need)) return st;
     if (const qt2_status st = check_device()) return st;
-    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R, pairing);
+    QkArgs a = qk_args(x, T, Hq, Hk, D, ldx, hsx, wq, wk, w_dtype, eps, positions, cos, sin, P, R);
     a.dy = dy;
-    a.lddy = lddy;
-    a.hsdy = hsdy;
+    a.lddy = (uint32_t)lddy;
+    a.hsdy = (uint32_t)hsdy;
     a.y = dx;
-    a.ldy = lddx;
-    a.hsy = hsdx;
+    a.ldy = (uint32_t)lddx;
+    a.hsy = (uint32_t)hsdx;
     a.dw[0] = dwq;
     a.dw[1] = dwk;
     a.part = dwq || dwk ? static_cast<float *>(workspace) : nullptr;
     a.parts = (int)qk_bwd_blocks(T, Hq, Hk);
     const cudaStream_t s = as_stream(stream);
-    cudaError_t e = x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<true, float>(a, s) : qk_norm_rope<true, __nv_bfloat16>(a, s);
+    cudaError_t e = x_dtype == QT2_DTYPE_F32 ? qk_norm_rope<true, float>(a, pairing, s)
+                                             : qk_norm_rope<true, __nv_bfloat16>(a, pairing, s);
     if (e == cudaSuccess && a.part) e = launch_qk_dw(a, s);
     return from_cuda(e);
 }

@@ -8,11 +8,12 @@
 // A row is one head of one token.  The members of a rotated pair, (i, i + R/2) or (2i, 2i + 1), belong to
 // one lane: a lane's slot is two chunks of 4 elements, R/2 apart or next to each other, with the same 4
 // angles either way.  No element passes between lanes; only the row's one or two sums do, by shuffles.
-// G lanes share a row (N slots each), and a group takes U rows that follow one another, whose loads are
-// all issued before the first is used.  Backward recomputes r from x, which it reads anyway.
+// G lanes share a row (N slots each), and a group takes U heads of a token, which share their angles; their
+// loads are all issued before the first is used.  Backward recomputes r from x, which it reads anyway.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "qt2_device.cuh"
 #include "vec_device.cuh"
@@ -30,41 +31,76 @@ struct QkArgs {
     const float *cos, *sin;        // [P][R / 2]
     int64_t P, T;
     int heads[2], D, R;
-    int64_t ldx, hsx, ldy, hsy, lddy, hsdy;   // between tokens, between heads
-    int pairs, w_f32;
+    uint32_t ldx, hsx, ldy, hsy, lddy, hsdy;   // between tokens, between heads
+    int w_f32;
     float eps;
     float *part;                   // [blocks][2][D], or null
     int parts;
 };
 
-// Four elements in memory as they are loaded.
+// A slot's eight elements as they lie in memory: two chunks of four.
 template <class T>
-struct QkChunk;
+struct QkRaw;
 template <>
-struct QkChunk<__nv_bfloat16> {
-    uint2 r;
-    __device__ __forceinline__ void get(float *v) const {
-        v[0] = bf16_lo(r.x); v[1] = bf16_hi(r.x); v[2] = bf16_lo(r.y); v[3] = bf16_hi(r.y);
+struct QkRaw<__nv_bfloat16> {
+    uint2 c[2];
+};
+template <>
+struct QkRaw<float> {
+    float4 c[2];
+};
+// The same as the first (x) and the second members (y) of four pairs.
+struct QkPairs {
+    uint64_t x[2], y[2];
+};
+template <bool PAIRS>
+__device__ __forceinline__ QkPairs qk_get(const QkRaw<__nv_bfloat16> &r) {
+    const uint2 a = r.c[0], b = r.c[1];
+    if constexpr (PAIRS)
+        return {{f2(bf16_lo(a.x), bf16_lo(a.y)), f2(bf16_lo(b.x), bf16_lo(b.y))},
+                {f2(bf16_hi(a.x), bf16_hi(a.y)), f2(bf16_hi(b.x), bf16_hi(b.y))}};
+    else
+        return {{f2(bf16_lo(a.x), bf16_hi(a.x)), f2(bf16_lo(a.y), bf16_hi(a.y))},
+                {f2(bf16_lo(b.x), bf16_hi(b.x)), f2(bf16_lo(b.y), bf16_hi(b.y))}};
+}
+template <bool PAIRS>
+__device__ __forceinline__ QkPairs qk_get(const QkRaw<float> &r) {
+    const float4 a = r.c[0], b = r.c[1];
+    if constexpr (PAIRS)
+        return {{f2(a.x, a.z), f2(b.x, b.z)}, {f2(a.y, a.w), f2(b.y, b.w)}};
+    else
+        return {{f2(a.x, a.y), f2(a.z, a.w)}, {f2(b.x, b.y), f2(b.z, b.w)}};
+}
+template <class T, bool PAIRS>
+__device__ __forceinline__ QkRaw<T> qk_put(const QkPairs &p) {
+    const float2 x0 = f2_get(p.x[0]), x1 = f2_get(p.x[1]), y0 = f2_get(p.y[0]), y1 = f2_get(p.y[1]);
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (PAIRS)
+            return {{make_float4(x0.x, y0.x, x0.y, y0.y), make_float4(x1.x, y1.x, x1.y, y1.y)}};
+        else
+            return {{make_float4(x0.x, x0.y, x1.x, x1.y), make_float4(y0.x, y0.y, y1.x, y1.y)}};
+    } else {
+        if constexpr (PAIRS)
+            return {{make_uint2(bf16_pair(x0.x, y0.x), bf16_pair(x0.y, y0.y)), make_uint2(bf16_pair(x1.x, y1.x), bf16_pair(x1.y, y1.y))}};
+        else
+            return {{make_uint2(bf16_pair(x0.x, x0.y), bf16_pair(x1.x, x1.y)), make_uint2(bf16_pair(y0.x, y0.y), bf16_pair(y1.x, y1.y))}};
     }
-    __device__ __forceinline__ void set(const float *v) { r = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])); }
-};
-template <>
-struct QkChunk<float> {
-    float4 r;
-    __device__ __forceinline__ void get(float *v) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
-    __device__ __forceinline__ void set(const float *v) { r = make_float4(v[0], v[1], v[2], v[3]); }
-};
+}
 
-// Where a slot's two chunks are in a head, and whether they are rotated (by angles 4 s ... 4 s + 3).
+// Where slot s's two chunks are in a head, and whether they are rotated (by angles `angle` ... + 3).  A lane
+// without a slot reads what the first one does.
 struct QkSlot {
-    int c0, c1;
+    int c0, c1, angle;
     bool live, turned;
 };
+template <bool PAIRS>
 __device__ __forceinline__ QkSlot qk_slot(const QkArgs &a, int s) {
     QkSlot q;
     q.live = s < a.D / 8;
+    if (!q.live) s = 0;
     q.turned = s < a.R / 8;
-    if (a.pairs) {
+    q.angle = 4 * s;
+    if (PAIRS) {
         q.c0 = 8 * s;
         q.c1 = 8 * s + 4;
     } else if (q.turned) {
@@ -76,202 +112,206 @@ __device__ __forceinline__ QkSlot qk_slot(const QkArgs &a, int s) {
     }
     return q;
 }
+// Where element e (0..7: x[0], x[1], y[0], y[1] of QkPairs) of a slot is in its head.
+template <bool PAIRS>
+__device__ __forceinline__ int qk_place(const QkSlot &q, int e) {
+    if (PAIRS) return q.c0 + 2 * (e & 3) + (e >> 2);
+    return e < 4 ? q.c0 + e : q.c1 + e - 4;
+}
 
 template <class T>
-__device__ __forceinline__ void qk_load(const void *base, int64_t at, const QkSlot &q, QkChunk<T> (&c)[2]) {
+__device__ __forceinline__ QkRaw<T> qk_load(const void *base, int64_t at, const QkSlot &q) {
+    using Chunk = std::remove_reference_t<decltype(QkRaw<T>{}.c[0])>;
     const T *p = static_cast<const T *>(base) + at;
-    c[0] = *reinterpret_cast<const QkChunk<T> *>(p + q.c0);
-    c[1] = *reinterpret_cast<const QkChunk<T> *>(p + q.c1);
+    QkRaw<T> r;
+    r.c[0] = *reinterpret_cast<const Chunk *>(p + q.c0);
+    r.c[1] = *reinterpret_cast<const Chunk *>(p + q.c1);
+    return r;
 }
 template <class T>
-__device__ __forceinline__ void qk_store(const QkArgs &a, int64_t at, const QkSlot &q, const float (&v)[8]) {
+__device__ __forceinline__ void qk_store(const QkArgs &a, int64_t at, const QkSlot &q, const QkRaw<T> &r) {
+    using Chunk = std::remove_reference_t<decltype(QkRaw<T>{}.c[0])>;
     T *const base = static_cast<T *>(a.y);
-    const int64_t size = ((a.T - 1) * a.ldy + (a.heads[0] + a.heads[1] - 1) * a.hsy + a.D) * (int64_t)sizeof(T);
-    QkChunk<T> c[2];
-    c[0].set(v);
-    c[1].set(v + 4);
-    if (QT2_STORE_OK(base + at + q.c0, 4 * sizeof(T), base, size)) *reinterpret_cast<QkChunk<T> *>(base + at + q.c0) = c[0];
-    if (QT2_STORE_OK(base + at + q.c1, 4 * sizeof(T), base, size)) *reinterpret_cast<QkChunk<T> *>(base + at + q.c1) = c[1];
+    const int64_t size = ((a.T - 1) * a.ldy + (int64_t)(a.heads[0] + a.heads[1] - 1) * a.hsy + a.D) * (int64_t)sizeof(T);
+    T *const p = base + at;
+    if (QT2_STORE_OK(p + q.c0, 4 * sizeof(T), base, size)) *reinterpret_cast<Chunk *>(p + q.c0) = r.c[0];
+    if (QT2_STORE_OK(p + q.c1, 4 * sizeof(T), base, size)) *reinterpret_cast<Chunk *>(p + q.c1) = r.c[1];
 }
-__device__ __forceinline__ void qk_weight(const QkArgs &a, int kind, const QkSlot &q, float (&w)[8]) {
+template <bool PAIRS>
+__device__ __forceinline__ QkPairs qk_weight(const QkArgs &a, int kind, const QkSlot &q) {
     const void *p = a.w[kind];
+    const uint64_t one = f2(1.0f, 1.0f);
+    if (!p || !q.live) return {{one, one}, {one, one}};
+    return a.w_f32 ? qk_get<PAIRS>(qk_load<float>(p, 0, q)) : qk_get<PAIRS>(qk_load<__nv_bfloat16>(p, 0, q));
+}
+// cos and sin of four pairs; 1 and 0 where nothing is turned.
+struct QkAngles {
+    uint64_t c[2], s[2];
+};
+__device__ __forceinline__ QkAngles qk_angles(const QkArgs &a, int64_t pos, const QkSlot &q) {
+    float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (q.turned && (uint64_t)pos < (uint64_t)a.P) {
+        const int64_t at = pos * (a.R / 2) + q.angle;
+        c = *reinterpret_cast<const float4 *>(a.cos + at);
+        d = *reinterpret_cast<const float4 *>(a.sin + at);
+    }
+    return {{f2(c.x, c.y), f2(c.z, c.w)}, {f2(d.x, d.y), f2(d.z, d.w)}};
+}
+// (x, y) -> (x c - y s, y c + x s), or back.
+template <bool BACK>
+__device__ __forceinline__ void qk_turn(QkPairs &p, const QkAngles &g) {
+    const uint64_t minus = f2(-1.0f, -1.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-    if (!p || !q.live) return;
-    if (a.w_f32) {
-        QkChunk<float> c[2];
-        qk_load<float>(p, 0, q, c);
-        c[0].get(w);
-        c[1].get(w + 4);
-    } else {
-        QkChunk<__nv_bfloat16> c[2];
-        qk_load<__nv_bfloat16>(p, 0, q, c);
-        c[0].get(w);
-        c[1].get(w + 4);
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t s = f2_mul(g.s[i], minus), x = p.x[i], y = p.y[i];
+        p.x[i] = f2_fma(y, BACK ? g.s[i] : s, f2_mul(x, g.c[i]));
+        p.y[i] = f2_fma(x, BACK ? s : g.s[i], f2_mul(y, g.c[i]));
     }
 }
-__device__ __forceinline__ void qk_angles(const QkArgs &a, int64_t pos, const QkSlot &q, int s, float4 &c, float4 &d) {
-    c = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (!q.turned || (uint64_t)pos >= (uint64_t)a.P) return;
-    const int64_t at = pos * (a.R / 2) + 4 * s;
-    c = *reinterpret_cast<const float4 *>(a.cos + at);
-    d = *reinterpret_cast<const float4 *>(a.sin + at);
-}
-// Pair p is (v[p], v[4 + p]), or (v[2 p], v[2 p + 1]).
-__device__ __forceinline__ void qk_turn(float (&v)[8], const float4 &c4, const float4 &s4, int pairs, float sign) {
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x * sign, s4.y * sign, s4.z * sign, s4.w * sign};
-    if (pairs) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float x = v[2 * p], y = v[2 * p + 1];
-            v[2 * p] = x * c[p] - y * s[p];
-            v[2 * p + 1] = y * c[p] + x * s[p];
-        }
-    } else {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float x = v[p], y = v[4 + p];
-            v[p] = x * c[p] - y * s[p];
-            v[4 + p] = y * c[p] + x * s[p];
-        }
-    }
+__device__ __forceinline__ uint64_t qk_squares(const QkPairs &v, uint64_t sum) {
+    return f2_fma(v.x[0], v.x[0], f2_fma(v.x[1], v.x[1], f2_fma(v.y[0], v.y[0], f2_fma(v.y[1], v.y[1], sum))));
 }
 
-// U rows of a group: rows [row, row + U) of a kind's T x heads, token by token.
+// What a group of lanes takes at a time: U heads of one kind of one token, which share its angles; the last of
+// them again where the kind's heads have no more.
 template <int U>
-struct QkRows {
-    int64_t t[U], pos[U];
-    int h[U];
-    bool live[U];
+struct QkUnit {
+    uint32_t t, h, more;   // token, first head (of all), heads behind it
+    __device__ __forceinline__ bool live(int u) const { return (uint32_t)u <= more; }
+    __device__ __forceinline__ int64_t at(int u, uint32_t ld, uint32_t hs) const {
+        return (int64_t)((uint64_t)t * ld + (uint64_t)h * hs + (uint64_t)min((uint32_t)u, more) * hs);
+    }
 };
 template <int U>
-__device__ __forceinline__ void qk_rows(const QkArgs &a, int kind, int64_t row, QkRows<U> &q) {
-    const int H = a.heads[kind];
-    const int64_t n = a.T * H;
-    int64_t t = row < n ? row / H : 0;
-    int h = (int)(row < n ? row - t * H : 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        q.live[u] = row + u < n;
-        q.t[u] = q.live[u] ? t : 0;
-        q.h[u] = q.live[u] ? h + (kind ? a.heads[0] : 0) : 0;
-        if (++h == H) h = 0, ++t;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        q.pos[u] = a.R == 0 ? 0 : a.pos ? a.pos[q.t[u]] : q.t[u];
-        if (a.R && q.live[u] && (uint64_t)q.pos[u] >= (uint64_t)a.P) set_device_error(QT2_ERR_INVALID_ARG);
-    }
+__device__ __forceinline__ uint32_t qk_units(const QkArgs &a, int kind) {   // a token's
+    return ((uint32_t)a.heads[kind] + U - 1) / U;
+}
+template <int U>
+__device__ __forceinline__ QkUnit<U> qk_unit(const QkArgs &a, int kind, uint32_t units, uint32_t unit) {
+    QkUnit<U> q;
+    q.t = unit / units;
+    const uint32_t h = (unit - q.t * units) * U;
+    q.h = h + (kind ? a.heads[0] : 0);
+    q.more = min((uint32_t)U, (uint32_t)a.heads[kind] - h) - 1;
+    return q;
 }
 
-template <class T, int G, int N, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_fwd_kernel(const __grid_constant__ QkArgs a) {
-    constexpr int kRows = 32 / G * U;   // of a warp
+template <class T, int G, int N, int U, bool PAIRS>
+__global__ void __launch_bounds__(kQkThreads, N > 1 ? 2 : 5) qk_norm_rope_fwd_kernel(const __grid_constant__ QkArgs a) {
     grid_dependency();
-    const int lane = threadIdx.x & 31, g = lane % G;
+    const int g = threadIdx.x % G;
     const float inv_d = 1.0f / (float)a.D;
-    const int64_t items[2] = {(a.T * a.heads[0] + kRows - 1) / kRows, (a.T * a.heads[1] + kRows - 1) / kRows};
-    int64_t item = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
-    const int kind = item >= items[0];
-    if (kind) item -= items[0];
-    if (item >= items[kind]) return;
-    QkRows<U> rows;
-    qk_rows<U>(a, kind, item * kRows + lane / G * U, rows);
+    int64_t unit = (int64_t)blockIdx.x * (kQkThreads / G) + threadIdx.x / G;
+    // queries' units, filled up to whole warps so that a warp has one kind
+    const uint32_t units[2] = {qk_units<U>(a, 0), qk_units<U>(a, 1)};
+    const int64_t queries = (a.T * units[0] + 32 / G - 1) / (32 / G) * (32 / G);
+    const int kind = unit >= queries;
+    if (kind) unit -= queries;
+    const int64_t all = a.T * units[kind];
+    const bool live = unit < all;
+    if (!__any_sync(0xFFFFFFFFu, live)) return;
+    const QkUnit<U> q = qk_unit<U>(a, kind, units[kind], live ? (uint32_t)unit : (uint32_t)all - 1);
+    const int64_t pos = a.pos ? a.pos[q.t] : q.t;
     QkSlot slot[N];
-    QkChunk<T> raw[U][N][2] = {};
-    float4 c[U][N], s[U][N];
+    QkRaw<T> raw[U][N];
+    QkAngles angle[N];
+    QkPairs w[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[i] = qk_slot(a, g + i * G);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (slot[i].live && rows.live[u]) qk_load<T>(a.x, rows.t[u] * a.ldx + rows.h[u] * a.hsx, slot[i], raw[u][i]);
-    float w[N][8];
-#pragma unroll
-    for (int i = 0; i < N; ++i) qk_weight(a, kind, slot[i], w[i]);
+    for (int i = 0; i < N; ++i) slot[i] = qk_slot<PAIRS>(a, g + i * G);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < N; ++i) qk_angles(a, rows.pos[u], slot[i], g + i * G, c[u][i], s[u][i]);
+        for (int i = 0; i < N; ++i) raw[u][i] = qk_load<T>(a.x, q.at(u, a.ldx, a.hsx), slot[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        w[i] = qk_weight<PAIRS>(a, kind, slot[i]);
+        angle[i] = qk_angles(a, pos, slot[i]);
+    }
+    if (a.R && live && (uint64_t)pos >= (uint64_t)a.P) set_device_error(QT2_ERR_INVALID_ARG);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float v[N][8], sum = 0.0f;
+        QkPairs v[N];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            raw[u][i][0].get(v[i]);
-            raw[u][i][1].get(v[i] + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
+            v[i] = qk_get<PAIRS>(raw[u][i]);
+            const float part = f2_sum(qk_squares(v[i], 0));
+            sum += slot[i].live ? part : 0.0f;
         }
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
+        const uint64_t r2 = f2(r, r);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[i][e];
-            qk_turn(v[i], c[u][i], s[u][i], a.pairs, 1.0f);
-            if (slot[i].live && rows.live[u]) qk_store<T>(a, rows.t[u] * a.ldy + rows.h[u] * a.hsy, slot[i], v[i]);
+            for (int e = 0; e < 2; ++e) {
+                v[i].x[e] = f2_mul(f2_mul(v[i].x[e], r2), w[i].x[e]);
+                v[i].y[e] = f2_mul(f2_mul(v[i].y[e], r2), w[i].y[e]);
+            }
+            qk_turn<false>(v[i], angle[i]);
+            if (live && slot[i].live && q.live(u))
+                qk_store<T>(a, q.at(u, a.ldy, a.hsy), slot[i], qk_put<T, PAIRS>(v[i]));
         }
     }
 }
 
 // part[block][kind][D]: the block's share of dw.
-template <class T, int G, int N, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const __grid_constant__ QkArgs a) {
-    constexpr int kRows = 32 / G * U, kWarps = kQkThreads / 32;
+template <class T, int G, int N, int U, bool PAIRS>
+__global__ void __launch_bounds__(kQkThreads, N > 1 ? 1 : 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QkArgs a) {
+    constexpr int kWarps = kQkThreads / 32, kGroups = 32 / G;
     extern __shared__ float sums[];   // [kWarps][D]
     grid_dependency();
     const int lane = threadIdx.x & 31, g = lane % G, warp = threadIdx.x >> 5;
     const float inv_d = 1.0f / (float)a.D;
     QkSlot slot[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[i] = qk_slot(a, g + i * G);
+    for (int i = 0; i < N; ++i) slot[i] = qk_slot<PAIRS>(a, g + i * G);
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
-        float w[N][8], acc[N][8];
+        QkPairs w[N], acc[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            qk_weight(a, kind, slot[i], w[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+            w[i] = qk_weight<PAIRS>(a, kind, slot[i]);
+            acc[i] = QkPairs{};
         }
-        const int64_t items = (a.T * a.heads[kind] + kRows - 1) / kRows;
+        const uint32_t units = qk_units<U>(a, kind);
+        const int64_t all = a.T * units;
 #pragma unroll 1
-        for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < items; item += (int64_t)gridDim.x * kWarps) {
-            QkRows<U> rows;
-            qk_rows<U>(a, kind, item * kRows + lane / G * U, rows);
-            QkChunk<T> raw[U][N][2] = {}, up[U][N][2] = {};   // zeros where no row or slot is
-            float4 c[U][N], s[U][N];
+        for (int64_t first = ((int64_t)blockIdx.x * kWarps + warp) * kGroups; first < all; first += (int64_t)gridDim.x * kWarps * kGroups) {
+            const int64_t unit = first + lane / G;
+            const bool live = unit < all;
+            const QkUnit<U> q = qk_unit<U>(a, kind, units, live ? (uint32_t)unit : (uint32_t)all - 1);
+            const int64_t pos = a.pos ? a.pos[q.t] : q.t;
+            QkRaw<T> raw[U][N], up[U][N];
+            QkAngles angle[N];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (slot[i].live && rows.live[u]) {
-                        qk_load<T>(a.x, rows.t[u] * a.ldx + rows.h[u] * a.hsx, slot[i], raw[u][i]);
-                        qk_load<T>(a.dy, rows.t[u] * a.lddy + rows.h[u] * a.hsdy, slot[i], up[u][i]);
-                    }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < N; ++i) qk_angles(a, rows.pos[u], slot[i], g + i * G, c[u][i], s[u][i]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[N][8], b[N][8], sum = 0.0f, dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    raw[u][i][0].get(v[i]);
-                    raw[u][i][1].get(v[i] + 4);
-                    up[u][i][0].get(b[i]);
-                    up[u][i][1].get(b[i] + 4);
-                    qk_turn(b[i], c[u][i], s[u][i], a.pairs, -1.0f);
+                    raw[u][i] = qk_load<T>(a.x, q.at(u, a.ldx, a.hsx), slot[i]);
+                    up[u][i] = qk_load<T>(a.dy, q.at(u, a.lddy, a.hsdy), slot[i]);
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        sum = fmaf(v[i][e], v[i][e], sum);
-                        dot = fmaf(b[i][e] * w[i][e], v[i][e], dot);
+            for (int i = 0; i < N; ++i) angle[i] = qk_angles(a, pos, slot[i]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                QkPairs v[N], b[N];
+                float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    v[i] = qk_get<PAIRS>(raw[u][i]);
+                    b[i] = qk_get<PAIRS>(up[u][i]);
+                    qk_turn<true>(b[i], angle[i]);
+                    uint64_t dot2 = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        dot2 = f2_fma(f2_mul(b[i].x[e], w[i].x[e]), v[i].x[e], dot2);
+                        dot2 = f2_fma(f2_mul(b[i].y[e], w[i].y[e]), v[i].y[e], dot2);
                     }
+                    const float part = f2_sum(qk_squares(v[i], 0)), share = f2_sum(dot2);
+                    sum += slot[i].live ? part : 0.0f;
+                    dot += slot[i].live ? share : 0.0f;
                 }
 #pragma unroll
                 for (int o = G / 2; o > 0; o >>= 1) {
@@ -279,31 +319,37 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const __gr
                     dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
                 }
                 const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
-                const float mean = dot * r * inv_d;   // of b w n
+                const float minus_mean = -(dot * r * inv_d);   // of b w n
+                const uint64_t r2 = f2(r, r), m2 = f2(minus_mean, minus_mean);
+                const bool row = live && q.live(u);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    float d[8];
+                    QkPairs d;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float n = v[i][e] * r;
-                        d[e] = r * fmaf(-n, mean, b[i][e] * w[i][e]);
-                        if (rows.live[u]) acc[i][e] = fmaf(b[i][e], n, acc[i][e]);   // r may be inf where no row is
+                    for (int e = 0; e < 2; ++e) {
+                        const uint64_t nx = f2_mul(v[i].x[e], r2), ny = f2_mul(v[i].y[e], r2);
+                        d.x[e] = f2_mul(r2, f2_fma(nx, m2, f2_mul(b[i].x[e], w[i].x[e])));
+                        d.y[e] = f2_mul(r2, f2_fma(ny, m2, f2_mul(b[i].y[e], w[i].y[e])));
+                        if (row) {
+                            acc[i].x[e] = f2_fma(b[i].x[e], nx, acc[i].x[e]);
+                            acc[i].y[e] = f2_fma(b[i].y[e], ny, acc[i].y[e]);
+                        }
                     }
-                    if (a.y && slot[i].live && rows.live[u])
-                        qk_store<T>(a, rows.t[u] * a.ldy + rows.h[u] * a.hsy, slot[i], d);
+                    if (a.y && slot[i].live && row)
+                        qk_store<T>(a, q.at(u, a.ldy, a.hsy), slot[i], qk_put<T, PAIRS>(d));
                 }
             }
         }
         if (!a.part) continue;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            const float2 p[4] = {f2_get(acc[i].x[0]), f2_get(acc[i].x[1]), f2_get(acc[i].y[0]), f2_get(acc[i].y[1])};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 8; ++e) {
+                float x = e & 1 ? p[e / 2].y : p[e / 2].x;
 #pragma unroll
-                for (int o = G; o < 32; o <<= 1) acc[i][e] += __shfl_xor_sync(0xFFFFFFFFu, acc[i][e], o);
-            if (lane < G && slot[i].live) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sums[warp * a.D + (e < 4 ? slot[i].c0 + e : slot[i].c1 + e - 4)] = acc[i][e];
+                for (int o = G; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+                if (lane < G && slot[i].live) sums[warp * a.D + qk_place<PAIRS>(slot[i], e)] = x;
             }
         }
         __syncthreads();

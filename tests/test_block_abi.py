@@ -136,7 +136,7 @@ QK_BAD = [(dict(x=None), ARG), (dict(xd=2), ARG), (dict(wd=9), ARG), (dict(eps=-
           (dict(pairing=2), ARG), (dict(cos=None), ARG), (dict(sin=None), ARG), (dict(T=0), SHAPE), (dict(T=1 << 30), SHAPE), (dict(Hq=-1), SHAPE),
           (dict(Hq=0, Hk=0), SHAPE), (dict(Hk=1 << 20), SHAPE), (dict(T=1 << 20, Hq=1 << 13), SHAPE), (dict(D=0), SHAPE), (dict(D=12), SHAPE),
           (dict(D=1032), SHAPE), (dict(R=24), SHAPE), (dict(R=4), SHAPE), (dict(R=-8), SHAPE), (dict(P=0), SHAPE), (dict(P=1 << 30), SHAPE),
-          (dict(pos=None, P=4), SHAPE), (dict(ldx=56), SHAPE), (dict(hsx=8), SHAPE), (dict(ldx=-80), SHAPE), (dict(ldx=1 << 40), SHAPE),
+          (dict(pos=None, P=4), SHAPE), (dict(ldx=56), SHAPE), (dict(hsx=8), SHAPE), (dict(ldx=-80), SHAPE), (dict(ldx=1 << 32), SHAPE), (dict(hsx=1 << 32, ldx=16), SHAPE),
           (dict(ldx=16, hsx=72), SHAPE), (dict(x=0x1008), ALIGN), (dict(ldx=84), ALIGN), (dict(hsx=17), ALIGN), (dict(wq=0x2008), ALIGN),
           (dict(wk=0x3004), ALIGN), (dict(pos=0x4004), ALIGN), (dict(cos=0x5008), ALIGN), (dict(sin=0x6004), ALIGN)]
 
