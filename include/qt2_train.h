@@ -10,8 +10,8 @@
  * no abort, one NVTX range per call), with these differences:
  *   - Dimensions are any positive ints below 2^30, not multiples of 128 unless a call says so (a matrix
  *     of the head loss or of a gated product has fewer than 2^44 elements).  Matrices are row-major with a leading dimension that is a
- *     multiple of 8 elements, at least the row's length and below 2^40 (x and w of the head loss:
- *     2^39), and 16-byte aligned bases.  Elements between a row's length and its leading dimension
+ *     multiple of 8 elements, at least the row's length and below 2^40 (x and w of the head loss, gate and
+ *     up of the gated product's backward pass: 2^39), and 16-byte aligned bases.  Elements between a row's length and its leading dimension
  *     are neither used nor written.  All other arrays are contiguous.
  *   - Outputs and workspaces must not overlap inputs or each other, except where a call says so.
  *     Two calls that can run at the same time need workspaces of their own (as do two captured

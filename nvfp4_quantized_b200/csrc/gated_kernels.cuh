@@ -15,12 +15,13 @@
 // Rows and columns come in 128s; a tile's second half may lie behind the end (TMA fills it with zeros,
 // codes and scales, and nothing of it is stored).
 //
-// Roles, per CTA of 384 threads, persistent over the tiles (K = 256 a stage, a ring of 5):
+// Roles, per CTA, persistent over the tiles (K = 256 a stage):
 //   warp 0        producer: a stage's scale atoms on one barrier, then its codes on another.
 //   warp 1        leader: issues the MMAs; both: allocate and free tensor memory.
 //   warp 2        leader: copies the scale atoms into the tensor memory of both SMs.
-//   warps 4..11   epilogue: warp w has TMEM lanes 32 (w % 4) on and half of the columns; all its sums go to
-//                 registers, then the accumulator is free for the next tile's MMAs.
+//   warps 4...    epilogue: warp w has TMEM lanes 32 (w % 4) on and its share of the columns; all its sums go to
+//                 registers, then the accumulator is free for the next tile's MMAs.  Backward each warp loads its own
+//                 pieces of gate and up by TMA ahead of their use.
 // Every wait is bounded; after a timeout the leader drains what was issued, both CTAs meet, and TMEM is
 // freed.
 #pragma once
@@ -33,36 +34,43 @@
 
 namespace qt2 {
 
+template <bool BWD>
 struct GatedCfg {
-    static constexpr int kStages = 5;
-    static constexpr int kThreads = 384;
+    static constexpr int kStages = BWD ? 4 : 5;
     static constexpr int kEpiWarp0 = 4;
     static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+    static constexpr int kRegsOthers = 40, kRegsEpi = 232;   // backward
     static constexpr int kA = 128 * 128;          // own 128 rows, K = 256
     static constexpr int kB = 128 * 128;          // own half of B's 256 rows
     static constexpr int kSfa = 4 * 512;          // 4 k-blocks x one 512-byte atom
     static constexpr int kSfb = 2 * 4 * 512;      // of all of B's rows
     static constexpr int kStageBytes = kA + kB + kSfa + kSfb;
-    static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 512;
+    // what an epilogue warp has of shared memory: 32 rows x 64 columns of bf16, backward of gate and of up
+    static constexpr int kPiece = 32 * 64 * 2;
+    static constexpr int kOwnBytes = BWD ? 2 * kPiece : kPiece;
+    static constexpr int kBars = 4 * kStages + 2 + (BWD ? kEpiWarps : 0);
+    static constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kOwnBytes + 1024 + 512;
     static constexpr int kTmemCols = 512;         // accumulator 256 + 5 scale regions x 48
     static constexpr int kSfRegionCols = 48;
     // E2M1 x E2M1, UE4M3 scales, K-major A and B, M = 256 (pair), N = 256
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (32u << 17) | (16u << 24);
+    static_assert(kStageBytes % 1024 == 0, "stage alignment");
+    static_assert(256 + kStages * kSfRegionCols <= kTmemCols, "TMEM columns");
+    static_assert(8 * kBars + 8 <= 512, "barriers");
 };
-static_assert(GatedCfg::kStageBytes % 1024 == 0, "stage alignment");
-static_assert(256 + GatedCfg::kStages * GatedCfg::kSfRegionCols <= GatedCfg::kTmemCols, "TMEM columns");
 
 // b and sfb: gate and up (forward); the down projection in the first (backward).
 struct GatedMaps {
     CUtensorMap a, b[2], sfa, sfb[2];
+    CUtensorMap gate, up;   // backward
 };
 
 struct GatedArgs {
     const float *ga, *gb[2];      // tensor scales of a and of the one or two b
     float alpha;
     int M, F, K;                  // multiples of 128
-    int m_fast;                   // tiles run over M first
-    int wide;                     // every array's rows start on 32 bytes
+    int group_m;                  // rows of tiles that are run through together
     __nv_bfloat16 *gate, *up;     // forward: written, or both null; backward: read
     int64_t ldgu;
     __nv_bfloat16 *dgate, *dup;   // backward
@@ -71,123 +79,149 @@ struct GatedArgs {
     int64_t ldh;
 };
 
-__device__ __forceinline__ float gated_exp(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-    return y;
-}
-
-// s of act(x) = x s, and its derivative.  exp overflows to inf and s to 0 where x is far below zero.
-template <int ACT>
-__device__ __forceinline__ float gated_sigmoid(float x, float &rise) {
+// act(x) = x s of two elements, and (SLOPE) its derivative.  exp overflows to inf, and s is 0, where x is far below
+// zero; the exponent of GELU is taken at most 10 from zero, further out s is 0 or 1.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ uint64_t gated_act(uint64_t x, uint64_t &slope) {
+    constexpr float kLog2e = 1.4426950408889634f, c = 1.5957691216057308f, d = 0.044715f;   // c: 2 sqrt(2/pi)
+    const uint64_t one = f2(1.0f, 1.0f);
+    uint64_t b = x, t, rise = one;   // the exponent of s (in base 2, sign turned), and its derivative
     if constexpr (ACT == QT2_ACT_SILU) {
-        const float s = __fdividef(1.0f, 1.0f + gated_exp(-x));
-        rise = s * (1.0f - s);
-        return s;
+        t = f2_mul(x, f2(-kLog2e, -kLog2e));
     } else {
-        constexpr float c = 1.5957691216057308f;   // 2 sqrt(2/pi)
-        const float b = fminf(fmaxf(x, -10.0f), 10.0f), q = b * b;   // further out s is 0 or 1
-        const float s = __fdividef(1.0f, 1.0f + gated_exp(-c * b * fmaf(0.044715f, q, 1.0f)));
-        rise = s * (1.0f - s) * c * fmaf(3.0f * 0.044715f, q, 1.0f);
-        return s;
+        const float2 y = f2_get(x);
+        b = f2(fminf(fmaxf(y.x, -10.0f), 10.0f), fminf(fmaxf(y.y, -10.0f), 10.0f));
+        const uint64_t q = f2_mul(b, b);
+        t = f2_mul(f2_mul(b, f2(-c * kLog2e, -c * kLog2e)), f2_fma(q, f2(d, d), one));
+        rise = f2_fma(q, f2(3 * c * d, 3 * c * d), f2(c, c));
     }
+    const float2 e = f2_get(t);
+    float ex, ey, sx, sy;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(e.y));
+    const float2 n = f2_get(f2_add(f2(ex, ey), one));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sx) : "f"(n.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sy) : "f"(n.y));
+    const uint64_t s = f2(sx, sy);
+    if constexpr (SLOPE) {   // s + b s (1 - s) rise
+        const uint64_t bs = f2_mul(f2_mul(b, s), f2_fma(s, f2(-1.0f, -1.0f), one));
+        slope = ACT == QT2_ACT_SILU ? f2_add(bs, s) : f2_fma(bs, rise, s);
+    }
+    return f2_mul(x, s);
+}
+__device__ __forceinline__ uint32_t gated_bits(uint64_t v) {
+    const float2 p = f2_get(v);
+    return bf16_pair(p.x, p.y);
 }
 
-// 16 bf16 of a row; 16-byte aligned, or (wide) 32.
-__device__ __forceinline__ void gated_store(__nv_bfloat16 *p, const uint32_t (&v)[8], bool wide) {
-    if (wide) {
-        st_global_v8(p, v);
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+// A piece lies in shared memory in rows of 128 bytes whose 16-byte parts are permuted (part ^ row % 8), as TMA loads
+// them with the 128-byte swizzle: a warp meets in no bank, whether each lane has a row or eight lanes share one.
+// Columns [16 i, 16 i + 16) of this lane's row:
+__device__ __forceinline__ void piece_get(const uint8_t *piece, int lane, int i, uint32_t (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(piece + lane * 128 + (((2 * i + k) ^ (lane & 7)) << 4));
+        v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
     }
 }
-__device__ __forceinline__ void gated_load(const __nv_bfloat16 *p, uint32_t (&v)[8]) {
-    const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void piece_put(uint8_t *piece, int lane, int i, const uint32_t *v) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint4 *>(piece + lane * 128 + (((2 * i + k) ^ (lane & 7)) << 4)) =
+            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+// The piece to 32 rows of a matrix, whole 128-byte lines at a time: stored by each lane along its own row, 32
+// bytes at a time, the outputs took as many requests to L2 as the operands and cost most of their time.
+__device__ __forceinline__ void piece_store(const uint8_t *piece, int lane, __nv_bfloat16 *to, int64_t ld, const void *base,
+                                            uint64_t extent) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3), part = lane & 7;
+        __nv_bfloat16 *const p = to + row * ld + part * 8;
+        const uint4 q = *reinterpret_cast<const uint4 *>(piece + row * 128 + ((part ^ (row & 7)) << 4));
+        if (QT2_STORE_OK(p, 16, base, extent)) *reinterpret_cast<uint4 *>(p) = q;
+    }
+    __syncwarp();
 }
 
-// 64 columns of h from the sums of gate (v[0..63]) and up (v[64..127]).
+// 64 columns of h, gate and up from their sums: v[0..63] and v[64..127].
 template <int ACT>
-__device__ __forceinline__ void gated_forward(const GatedArgs &a, const uint32_t (&v)[128], int64_t row, int64_t col,
-                                              float sg, float su) {
+__device__ __forceinline__ void gated_forward(const GatedArgs &a, const uint32_t (&v)[128], uint8_t *piece, int lane,
+                                              int64_t row, int64_t col, float sg, float su) {
     const uint64_t hs = ((uint64_t)(a.M - 1) * a.ldh + a.F) * 2, gs = ((uint64_t)(a.M - 1) * a.ldgu + a.F) * 2;
-    __nv_bfloat16 *const h = a.h + row * a.ldh + col;
-    __nv_bfloat16 *const gate = a.gate + row * a.ldgu + col, *const up = a.up + row * a.ldgu + col;
-    if (!QT2_STORE_OK(h, 128, a.h, hs)) return;
-    if (a.gate && (!QT2_STORE_OK(gate, 128, a.gate, gs) || !QT2_STORE_OK(up, 128, a.up, gs))) return;
+    uint32_t pg[32], pu[32];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t ph[8], pg[8], pu[8];
+        uint32_t ph[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int j = 16 * i + 2 * k;
-            const float g0 = __uint_as_float(v[j]) * sg, g1 = __uint_as_float(v[j + 1]) * sg;
-            const float u0 = __uint_as_float(v[64 + j]) * su, u1 = __uint_as_float(v[65 + j]) * su;
-            float r;
-            ph[k] = bf16_pair(g0 * gated_sigmoid<ACT>(g0, r) * u0, g1 * gated_sigmoid<ACT>(g1, r) * u1);
-            pg[k] = bf16_pair(g0, g1);
-            pu[k] = bf16_pair(u0, u1);
+            const uint64_t g = f2_mul(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2(sg, sg));
+            const uint64_t u = f2_mul(f2(__uint_as_float(v[64 + j]), __uint_as_float(v[65 + j])), f2(su, su));
+            uint64_t none;
+            ph[k] = gated_bits(f2_mul(gated_act<ACT, false>(g, none), u));
+            pg[8 * i + k] = gated_bits(g);
+            pu[8 * i + k] = gated_bits(u);
         }
-        gated_store(h + 16 * i, ph, a.wide);
-        if (a.gate) {
-            gated_store(gate + 16 * i, pg, a.wide);
-            gated_store(up + 16 * i, pu, a.wide);
-        }
+        piece_put(piece, lane, i, ph);
     }
+    piece_store(piece, lane, a.h + row * a.ldh + col, a.ldh, a.h, hs);
+    if (!a.gate) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) piece_put(piece, lane, i, &pg[8 * i]);
+    piece_store(piece, lane, a.gate + row * a.ldgu + col, a.ldgu, a.gate, gs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) piece_put(piece, lane, i, &pu[8 * i]);
+    piece_store(piece, lane, a.up + row * a.ldgu + col, a.ldgu, a.up, gs);
 }
 
-// 128 columns of dgate, dup and h from the sums of dh.
+// 64 columns of dgate, dup and h from the sums of dh (v) and the pieces of gate and up, which are overwritten.
 template <int ACT>
-__device__ __forceinline__ void gated_backward(const GatedArgs &a, const uint32_t (&v)[128], int64_t row, int64_t col,
-                                               float sc) {
+__device__ __forceinline__ void gated_backward(const GatedArgs &a, const uint32_t *v, uint8_t *piece, int lane, int64_t row,
+                                               int64_t col, float sc) {
     const uint64_t hs = ((uint64_t)(a.M - 1) * a.ldh + a.F) * 2, ds = ((uint64_t)(a.M - 1) * a.lddgu + a.F) * 2;
-    const __nv_bfloat16 *const gate = a.gate + row * a.ldgu + col, *const up = a.up + row * a.ldgu + col;
-    __nv_bfloat16 *const dg = a.dgate + row * a.lddgu + col, *const du = a.dup + row * a.lddgu + col;
-    __nv_bfloat16 *const h = a.h + row * a.ldh + col;
-    if (!QT2_STORE_OK(dg, 256, a.dgate, ds) || !QT2_STORE_OK(du, 256, a.dup, ds)) return;
-    if (a.h && !QT2_STORE_OK(h, 256, a.h, hs)) return;
+    uint8_t *const piece_u = piece + GatedCfg<true>::kPiece;
+    uint32_t ph[32];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t pg[8], pu[8], ph[8];
-        gated_load(gate + 16 * i, pg);
-        gated_load(up + 16 * i, pu);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t pg[8], pu[8];
+        piece_get(piece, lane, i, pg);
+        piece_get(piece_u, lane, i, pu);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            float d[2], e[2], f[2];
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const float g = o ? bf16_hi(pg[k]) : bf16_lo(pg[k]), u = o ? bf16_hi(pu[k]) : bf16_lo(pu[k]);
-                const float dh = __uint_as_float(v[16 * i + 2 * k + o]) * sc;
-                float rise;
-                const float s = gated_sigmoid<ACT>(g, rise), act = g * s;
-                const float x = ACT == QT2_ACT_SILU ? g : fminf(fmaxf(g, -10.0f), 10.0f);
-                d[o] = dh * u * fmaf(x, rise, s);
-                e[o] = dh * act;
-                f[o] = act * u;
-            }
-            pg[k] = bf16_pair(d[0], d[1]);
-            pu[k] = bf16_pair(e[0], e[1]);
-            ph[k] = bf16_pair(f[0], f[1]);
+            const uint64_t g = f2(bf16_lo(pg[k]), bf16_hi(pg[k])), u = f2(bf16_lo(pu[k]), bf16_hi(pu[k]));
+            const int j = 16 * i + 2 * k;
+            const uint64_t dh = f2_mul(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2(sc, sc));
+            uint64_t slope;
+            const uint64_t act = gated_act<ACT, true>(g, slope);
+            pg[k] = gated_bits(f2_mul(f2_mul(dh, u), slope));
+            pu[k] = gated_bits(f2_mul(dh, act));
+            ph[8 * i + k] = gated_bits(f2_mul(act, u));
         }
-        gated_store(dg + 16 * i, pg, a.wide);
-        gated_store(du + 16 * i, pu, a.wide);
-        if (a.h) gated_store(h + 16 * i, ph, a.wide);
+        piece_put(piece, lane, i, pg);
+        piece_put(piece_u, lane, i, pu);
     }
+    piece_store(piece, lane, a.dgate + row * a.lddgu + col, a.lddgu, a.dgate, ds);
+    piece_store(piece_u, lane, a.dup + row * a.lddgu + col, a.lddgu, a.dup, ds);
+    if (!a.h) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) piece_put(piece, lane, i, &ph[8 * i]);
+    piece_store(piece, lane, a.h + row * a.ldh + col, a.ldh, a.h, hs);
 }
 
 template <bool BWD, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg<BWD>::kThreads, 1)
     gated_pair_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedArgs a) {
-    using Cfg = GatedCfg;
+    using Cfg = GatedCfg<BWD>;
     constexpr int S = Cfg::kStages;
     constexpr int kCols = BWD ? 256 : 128;   // of F a tile
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    // barriers: full[S] sftm[S] empty[S] acc_full acc_empty sfull[S]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(base + S * Cfg::kStageBytes);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 4 * S + 2);
+    uint8_t *const pieces = base + S * Cfg::kStageBytes;   // of the epilogue warps
+    // barriers: full[S] sftm[S] empty[S] acc_full acc_empty sfull[S], backward piece[warp]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(pieces + Cfg::kEpiWarps * Cfg::kOwnBytes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::kBars);
 
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -210,6 +244,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg::kThreads, 
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * Cfg::kEpiWarps);
+        if (BWD)
+            for (int i = 0; i < Cfg::kEpiWarps; ++i) mbar_init(sfull0 + 8 * (S + i), 1);   // the warp's own loads
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -222,19 +258,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg::kThreads, 
     const uint32_t tmem = *tmem_slot;
     grid_dependency();
 
-    // With m_fast the tiles in flight cover all of a small x and a few row blocks of the weights, which
-    // then stream from DRAM once; else the other way round.
+    // Tiles run over group_m rows of tiles first, then over F: those in flight share their operands' rows.
     auto tile_coords = [&](int tile, int &pm, int &pn) {
-        if (a.m_fast) {
-            pn = tile / num_pm;
-            pm = tile - pn * num_pm;
-        } else {
-            pm = tile / num_pn;
-            pn = tile - pm * num_pn;
-        }
+        const int group = tile / (a.group_m * num_pn), first = group * a.group_m;
+        const int rows = min(a.group_m, num_pm - first), r = tile - first * num_pn;
+        pn = r / rows;
+        pm = first + r - pn * rows;
     };
 
+    // The epilogue's warpgroups take registers over from the others' (the launch has 168 a thread).
+    static_assert(128 * Cfg::kRegsOthers + 32 * Cfg::kEpiWarps * Cfg::kRegsEpi <= 168 * Cfg::kThreads, "register split");
+
     int issued = 0, mma_done = 0, copied = 0;   // stages whose loads, MMAs and scale copies were issued
+    if (BWD && warp < Cfg::kEpiWarp0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOthers));
     if (warp == 0) {
         // -------------------------------------------------------------- producer (both CTAs)
         if (elect_one()) {
@@ -335,18 +371,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg::kThreads, 
             copied = j + 1;
         }
     } else if (warp >= Cfg::kEpiWarp0) {
+        if (BWD) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
         // -------------------------------------------------------------- epilogue (both CTAs)
-        const int quad = warp & 3, half = (warp - Cfg::kEpiWarp0) >> 2;
+        constexpr int kOwn = kCols / 2;   // columns of F that a warp has of a tile
+        const int quad = warp & 3, part = (warp - Cfg::kEpiWarp0) >> 2, ew = warp - Cfg::kEpiWarp0;
         const uint32_t acc_empty_leader = mapa_shared(acc_empty, 0);
         const float sc0 = a.alpha * *a.ga * *a.gb[0], sc1 = BWD ? 0.0f : a.alpha * *a.ga * *a.gb[1];
+        uint8_t *const piece = pieces + ew * Cfg::kOwnBytes;
+        // Backward: the warp's pieces of gate and up, two a tile.  One is loaded as soon as the one before it has left.
+        const uint32_t piece_bar = sfull0 + 8 * (S + ew);
+        int loads = 0, used = 0;
+        auto piece_at = [&](int j, int &x, int &y) {
+            int pm, pn;
+            tile_coords(cluster_id + (j >> 1) * num_clusters, pm, pn);
+            y = pm * 256 + (int)rank * 128 + quad * 32;
+            x = pn * kCols + part * kOwn + (j & 1) * 64;
+        };
+        auto load_piece = [&] {   // by one lane of the converged warp
+            if (loads == 2 * my_tiles) return;
+            int x, y;
+            piece_at(loads, x, y);
+            if (elect_one()) {
+                const uint32_t to = smem_u32(piece);
+                mbar_arrive_expect_tx(piece_bar, 2 * Cfg::kPiece);
+                tma_load_2d(to, &maps.gate, x, y, piece_bar);
+                tma_load_2d(to + Cfg::kPiece, &maps.up, x, y, piece_bar);
+            }
+            __syncwarp();
+            ++loads;
+        };
+        if constexpr (BWD) load_piece();
         for (int t = 0; t < my_tiles; ++t) {
             if (!mbar_wait_warp(acc_full, t & 1)) break;
             tc_fence_after();
             int pm, pn;
             tile_coords(cluster_id + t * num_clusters, pm, pn);
-            const int64_t row = (int64_t)pm * 256 + rank * 128 + quad * 32 + lane;
-            const int64_t col = (int64_t)pn * kCols + half * (kCols / 2);
-            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + half * (kCols / 2);
+            const int64_t row = (int64_t)pm * 256 + rank * 128 + quad * 32;   // the warp's first
+            const int64_t col = (int64_t)pn * kCols + part * kOwn;
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + part * kOwn;
+            const bool inside = row < a.M && col < a.F;   // M and F are multiples of 128: all of the warp's or nothing
             uint32_t v[128];
 #pragma unroll
             for (int c = 0; c < 128; c += 16)   // forward: 64 columns of gate, and of up 128 columns on
@@ -355,12 +418,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg::kThreads, 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader);
-            if (row >= a.M || col >= a.F) continue;   // M and F are multiples of 128: all of the warp's or nothing
-            if constexpr (BWD)
-                gated_backward<ACT>(a, v, row, col, sc0);
-            else
-                gated_forward<ACT>(a, v, row, col, sc0, sc1);
+            if constexpr (!BWD) {
+                if (inside) gated_forward<ACT>(a, v, piece, lane, row, col, sc0, sc1);
+            } else {
+                bool ok = true;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ok = ok && mbar_wait_warp(piece_bar, used & 1);
+                    if (!ok) continue;
+                    ++used;
+                    if (inside) gated_backward<ACT>(a, &v[64 * i], piece, lane, row, col + 64 * i, sc0);
+                    fence_proxy_async();   // this lane's accesses to the piece come before the load's
+                    __syncwarp();
+                    load_piece();
+                }
+                if (!ok) break;
+            }
         }
+        // after a timeout the warp's own load is waited for
+        if constexpr (BWD)
+            for (; used < loads; ++used) mbar_wait_warp(piece_bar, used & 1);
     }
     // Every role ends converged.  Only after a timeout can work still be in flight: the leader
     // waits (bounded) for the loads it issued past the last consumed stage and for the last

@@ -434,21 +434,19 @@ bool encode_view(CUtensorMap *codes, CUtensorMap *scales, const qt2_nvfp4_view *
                           (uint64_t)K * 8, 256, (uint32_t)atoms, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-bool rows_of_32_bytes(const void *p, int64_t ld) { return !p || (aligned(p, 32) && ld % 16 == 0); }
-
 template <bool BWD, int ACT>
 cudaError_t launch_gated(const GatedMaps &maps, const GatedArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
     static PerDeviceOnce once;
     const cudaError_t e = once.run([] {
         return cudaFuncSetAttribute(gated_pair_kernel<BWD, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    GatedCfg::kSmemBytes);
+                                    GatedCfg<BWD>::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
     const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.F, BWD ? 256 : 128);
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
-    return launch(gated_pair_kernel<BWD, ACT>, (unsigned)(2 * clusters), GatedCfg::kThreads, GatedCfg::kSmemBytes, s,
-                  maps, a);
+    return launch(gated_pair_kernel<BWD, ACT>, (unsigned)(2 * clusters), GatedCfg<BWD>::kThreads,
+                  GatedCfg<BWD>::kSmemBytes, s, maps, a);
 }
 template <bool BWD>
 cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream_t s) {
@@ -1019,13 +1017,12 @@ qt2_status qt2_gemm_nvfp4_gated(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b
     g.M = (int)M;
     g.F = (int)F;
     g.K = (int)K;
-    g.m_fast = M < 2 * F;
+    g.group_m = M < 2 * F ? (int)ceil_div(M, 256) : 1;
     g.gate = static_cast<__nv_bfloat16 *>(gate);
     g.up = static_cast<__nv_bfloat16 *>(up);
     g.ldgu = ldgu;
     g.h = static_cast<__nv_bfloat16 *>(h);
     g.ldh = ldh;
-    g.wide = rows_of_32_bytes(h, ldh) && rows_of_32_bytes(gate, ldgu) && rows_of_32_bytes(up, ldgu);
     return from_cuda(gated<false>(maps, g, act, as_stream(stream)));
 }
 
@@ -1038,12 +1035,19 @@ qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_vie
         return QT2_ERR_INVALID_ARG;
     if (!gated_dims_ok(M, F, K) || !ld_shape_ok(ldgu, F) || !ld_shape_ok(lddgu, F) || (h && !ld_shape_ok(ldh, F)))
         return QT2_ERR_SHAPE;
+    if (ldgu >= (int64_t(1) << 39)) return QT2_ERR_SHAPE;   // a tensor map's rows: below 2^40 bytes
     if (!view_aligned(a) || !view_aligned(b) || !aligned(gate, 16) || !aligned(up, 16) || ldgu % 8 ||
         !aligned(dgate, 16) || !aligned(dup, 16) || lddgu % 8 || (h && (!aligned(h, 16) || ldh % 8)))
         return QT2_ERR_ALIGN;
     if (const qt2_status st = check_device()) return st;
     GatedMaps maps{};
-    if (!encode_view(&maps.a, &maps.sfa, a, M, K, 1) || !encode_view(&maps.b[0], &maps.sfb[0], b, F, K, 2))
+    // gate and up in boxes of 32 rows x 64 columns
+    auto encode_piece = [&](CUtensorMap *m, const void *p) {
+        return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)F, (uint64_t)M, (uint64_t)ldgu * 2, 64, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!encode_view(&maps.a, &maps.sfa, a, M, K, 1) || !encode_view(&maps.b[0], &maps.sfb[0], b, F, K, 2) ||
+        !encode_piece(&maps.gate, gate) || !encode_piece(&maps.up, up))
         return QT2_ERR_CUDA;
     GatedArgs g{};
     g.ga = a->tensor_scale;
@@ -1052,7 +1056,7 @@ qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_vie
     g.M = (int)M;
     g.F = (int)F;
     g.K = (int)K;
-    g.m_fast = M < F;
+    g.group_m = 8;
     g.gate = static_cast<__nv_bfloat16 *>(const_cast<void *>(gate));
     g.up = static_cast<__nv_bfloat16 *>(const_cast<void *>(up));
     g.ldgu = ldgu;
@@ -1061,7 +1065,6 @@ qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_vie
     g.lddgu = lddgu;
     g.h = static_cast<__nv_bfloat16 *>(h);
     g.ldh = ldh;
-    g.wide = rows_of_32_bytes(dgate, lddgu) && rows_of_32_bytes(dup, lddgu) && rows_of_32_bytes(h, ldh);
     return from_cuda(gated<true>(maps, g, act, as_stream(stream)));
 }
 
