@@ -248,15 +248,15 @@ def qt2_linear_xent_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
 
 
 def _view(fn: str, v: qt2.View, R: int, C: int):
-    """The C form of an [R, C] view whose arrays are on the current device."""
-    if v.codes.dtype is not torch.uint8 or v.scales.dtype is not torch.uint8:
+    """The arrays of an [R, C] view."""
+    codes, scales, scale = v.codes, v.scales, v.tensor_scale
+    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or scale.dtype is not torch.float32
+            or not codes.is_contiguous() or not scales.is_contiguous()):
         raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-    _only(fn, torch.float32, v.tensor_scale)
-    _vectors(fn, v.codes, v.scales)
     # a view of other sizes holds fewer elements than the call reads, or others (sizes that no call takes are its to refuse)
-    if R > 0 and C > 0 and (v.codes.numel() != R * C // 2 or v.scales.numel() != R * C // 16):
+    if R > 0 and C > 0 and (codes.numel() != R * C // 2 or scales.numel() != R * C // 16):
         raise QT2Error(fn, QT2_ERR_SHAPE)
-    return ctypes.byref(qt2.NVFP4ViewC(*_ptrs(fn, v.codes, v.scales, v.tensor_scale)))
+    return codes, scales, scale
 
 
 def qt2_gemm_nvfp4_gated(a: qt2.View, b_gate: qt2.View, b_up: qt2.View, M: int, F: int, K: int, alpha: float, act: int,
@@ -266,9 +266,10 @@ def qt2_gemm_nvfp4_gated(a: qt2.View, b_gate: qt2.View, b_up: qt2.View, M: int, 
     [F, K]); g and u go to gate and up (for the backward pass; None: not kept).  bf16 outputs."""
     fn = "qt2_gemm_nvfp4_gated"
     _only(fn, torch.bfloat16, gate, up, h)
-    pa, pg, pu = _view(fn, a, M, K), _view(fn, b_gate, F, K), _view(fn, b_up, F, K)
-    qg, qu, qh = _ptrs(fn, gate, up, h)
-    _check(fn, lib().qt2_gemm_nvfp4_gated(pa, pg, pu, M, F, K, alpha, act, qg, qu, ldgu, qh, ldh, _stream(stream)))
+    p = _ptrs(fn, *_view(fn, a, M, K), *_view(fn, b_gate, F, K), *_view(fn, b_up, F, K), gate, up, h)
+    va, vg, vu = qt2.NVFP4ViewC(*p[:3]), qt2.NVFP4ViewC(*p[3:6]), qt2.NVFP4ViewC(*p[6:9])
+    _check(fn, lib().qt2_gemm_nvfp4_gated(va, vg, vu, M, F, K, alpha, act, p[9], p[10], ldgu, p[11], ldh,
+                                          _stream(stream)))
 
 
 def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, alpha: float, act: int,
@@ -278,10 +279,10 @@ def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, a
     dh = alpha a b^T (views [M, K], [F, K]), which is not stored.  bf16 outputs."""
     fn = "qt2_gemm_nvfp4_gated_bwd"
     _only(fn, torch.bfloat16, gate, up, dgate, dup, h)
-    pa, pb = _view(fn, a, M, K), _view(fn, b, F, K)
-    qg, qu, qdg, qdu, qh = _ptrs(fn, gate, up, dgate, dup, h)
-    _check(fn, lib().qt2_gemm_nvfp4_gated_bwd(pa, pb, M, F, K, alpha, act, qg, qu, ldgu, qdg, qdu, lddgu, qh, ldh,
-                                              _stream(stream)))
+    p = _ptrs(fn, *_view(fn, a, M, K), *_view(fn, b, F, K), gate, up, dgate, dup, h)
+    va, vb = qt2.NVFP4ViewC(*p[:3]), qt2.NVFP4ViewC(*p[3:6])
+    _check(fn, lib().qt2_gemm_nvfp4_gated_bwd(va, vb, M, F, K, alpha, act, p[6], p[7], ldgu, p[8], p[9], lddgu, p[10],
+                                              ldh, _stream(stream)))
 
 
 def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx: int, hsx: int,
