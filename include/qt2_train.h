@@ -155,7 +155,7 @@ QT2_API qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_n
  * qt2_train_device_status.  R = 0: nothing is turned; positions and tables may be NULL.
  * x and y have type x_dtype, wq and wk w_dtype; all of it 16-byte aligned (positions 8), strides multiples of
  * 8 elements below 2^32, such that no two heads overlap.  D and R are multiples of 8, D <= 1024, R <= D.  Statistics and
- * products are fp32, rounded once on writing (squares too: elements from 2^63 on overflow them).  y may be x
+ * products are fp32, rounded once on writing (a head's sum of squares has to stay within fp32).  y may be x
  * with its strides.  eps >= 0 and finite.  T, Hq and Hk are below 2^30, 2^20 and 2^20.
  * --------------------------------------------------------------------------------------- */
 enum { QT2_ROPE_HALVES = 0, QT2_ROPE_PAIRS = 1 };
@@ -227,7 +227,8 @@ QT2_API qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const flo
  *     (lo32(i / 4), hi32(i / 4), the tensor's place in the list, lo32(*step)) under the key seed: its low 16 bits
  *     for m, the others for v.  Blocks whose largest magnitude is below 2^-100 become zeros with scale 0; an inf
  *     or NaN makes its block of 256 NaN.  Zeros with scales of zero are a fresh state.
- * Codes, scales and v are rounded operation by operation in the order above (fp32, no contraction).
+ * Codes, scales and v are rounded operation by operation in the order above (fp32, no contraction); squares of
+ * gradients have to stay within fp32.
  * lr (fp32), step (int64, 1 for the first step) and norm (fp32, what qt2_grad_norm gives) are one element each
  * in device memory, so that a captured graph can be replayed as they change.  A step below 1 is reported as
  * QT2_ERR_INVALID_ARG through qt2_train_device_status; then, and where the norm is inf or NaN, nothing changes.

@@ -40,7 +40,7 @@ struct GatedCfg {
     static constexpr int kEpiWarp0 = 4;
     static constexpr int kEpiWarps = 8;
     static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-    static constexpr int kRegsOthers = 40, kRegsEpi = 232;   // backward
+    static constexpr int kRegs = 168, kRegsOthers = 40, kRegsEpi = 232;   // a thread, at launch and (backward) then
     static constexpr int kA = 128 * 128;          // own 128 rows, K = 256
     static constexpr int kB = 128 * 128;          // own half of B's 256 rows
     static constexpr int kSfa = 4 * 512;          // 4 k-blocks x one 512-byte atom
@@ -266,8 +266,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg<BWD>::kThre
         pm = first + r - pn * rows;
     };
 
-    // The epilogue's warpgroups take registers over from the others' (the launch has 168 a thread).
-    static_assert(128 * Cfg::kRegsOthers + 32 * Cfg::kEpiWarps * Cfg::kRegsEpi <= 168 * Cfg::kThreads, "register split");
+    // Backward the epilogue's warpgroups take registers over from the others', so that the arithmetic of 64 columns
+    // overlaps beside the 128 sums (16384 x 4096 x 14336: 168 a thread 824 us, 216 816, 224 775, 232 750).  Forward
+    // 168 hold it all.
+    static_assert(128 * Cfg::kRegsOthers + 32 * Cfg::kEpiWarps * Cfg::kRegsEpi <= Cfg::kRegs * Cfg::kThreads, "register split");
 
     int issued = 0, mma_done = 0, copied = 0;   // stages whose loads, MMAs and scale copies were issued
     if (BWD && warp < Cfg::kEpiWarp0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOthers));

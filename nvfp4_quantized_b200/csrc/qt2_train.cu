@@ -437,16 +437,21 @@ bool encode_view(CUtensorMap *codes, CUtensorMap *scales, const qt2_nvfp4_view *
 template <bool BWD, int ACT>
 cudaError_t launch_gated(const GatedMaps &maps, const GatedArgs &a, cudaStream_t s) {
     QT2_LAUNCH_SITE();
+    using Cfg = GatedCfg<BWD>;
     static PerDeviceOnce once;
     const cudaError_t e = once.run([] {
+        // the backward kernel's warps wait for registers that the launch has to have
+        cudaFuncAttributes f;
+        if (const cudaError_t q = cudaFuncGetAttributes(&f, gated_pair_kernel<BWD, ACT>)) return q;
+        if (BWD && f.numRegs < Cfg::kRegs) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(gated_pair_kernel<BWD, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    GatedCfg<BWD>::kSmemBytes);
+                                    Cfg::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
     const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.F, BWD ? 256 : 128);
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
-    return launch(gated_pair_kernel<BWD, ACT>, (unsigned)(2 * clusters), GatedCfg<BWD>::kThreads,
-                  GatedCfg<BWD>::kSmemBytes, s, maps, a);
+    return launch(gated_pair_kernel<BWD, ACT>, (unsigned)(2 * clusters), Cfg::kThreads, Cfg::kSmemBytes, s,
+                  maps, a);
 }
 template <bool BWD>
 cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream_t s) {
