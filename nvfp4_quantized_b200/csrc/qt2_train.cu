@@ -1022,6 +1022,8 @@ qt2_status qt2_gemm_nvfp4_gated(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b
     g.M = (int)M;
     g.F = (int)F;
     g.K = (int)K;
+    // all of x's rows at a time where x is the smaller operand, so that the weights stream once (16384 x 4096 x 14336: 16
+    // rows 997 us, all 980; one row 1126); else F first (32768 x 2048 x 5632: one row 453 us, 16 rows 468)
     g.group_m = M < 2 * F ? (int)ceil_div(M, 256) : 1;
     g.gate = static_cast<__nv_bfloat16 *>(gate);
     g.up = static_cast<__nv_bfloat16 *>(up);
@@ -1061,6 +1063,8 @@ qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_nvfp4_vie
     g.M = (int)M;
     g.F = (int)F;
     g.K = (int)K;
+    // 8 rows of tiles: what the streams of gate, up and outputs push out of L2 is soon used again (16384 x 4096 x 14336:
+    // 1 row 816 us, 4 787, 8 771, 16 772, 32 791; 32768 x 2048 x 5632: 482 to 490 all)
     g.group_m = 8;
     g.gate = static_cast<__nv_bfloat16 *>(const_cast<void *>(gate));
     g.up = static_cast<__nv_bfloat16 *>(const_cast<void *>(up));
