@@ -112,7 +112,8 @@ QT2_API qt2_status qt2_linear_xent_bwd(const void *x, const void *w, const int64
  * Gated feed-forward product: both projections, the activation and the product in one kernel.
  *   g = alpha ga gg sum_k val(a)*sa * val(b_gate)*sg,  u the same of b_up,  h = act(g) * u.
  * a is an [M][K] view (the quantized x), b_gate and b_up are [F][K] views (the two weights, each with a
- * tensor scale of its own), as qt2_gemm_nvfp4 takes them; M, F and K are multiples of 128.  act(x) = x s(x):
+ * tensor scale of its own), as qt2_gemm_nvfp4 takes them; M, F and K are multiples of 128, the products' steps of
+ * 256 x 128 x 256 fewer than 2^31.  act(x) = x s(x):
  *   QT2_ACT_SILU       s = 1 / (1 + exp(-x)),
  *   QT2_ACT_GELU_TANH  s = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (x + 0.044715 x^3).
  * Sums, activation and product are fp32, each output rounded once.  h [M][F] is bf16; gate and up [M][F]
@@ -156,7 +157,7 @@ QT2_API qt2_status qt2_gemm_nvfp4_gated_bwd(const qt2_nvfp4_view *a, const qt2_n
  * x and y have type x_dtype, wq and wk w_dtype; all of it 16-byte aligned (positions 8), strides multiples of
  * 8 elements below 2^32, such that no two heads overlap.  D and R are multiples of 8, D <= 1024, R <= D.  Statistics and
  * products are fp32, rounded once on writing (a head's sum of squares has to stay within fp32).  y may be x
- * with its strides.  eps >= 0 and finite.  T, Hq and Hk are below 2^30, 2^20 and 2^20.
+ * with its strides.  eps >= 0 and finite.  T, Hq and Hk are below 2^30, 2^20 and 2^20, T (Hq + Hk) below 2^32.
  * --------------------------------------------------------------------------------------- */
 enum { QT2_ROPE_HALVES = 0, QT2_ROPE_PAIRS = 1 };
 QT2_API qt2_status qt2_qk_norm_rope_fwd(const void *x, int x_dtype, int64_t T, int64_t Hq, int64_t Hk, int64_t D,

@@ -116,10 +116,15 @@ def _check(fn: str, status: int):
 def _ptrs(fn: str, *tensors):
     """Device pointers of tensors (None stays None); all of them on the current device."""
     dev = torch.cuda.current_device()
+    found = []
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is None:
+            found.append(None)
+            continue
+        if t.get_device() != dev:
             raise QT2Error(fn, QT2_ERR_DEVICE)
-    return [None if t is None else t.data_ptr() for t in tensors]
+        found.append(t.data_ptr())
+    return found
 
 
 def _dtype(fn: str, *tensors) -> int:
@@ -151,9 +156,10 @@ def _vectors(fn: str, *tensors):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int | None = None) -> int:
+    """`device`: the current one, where the caller knows it (its tensors were found to be on it)."""
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     return qt2._stream(stream)
 
 
@@ -269,7 +275,7 @@ def qt2_gemm_nvfp4_gated(a: qt2.View, b_gate: qt2.View, b_up: qt2.View, M: int, 
     p = _ptrs(fn, *_view(fn, a, M, K), *_view(fn, b_gate, F, K), *_view(fn, b_up, F, K), gate, up, h)
     va, vg, vu = qt2.NVFP4ViewC(*p[:3]), qt2.NVFP4ViewC(*p[3:6]), qt2.NVFP4ViewC(*p[6:9])
     _check(fn, lib().qt2_gemm_nvfp4_gated(va, vg, vu, M, F, K, alpha, act, p[9], p[10], ldgu, p[11], ldh,
-                                          _stream(stream)))
+                                          _stream(stream, h.get_device())))
 
 
 def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, alpha: float, act: int,
@@ -282,7 +288,7 @@ def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, a
     p = _ptrs(fn, *_view(fn, a, M, K), *_view(fn, b, F, K), gate, up, dgate, dup, h)
     va, vb = qt2.NVFP4ViewC(*p[:3]), qt2.NVFP4ViewC(*p[3:6])
     _check(fn, lib().qt2_gemm_nvfp4_gated_bwd(va, vb, M, F, K, alpha, act, p[6], p[7], ldgu, p[8], p[9], lddgu, p[10],
-                                              ldh, _stream(stream)))
+                                              ldh, _stream(stream, gate.get_device())))
 
 
 def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx: int, hsx: int,
@@ -298,7 +304,7 @@ def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx:
     _vectors(fn, wq, wk, positions, cos, sin)
     px, pq, pk, pp, pc, ps, py = _ptrs(fn, x, wq, wk, positions, cos, sin, y)
     _check(fn, lib().qt2_qk_norm_rope_fwd(px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P, R, pairing, py,
-                                          ldy, hsy, _stream(stream)))
+                                          ldy, hsy, _stream(stream, x.get_device())))
 
 
 def qt2_qk_norm_rope_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int) -> int:
@@ -324,7 +330,7 @@ def qt2_qk_norm_rope_bwd(dy: torch.Tensor, lddy: int, hsdy: int, x: torch.Tensor
     pdy, px, pq, pk, pp, pc, ps, pdx, pdq, pdk, pws = _ptrs(fn, dy, x, wq, wk, positions, cos, sin, dx, dwq, dwk,
                                                             workspace)
     _check(fn, lib().qt2_qk_norm_rope_bwd(pdy, lddy, hsdy, px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P,
-                                          R, pairing, pdx, lddx, hsdx, pdq, pdk, pws, ws_bytes, _stream(stream)))
+                                          R, pairing, pdx, lddx, hsdx, pdq, pdk, pws, ws_bytes, _stream(stream, x.get_device())))
 
 
 class GradList:
@@ -469,7 +475,7 @@ def qt2_adamw(tensors: AdamWList, lr: torch.Tensor, step: torch.Tensor, beta1: f
     if tensors.count and tensors.device != lr.get_device():
         raise QT2Error(fn, QT2_ERR_DEVICE)
     _check(fn, lib().qt2_adamw(tensors.address, tensors.count, pl, ps, beta1, beta2, eps, pn, max_norm, seed,
-                               _stream(stream)))
+                               _stream(stream, lr.get_device())))
 
 
 class fault_hook(qt2.fault_hook):
