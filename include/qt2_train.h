@@ -224,7 +224,10 @@ QT2_API qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const flo
  *     scale is the largest magnitude / 448 (in the step's own update m and v are not rounded); a code is
  *     one of the two neighbours of its value, picked by 16 random bits r so that the mean stays: the fp32
  *     encoding of |value| * (448 / largest) plus r * 2^4, cut to 3 bits of mantissa (below 2^-6 with 2^-6 added
- *     before and taken off after).  Element i draws from word i % 4 of the Philox4x32-10 block of counter
+ *     before and taken off after).  A root that is not zero never becomes code 0: where it would, its code is the
+ *     smallest, 2^-9, so that no m that rounded up is divided by next to nothing (elements whose root is less than
+ *     2^-17.8 of their block's largest move by less than with fp32 states).
+ *     Element i draws from word i % 4 of the Philox4x32-10 block of counter
  *     (lo32(i / 4), hi32(i / 4), the tensor's place in the list, lo32(*step)) under the key seed: its low 16 bits
  *     for m, the others for v.  Blocks whose largest magnitude is below 2^-100 become zeros with scale 0; an inf
  *     or NaN makes its block of 256 NaN.  Zeros with scales of zero are a fresh state.

@@ -184,6 +184,9 @@ __device__ __forceinline__ uint32_t adam_down(uint32_t b, uint32_t s, uint32_t c
 // behind them carries with the right probability; the largest is off 448 by two units at most, which no draw
 // carries any further.  Below the normal numbers the spacing is that of the smallest normal, 2^-6, which is
 // added meanwhile: a warp without such elements (and zeros count as such) takes the shorter way.
+// A root (V) that is not zero keeps the smallest code where it would round to zero: m, drawn by itself, may have
+// rounded up to its smallest code there, and a step that divides that by eps or by the next gradient alone is
+// hundreds of learning rates (elements 10^5 below their block's largest: 300; 10^6: 3500; with the smallest code 2.5).
 template <bool V>
 __device__ __forceinline__ float adam_cut(float x, uint32_t word) {
     const uint32_t b = __float_as_uint(x);
@@ -199,6 +202,10 @@ __device__ __forceinline__ uint32_t adam_round(const float (&x)[4], bool small, 
         y[1] = __fsub_rn(adam_cut<V>(__fadd_rn(x[1], l[1]), w.y), l[1]);
         y[2] = __fsub_rn(adam_cut<V>(__fadd_rn(x[2], l[2]), w.z), l[2]);
         y[3] = __fsub_rn(adam_cut<V>(__fadd_rn(x[3], l[3]), w.w), l[3]);
+        if constexpr (V) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = x[e] > 0.0f ? fmaxf(y[e], 0x1p-9f) : y[e];
+        }
     } else {
         y[0] = adam_cut<V>(x[0], w.x);
         y[1] = adam_cut<V>(x[1], w.y);
