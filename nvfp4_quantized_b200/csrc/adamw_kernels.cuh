@@ -55,6 +55,9 @@ struct AdamArgs {
     const int64_t *step;
     double log_b1, log_b2;
     float b1, b2, one_b1, one_b2, eps, max_norm;
+    // what both sides of the update's quotient are multiplied by, eps among them: 1, or a power of two that makes a
+    // subnormal eps a normal number (adam_rcp takes any other for zero)
+    float unit;
     float minus_zero;
     uint32_t key0[10], key1[10];   // Philox's keys of each round
 };
@@ -375,8 +378,8 @@ __global__ void __launch_bounds__(kAdamThreads, E4M3 ? 5 : 2) adamw_kernel(const
         corr[threadIdx.x] = (float)(threadIdx.x ? sqrt(1.0 / left) : 1.0 / left);
     }
     __syncthreads();
-    j.rate = j.lr * corr[0];
-    j.c2 = corr[1];
+    j.rate = j.lr * corr[0] * a.unit;
+    j.c2 = corr[1] * a.unit;
     j.step = (uint32_t)step;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // the same in all lanes
     int k = 0, end = 0;   // the current tensor, and the chunk behind its last

@@ -1199,7 +1199,8 @@ qt2_status qt2_adamw(const qt2_adamw_tensor *tensors, int64_t count, const float
     a.b2 = (float)beta2;
     a.one_b1 = (float)(1.0 - beta1);
     a.one_b2 = (float)(1.0 - beta2);
-    a.eps = eps;
+    a.unit = eps > 0.0f && eps < 0x1p-126f ? 0x1p24f : 1.0f;
+    a.eps = eps * a.unit;
     a.max_norm = max_norm;
     a.minus_zero = -0.0f;
     for (uint32_t r = 0; r < 10; ++r) {
