@@ -85,7 +85,8 @@ struct GatedArgs {
 };
 
 // act(x) = x s of two elements, and (SLOPE) its derivative.  exp overflows to inf, and s is 0, where x is far below
-// zero; the exponent of GELU is taken at most 10 from zero, further out s is 0 or 1.
+// zero.  GELU's exponent is that of x or, further than 11 from zero, of 11: 2^162 and 2^-162 there, s is 0 or 1 as it
+// is from 10.01 on.
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ uint64_t gated_act(uint64_t x, uint64_t &slope) {
     constexpr float kLog2e = 1.4426950408889634f, c = 1.5957691216057308f, d = 0.044715f;   // c: 2 sqrt(2/pi)
@@ -95,7 +96,7 @@ __device__ __forceinline__ uint64_t gated_act(uint64_t x, uint64_t &slope) {
         t = f2_mul(x, f2(-kLog2e, -kLog2e));
     } else {
         const float2 y = f2_get(x);
-        b = f2(fminf(fmaxf(y.x, -10.0f), 10.0f), fminf(fmaxf(y.y, -10.0f), 10.0f));
+        b = f2(fminf(fmaxf(y.x, -11.0f), 11.0f), fminf(fmaxf(y.y, -11.0f), 11.0f));
         const uint64_t q = f2_mul(b, b);
         t = f2_mul(f2_mul(b, f2(-c * kLog2e, -c * kLog2e)), f2_fma(q, f2(d, d), one));
         rise = f2_fma(q, f2(3 * c * d, 3 * c * d), f2(c, c));
