@@ -86,17 +86,17 @@ struct GatedArgs {
 
 // act(x) = x s of two elements, and (SLOPE) its derivative.  exp overflows to inf, and s is 0, where x is far below
 // zero.  GELU's exponent is that of x or, further than 11 from zero, of 11: 2^162 and 2^-162 there, s is 0 or 1 as it
-// is from 10.01 on.
+// is from 10.01 on.  What multiplies s is x itself, so that a NaN stays one and -inf becomes one (-inf * 0).
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ uint64_t gated_act(uint64_t x, uint64_t &slope) {
     constexpr float kLog2e = 1.4426950408889634f, c = 1.5957691216057308f, d = 0.044715f;   // c: 2 sqrt(2/pi)
     const uint64_t one = f2(1.0f, 1.0f);
-    uint64_t b = x, t, rise = one;   // the exponent of s (in base 2, sign turned), and its derivative
+    uint64_t t, rise = one;   // the exponent of s (in base 2, sign turned), and its derivative
     if constexpr (ACT == QT2_ACT_SILU) {
         t = f2_mul(x, f2(-kLog2e, -kLog2e));
     } else {
         const float2 y = f2_get(x);
-        b = f2(fminf(fmaxf(y.x, -11.0f), 11.0f), fminf(fmaxf(y.y, -11.0f), 11.0f));
+        const uint64_t b = f2(fminf(fmaxf(y.x, -11.0f), 11.0f), fminf(fmaxf(y.y, -11.0f), 11.0f));
         const uint64_t q = f2_mul(b, b);
         t = f2_mul(f2_mul(b, f2(-c * kLog2e, -c * kLog2e)), f2_fma(q, f2(d, d), one));
         rise = f2_fma(q, f2(3 * c * d, 3 * c * d), f2(c, c));
@@ -109,11 +109,12 @@ __device__ __forceinline__ uint64_t gated_act(uint64_t x, uint64_t &slope) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sx) : "f"(n.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sy) : "f"(n.y));
     const uint64_t s = f2(sx, sy);
-    if constexpr (SLOPE) {   // s + b s (1 - s) rise
-        const uint64_t bs = f2_mul(f2_mul(b, s), f2_fma(s, f2(-1.0f, -1.0f), one));
-        slope = ACT == QT2_ACT_SILU ? f2_add(bs, s) : f2_fma(bs, rise, s);
+    const uint64_t xs = f2_mul(x, s);
+    if constexpr (SLOPE) {   // s + x s (1 - s) rise
+        const uint64_t t2 = f2_mul(xs, f2_fma(s, f2(-1.0f, -1.0f), one));
+        slope = ACT == QT2_ACT_SILU ? f2_add(t2, s) : f2_fma(t2, rise, s);
     }
-    return f2_mul(x, s);
+    return xs;
 }
 __device__ __forceinline__ uint32_t gated_bits(uint64_t v) {
     const float2 p = f2_get(v);
