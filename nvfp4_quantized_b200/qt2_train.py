@@ -262,6 +262,10 @@ def _view(fn: str, v: qt2.View, R: int, C: int):
     # a view of other sizes holds fewer elements than the call reads, or others (sizes that no call takes are its to refuse)
     if R > 0 and C > 0 and (codes.numel() != R * C // 2 or scales.numel() != R * C // 16):
         raise QT2Error(fn, QT2_ERR_SHAPE)
+    # of the scales of a view with one for 128 rows, which differs from this one in nothing else, all but the first
+    # would be left out
+    if scale.numel() != 1:
+        raise QT2Error(fn, QT2_ERR_SHAPE)
     return codes, scales, scale
 
 
