@@ -10,6 +10,8 @@ the call a tensor that is not on the current CUDA device raises ``QT2Error`` wit
 of a type that the call does not take with QT2_ERR_INVALID_ARG, as does a vector (weights, statistics,
 targets, losses and their gradients, workspaces) that is not contiguous: an expanded or strided one
 holds other elements, or fewer, than the call reads.  Matrices are given by their leading dimension.
+Views, and the weights, positions and tables of the norm of queries and keys, that do not have the sizes of the
+call raise it with QT2_ERR_SHAPE.
 There is no fallback.
 """
 from __future__ import annotations
@@ -131,11 +133,12 @@ def _dtype(fn: str, *tensors) -> int:
     """The common element type of tensors (None is skipped); QT2_DTYPE_BF16 if there is none."""
     found = None
     for t in tensors:
-        if t is None or t.dtype is found:
-            continue
-        if found is not None or t.dtype not in _DTYPE:
-            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
-        found = t.dtype
+        if t is not None:
+            d = t.dtype
+            if d is not found:
+                if found is not None or d not in _DTYPE:
+                    raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+                found = d
     return QT2_DTYPE_BF16 if found is None else _DTYPE[found]
 
 
@@ -295,6 +298,33 @@ def qt2_gemm_nvfp4_gated_bwd(a: qt2.View, b: qt2.View, M: int, F: int, K: int, a
                                               ldh, _stream(stream, gate.get_device())))
 
 
+def _qk_vectors(fn: str, T: int, D: int, P: int, R: int, positions, cos, sin, *weights):
+    """Contiguous weights of D elements, an int64 position for each token, fp32 tables of [P, R/2] or of more such
+    rows (sizes that no call takes are its to refuse).  One function: the checks of a small call are part of its time."""
+    status = 0
+    for w in weights:
+        if w is not None:
+            if not w.is_contiguous():
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            if w.numel() != D > 0:
+                status = QT2_ERR_SHAPE
+    if positions is not None:
+        if positions.dtype is not torch.int64 or not positions.is_contiguous():
+            raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+        if positions.numel() < T:
+            status = QT2_ERR_SHAPE
+    n = P * (R // 2)
+    for t in (cos, sin):
+        if t is not None:
+            if t.dtype is not torch.float32 or not t.is_contiguous():
+                raise QT2Error(fn, QT2_ERR_INVALID_ARG)
+            # more elements are more rows, or rows that hold an angle twice
+            if t.numel() != n > 0 and (t.numel() < n or t.dim() < 2 or t.shape[-1] != R // 2):
+                status = QT2_ERR_SHAPE
+    if status:
+        raise QT2Error(fn, status)
+
+
 def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx: int, hsx: int,
                          wq: torch.Tensor | None, wk: torch.Tensor | None, eps: float, positions: torch.Tensor | None,
                          cos: torch.Tensor | None, sin: torch.Tensor | None, P: int, R: int, pairing: int,
@@ -303,9 +333,7 @@ def qt2_qk_norm_rope_fwd(x: torch.Tensor, T: int, Hq: int, Hk: int, D: int, ldx:
     turned by row positions[t] of the tables cos and sin [P, R/2].  x and y of one type, wq and wk of one type."""
     fn = "qt2_qk_norm_rope_fwd"
     xd, wd = _dtype(fn, x, y), _dtype(fn, wq, wk)
-    _only(fn, torch.int64, positions)
-    _only(fn, torch.float32, cos, sin)
-    _vectors(fn, wq, wk, positions, cos, sin)
+    _qk_vectors(fn, T, D, P, R, positions, cos, sin, wq, wk)
     px, pq, pk, pp, pc, ps, py = _ptrs(fn, x, wq, wk, positions, cos, sin, y)
     _check(fn, lib().qt2_qk_norm_rope_fwd(px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P, R, pairing, py,
                                           ldy, hsy, _stream(stream, x.get_device())))
@@ -328,9 +356,8 @@ def qt2_qk_norm_rope_bwd(dy: torch.Tensor, lddy: int, hsdy: int, x: torch.Tensor
     dwq and dwk of one type."""
     fn = "qt2_qk_norm_rope_bwd"
     xd, wd = _dtype(fn, dy, x, dx), _dtype(fn, wq, wk, dwq, dwk)
-    _only(fn, torch.int64, positions)
-    _only(fn, torch.float32, cos, sin)
-    _vectors(fn, wq, wk, positions, cos, sin, dwq, dwk, workspace)
+    _vectors(fn, workspace)
+    _qk_vectors(fn, T, D, P, R, positions, cos, sin, wq, wk, dwq, dwk)
     pdy, px, pq, pk, pp, pc, ps, pdx, pdq, pdk, pws = _ptrs(fn, dy, x, wq, wk, positions, cos, sin, dx, dwq, dwk,
                                                             workspace)
     _check(fn, lib().qt2_qk_norm_rope_bwd(pdy, lddy, hsdy, px, xd, T, Hq, Hk, D, ldx, hsx, pq, pk, wd, eps, pp, pc, ps, P,
