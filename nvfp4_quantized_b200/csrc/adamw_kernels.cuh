@@ -12,7 +12,7 @@
 // operation (no contraction), so that it is the same wherever it is computed.
 //
 // A stream over HBM: everything is read and written once, and the clipping takes no pass of its own (411M elements:
-// fp32 1.83 ms, 6.3 TB/s).  States in 8 bits make it a stream of instructions: 71 an element, of them 15 for the draws,
+// fp32 1.81 to 1.87 ms, 6.2 to 6.4 TB/s).  States in 8 bits make it a stream of instructions: 71 an element, of them 15 for the draws,
 // issue 70% (with bf16 parameters and gradients and fp32 masters 1.21 to 1.32 ms, 5.0 to 5.5 TB/s).  A warp takes 256 elements, its lanes 4 neighbours twice, and loads all arrays before it uses any.  The
 // list travels in the kernel's parameters; tensors of different types take launches of their own, each
 // compiled for its types.
@@ -354,7 +354,8 @@ __device__ __forceinline__ void adam_step(const AdamTable<N> &t, int k, int64_t 
     }
 }
 
-// Blocks an SM, 411M elements: 8 bits 4 1446 us, 5 1206, 6 1275 (spills); fp32 2 1824, 3 1855, 4 1847.
+// Blocks an SM, 411M elements: 8 bits 4 1446 us, 5 1206 (4 bytes of spills with masters), 6 1275 (more); fp32 2 1824, 3
+// 1855, 4 1847.
 template <int N, bool E4M3, AdamParam P, bool GF32>
 __global__ void __launch_bounds__(kAdamThreads, E4M3 ? 5 : 2) adamw_kernel(const __grid_constant__ AdamTable<N> t,
                                                                 const __grid_constant__ AdamArgs a) {

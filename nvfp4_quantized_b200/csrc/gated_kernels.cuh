@@ -25,10 +25,13 @@
 // Every wait is bounded; after a timeout the leader drains what was issued, both CTAs meet, and TMEM is
 // freed.
 //
-// Bound by the operands' way from L2 (a pair streams 1.2 MB for a tile of K = 4096) and, backward, by what shares it:
-// gate, up and three outputs.  16384 x 4096 x 14336: forward, gate and up kept, 1.00 ms (3.8 PFLOP/s; cold and alone
-// 4.5), backward 0.75 ms (without its stores 0.59, without its loads 0.65, without the MMAs 0.67).  Memory alone would
-// take 0.23 and 0.37 ms, the MMAs at 9 PFLOP/s 0.43 and 0.21.
+// 16384 x 4096 x 14336: forward, gate and up kept, 0.99 to 1.03 ms (3.8 PFLOP/s; cold and alone 4.5), not kept 0.85 ms,
+// backward 0.74 to 0.77 ms (without its stores 0.59, without its loads 0.65, without the MMAs 0.67).  Memory alone
+// would take 0.23 and 0.37 ms, the MMAs at four times the measured bf16 rate (6.6 PFLOP/s) 0.58 and 0.29.  Nothing is
+// full: a pair streams 1.2 MB from L2 for a tile of K = 4096, 8.9 GB forward (8.7 TB/s, where the linears' GEMM gets
+// 13.8) and 4.5 GB backward beside gate, up and three outputs; the tensor pipe is 61% and 39% active.  There is one
+// accumulator, so the MMAs wait while a tile's sums are read, and backward a warp's load, arithmetic and stores of a
+// piece come one after the other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -275,8 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GatedCfg<BWD>::kThre
     };
 
     // Backward the epilogue's warpgroups take registers over from the others', so that the arithmetic of 64 columns
-    // overlaps beside the 128 sums (16384 x 4096 x 14336: 168 a thread 824 us, 216 816, 224 775, 232 750).  Forward
-    // 168 hold it all.
+    // overlaps beside the 128 sums (16384 x 4096 x 14336: 168 a thread 824 us, 216 816, 224 775, 232 750; 52 bytes are
+    // still spilled with GELU, 60 with SiLU).  Forward 168 hold it all.
     static_assert(128 * Cfg::kRegsOthers + 32 * Cfg::kEpiWarps * Cfg::kRegsEpi <= Cfg::kRegs * Cfg::kThreads, "register split");
 
     int issued = 0, mma_done = 0, copied = 0;   // stages whose loads, MMAs and scale copies were issued

@@ -460,9 +460,8 @@ cudaError_t gated(const GatedMaps &maps, const GatedArgs &a, int act, cudaStream
 }
 
 // ------------------------------------------------------------------------------- queries and keys
-// Heads that a group of lanes takes at a time.  Forward, 32768 x 16+16 x 128 bf16: 1 head 190 us, 2 heads 143, 4
-// heads 103, 8 heads 100 (but twice the work where a kind has 4); backward 1 head 279, 2 heads 196, 4 heads 158,
-// 8 heads, which spill, 231.
+// Heads that a group of lanes takes at a time.  Forward, 32768 x 16+16 x 128 bf16: 1 head 168 us, 2 heads 125, 4
+// heads 108, 8 heads, which spill, 140; backward 1 head 282, 2 heads 196, 4 heads 163, 8 heads 171.
 template <class T, int N>
 constexpr int kQkRows = std::max(1, (sizeof(T) == 2 ? 4 : 2) / N);
 
@@ -1023,7 +1022,9 @@ qt2_status qt2_gemm_nvfp4_gated(const qt2_nvfp4_view *a, const qt2_nvfp4_view *b
     g.F = (int)F;
     g.K = (int)K;
     // all of x's rows at a time where x is the smaller operand, so that the weights stream once (16384 x 4096 x 14336: 16
-    // rows 997 us, all 980; one row 1126); else F first (32768 x 2048 x 5632: one row 453 us, 16 rows 468)
+    // rows 997 us, all 980; one row 1126); else F first (32768 x 2048 x 5632: one row 453 us, 16 rows 468).  The rule does
+    // not look at K: at 16384 x 8192 x 28672 x's 75 MB do not stay in L2 beside the outputs, and 16 rows take 3406 us
+    // where all take 3950 (one row 4574)
     g.group_m = M < 2 * F ? (int)ceil_div(M, 256) : 1;
     g.gate = static_cast<__nv_bfloat16 *>(gate);
     g.up = static_cast<__nv_bfloat16 *>(up);

@@ -12,9 +12,10 @@
 // loads are all issued before the first is used.  Backward recomputes r from x, which it reads anyway.
 //
 // A stream over HBM that instructions hold back: 17 an element forward (issue 68%, 5.1 TB/s: 32768 x 16+16 x 128 bf16
-// 107 us, 83 for its bytes), 21 backward (54% with 16 warps an SM, 5.0 TB/s: 163 us, 124 for its bytes).  Four heads a
-// group share the angles' loads and the index arithmetic (one row a group's iteration: 134 and 185 us); conditional
-// loads, or the next unit's ahead of this one's work, were slower (147; 202 to 270 us).
+// 105 to 108 us, 83 for its bytes), 21 backward (54% with 16 warps an SM, 5.0 TB/s: 159 to 164 us, 124 for its bytes).
+// Four heads a group share the angles' loads and the index arithmetic (one head: 168 and 282 us); conditional
+// loads, or the next unit's ahead of this one's work, were slower (147; 202 to 270 us).  fp32, half the tokens: 92 and
+// 138 us (5.9 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -201,6 +202,8 @@ __device__ __forceinline__ QkUnit<U> qk_unit(const QkArgs &a, int kind, uint32_t
     return q;
 }
 
+// Blocks an SM, 32768 x 16+16 x 128 bf16 and 16384 tokens of fp32: 3 and 4 (64 registers) 107 and 97 us, 5 (48, of
+// which 12 to 24 bytes are spilled) 105 and 91, 6 (40, 44 to 112 bytes) 120 and 102.
 template <class T, int G, int N, int U, bool PAIRS>
 __global__ void __launch_bounds__(kQkThreads, N > 1 ? 2 : 5) qk_norm_rope_fwd_kernel(const __grid_constant__ QkArgs a) {
     grid_dependency();
