@@ -230,7 +230,8 @@ QT2_API qt2_status qt2_grad_clip(const qt2_grad *grads, int64_t count, const flo
  *     Element i draws from word i % 4 of the Philox4x32-10 block of counter
  *     (lo32(i / 4), hi32(i / 4), the tensor's place in the list, lo32(*step)) under the key seed: its low 16 bits
  *     for m, the others for v.  Blocks whose largest magnitude is below 2^-100 become zeros with scale 0; an inf
- *     or NaN makes its block of 256 NaN.  Zeros with scales of zero are a fresh state.
+ *     or NaN makes its block of 256 NaN.  Zeros with scales of zero are a fresh state; states that a caller makes
+ *     of others hold no root of code 0 beside an m that is not zero, which the next step would divide by eps.
  * Codes, scales and v are rounded operation by operation in the order above (fp32, no contraction); squares of
  * gradients have to stay within fp32.
  * lr (fp32), step (int64, 1 for the first step) and norm (fp32, what qt2_grad_norm gives) are one element each

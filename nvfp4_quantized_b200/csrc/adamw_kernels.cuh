@@ -12,8 +12,9 @@
 // operation (no contraction), so that it is the same wherever it is computed.
 //
 // A stream over HBM: everything is read and written once, and the clipping takes no pass of its own (411M elements:
-// fp32 1.81 to 1.87 ms, 6.2 to 6.4 TB/s).  States in 8 bits make it a stream of instructions: 71 an element, of them 15 for the draws,
-// issue 70% (with bf16 parameters and gradients and fp32 masters 1.21 to 1.32 ms, 5.0 to 5.5 TB/s).  A warp takes 256 elements, its lanes 4 neighbours twice, and loads all arrays before it uses any.  The
+// fp32 1.81 to 1.87 ms, 6.2 to 6.4 TB/s).  States in 8 bits make it a stream of instructions: 71 an element, of
+// them 15 for the draws, issue 70% (with bf16 parameters and gradients and fp32 masters 1.21 to 1.32 ms, 5.0 to 5.5
+// TB/s).  A warp takes 256 elements, its lanes 4 neighbours twice, and loads all arrays before it uses any.  The
 // list travels in the kernel's parameters; tensors of different types take launches of their own, each
 // compiled for its types.
 #pragma once
