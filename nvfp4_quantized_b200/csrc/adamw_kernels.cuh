@@ -7,7 +7,7 @@
 // States in 8 bits are E4M3 codes with an fp32 scale for 256 elements, m / scale and sqrt(v) / scale: the
 // root spans the range of v in half as many binades and is what the update divides by.  A step moves v by
 // (1 - b2), far less than the codes' spacing, so codes are rounded up or down at random, with probabilities
-// that keep their mean; rounded to nearest, v would stay where it is.  The draws are Philox words of
+// that keep their mean (a root's never to zero); rounded to nearest, v would stay where it is.  The draws are Philox words of
 // (seed, tensor, step, element): 16 bits for m, 16 for v.  What decides a code is rounded operation by
 // operation (no contraction), so that it is the same wherever it is computed.
 //
@@ -190,7 +190,8 @@ __device__ __forceinline__ uint32_t adam_down(uint32_t b, uint32_t s, uint32_t c
 // added meanwhile: a warp without such elements (and zeros count as such) takes the shorter way.
 // A root (V) that is not zero keeps the smallest code where it would round to zero: m, drawn by itself, may have
 // rounded up to its smallest code there, and a step that divides that by eps or by the next gradient alone is
-// hundreds of learning rates (elements 10^5 below their block's largest: 300; 10^6: 3500; with the smallest code 2.5).
+// hundreds of learning rates (elements 10^5 below their block's largest: 300 within 300 steps; 10^6: 3500; with the
+// smallest code 2.4).
 template <bool V>
 __device__ __forceinline__ float adam_cut(float x, uint32_t word) {
     const uint32_t b = __float_as_uint(x);
